@@ -1,4 +1,5 @@
-"""Predictor-gated bank-wise sparse SwiGLU FFN forward on AMD MI355X.
+"""Predictor-gated bank-wise sparse SwiGLU FFN forward on AMD MI355X, and the
+attention-side operators of the layer around it (see attention.py).
 
 A thin ctypes binding over libsparse_ffn.so (include/sparse_ffn.h). Every
 step of the forward runs in the library's HIP kernels; this module only
@@ -25,7 +26,9 @@ import torch
 
 __all__ = ["SparseFFN", "bank_topk", "library_path", "load_library", "SparseFFNError",
            "SFFN_OK", "SFFN_ERR_INVALID_ARG", "SFFN_ERR_UNSUPPORTED", "SFFN_ERR_WORKSPACE",
-           "SFFN_ERR_HIP", "Config", "EXPORTED_SYMBOLS"]
+           "SFFN_ERR_HIP", "Config", "EXPORTED_SYMBOLS",
+           "rope_table", "qk_norm_rope", "qk_norm_rope_backward", "KVCache", "CacheBatch", "kv_cache_append",
+           "kv_cache_read", "cache_attention"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 
@@ -100,6 +103,7 @@ def load_library():
     lib.sparse_ffn_backward.restype = st
     lib.sparse_ffn_forward_noalloc.argtypes = [P, P, I64, P, P, P, P]
     lib.sparse_ffn_forward_noalloc.restype = st
+    attention.declare(lib)
     _LIB = lib
     return lib
 
@@ -337,3 +341,10 @@ class SparseFFN:
             self.close()
         except Exception:
             pass
+
+
+from . import attention  # noqa: E402 (it uses the helpers above)
+from .attention import (CacheBatch, KVCache, cache_attention, kv_cache_append, kv_cache_read,  # noqa: E402
+                        qk_norm_rope, qk_norm_rope_backward, rope_table)
+
+EXPORTED_SYMBOLS = EXPORTED_SYMBOLS + attention.EXPORTED_SYMBOLS

@@ -1,0 +1,365 @@
+"""The attention-side operators of a decoder layer that stand next to the sparse
+FFN: norms of q and k for each head with the rotary positions, a paged cache
+that holds keys and values in 8 bits, and attention over it.
+
+    table = rope_table(32768, 128)
+    q, k = qk_norm_rope(q, k, positions, table, q_weight=w_q, k_weight=w_k)
+    cache = KVCache.empty(n_pages, kv_heads, head_dim)
+    batch = CacheBatch(block_table, kv_lens, max_kv, cu, max_new)
+    kv_cache_append(cache, batch, k, v)
+    o = cache_attention(cache, batch, q)
+
+A thin ctypes binding of include/sparse_ffn_attention.h: the arithmetic runs in
+the library's HIP kernels, asynchronously on torch's current stream.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional
+
+import torch
+
+from . import SFFN_BF16, SFFN_F32, _check, _need_buffer, _ptr, _stream, load_library
+
+__all__ = ["rope_table", "qk_norm_rope", "qk_norm_rope_backward", "KVCache", "CacheBatch", "kv_cache_append",
+           "kv_cache_read", "cache_attention"]
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = (None, "linear", "ntk", "by_parts")
+_DTYPES = {torch.bfloat16: SFFN_BF16, torch.float32: SFFN_F32}
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_token", ctypes.c_int64), ("stride_head", ctypes.c_int64)]
+
+
+class _RopeConfig(ctypes.Structure):
+    _fields_ = [("n_q_heads", ctypes.c_int32), ("n_k_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("max_pos", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("layout", ctypes.c_int), ("norm", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("keys", ctypes.c_void_p), ("values", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _Batch(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("kv_lens", ctypes.c_void_p),
+                ("cu", ctypes.c_void_p), ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("max_new", ctypes.c_int32), ("max_kv", ctypes.c_int32)]
+
+
+EXPORTED_SYMBOLS = ("qk_norm_rope", "qk_norm_rope_backward", "qk_norm_rope_backward_workspace_size",
+                    "kv_cache_append", "kv_cache_read", "cache_attention", "cache_attention_workspace_size")
+
+
+def declare(lib):
+    """The signatures of include/sparse_ffn_attention.h."""
+    P, S, I64, I32, F, st = (ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64, ctypes.c_int32, ctypes.c_float,
+                             ctypes.c_int)
+    H, R, C, B = (ctypes.POINTER(x) for x in (_Heads, _RopeConfig, _Cache, _Batch))
+    lib.qk_norm_rope.argtypes = [R, H, H, P, P, P, P, I64, H, H, P]
+    lib.qk_norm_rope.restype = st
+    lib.qk_norm_rope_backward_workspace_size.argtypes = [R, I64]
+    lib.qk_norm_rope_backward_workspace_size.restype = S
+    lib.qk_norm_rope_backward.argtypes = [R, H, H, H, H, P, P, P, P, I64, H, H, P, P, P, S, P]
+    lib.qk_norm_rope_backward.restype = st
+    for f in (lib.kv_cache_append, lib.kv_cache_read):
+        f.argtypes = [C, B, H, H, st, I64, P]
+        f.restype = st
+    lib.cache_attention_workspace_size.argtypes = [C, B, I32, st, I32, I64]
+    lib.cache_attention_workspace_size.restype = S
+    lib.cache_attention.argtypes = [C, B, H, I32, st, I64, F, I32, H, P, P, S, P]
+    lib.cache_attention.restype = st
+
+
+# ---------------------------------------------------------------------------
+# argument checks
+# ---------------------------------------------------------------------------
+
+def _heads(t: Optional[torch.Tensor], name: str, shape=None, dtype=None, device=None):
+    """A [T, heads, head_dim] view on the GPU as the library takes it."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have shape {tuple(shape) if shape else '[T, heads, head_dim]'} "
+                         f"(got {tuple(t.shape)})")
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype or 'bfloat16 or float32'} (got {t.dtype})")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be on {device or 'the GPU'} (got {t.device})")
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if sd != 1 and D > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    # a dimension of one element may carry any stride
+    sh = sh if H > 1 else D
+    return _Heads(t.data_ptr(), st if T > 1 else sh * H, sh)
+
+
+def _vector(t: Optional[torch.Tensor], name: str, shape, dtype, device):
+    if t is not None:
+        _need_buffer(t, name, shape, dtype, device)
+    return _ptr(t)
+
+
+# ---------------------------------------------------------------------------
+# head norms and rotary positions
+# ---------------------------------------------------------------------------
+
+def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None,
+               factor: float = 1.0, original_max_pos: Optional[int] = None, device="cuda") -> torch.Tensor:
+    """cos | sin of every position and pair, fp32 [max_pos, rot_dim]: made once
+    for a model, in 64 bits. Pair i turns by pos * base^(-2i / rot_dim); for
+    contexts `factor` times the trained one (original_max_pos tokens)
+
+      "linear"    positions are divided by factor;
+      "ntk"       base grows by factor^(rot_dim / (rot_dim - 2)), so that the
+                  slowest pair turns 1 / factor as fast and the fastest as before;
+      "by_parts"  pairs that turn less than once in the trained context are
+                  divided by factor, those that turn 32 times or more are kept,
+                  a ramp between; cos and sin are scaled by 1 + 0.1 ln factor.
+    """
+    if max_pos < 1 or rot_dim < 2 or rot_dim % 2:
+        raise ValueError("max_pos must be positive and rot_dim a positive even number")
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {ROPE_SCALINGS}")
+    if not (base > 0 and factor > 0):
+        raise ValueError("base and factor must be positive")
+    exponent = torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim
+    if scaling == "ntk" and rot_dim > 2:
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    freq = base ** -exponent
+    amplitude = 1.0
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "by_parts":
+        if not original_max_pos or original_max_pos < 1:
+            raise ValueError("by_parts needs original_max_pos, the trained context")
+        turns = original_max_pos * freq / (2 * math.pi)
+        keep = ((turns - 1) / 31).clamp(0, 1)
+        freq = freq * keep + freq / factor * (1 - keep)
+        amplitude = 1 + 0.1 * math.log(factor) if factor > 1 else 1.0
+    angle = torch.arange(max_pos, dtype=torch.float64)[:, None] * freq
+    return (torch.cat([angle.cos(), angle.sin()], 1) * amplitude).float().to(device)
+
+
+def _rope_call(x, other, positions, table, q_weight, k_weight, norm, eps, layout):
+    """The config and shared pointers of a call on q (or its gradient) `x` and
+    k `other` (or None)."""
+    T, n_q, D = x.shape
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError("layout must be 'half' or 'interleaved'")
+    if norm is None:
+        norm = q_weight is not None or k_weight is not None
+    if not norm and (q_weight is not None or k_weight is not None):
+        raise ValueError("weights are given but norm is False")
+    dev = x.device
+    rot = 0
+    if table is not None:
+        if table.dim() != 2:
+            raise ValueError("table must be [max_pos, rot_dim] float32")
+        rot = table.shape[1]
+        _need_buffer(table, "table", None, torch.float32, dev)
+        _need_buffer(positions, "positions", (T,), torch.int32, dev)
+    cfg = _RopeConfig(n_q, 0 if other is None else other.shape[1], D, rot, table.shape[0] if rot else 0,
+                      _DTYPES[x.dtype], ROPE_LAYOUTS[layout], int(norm), eps)
+    return (cfg, _ptr(positions) if rot else None, _ptr(table) if rot else None,
+            _vector(q_weight, "q_weight", (D,), x.dtype, dev), _vector(k_weight, "k_weight", (D,), x.dtype, dev))
+
+
+def _like_k(k, q):
+    """The shape k must have: q's with its own count of heads."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be [T, heads, head_dim]")
+    return torch.Size((q.shape[0], k.shape[1], q.shape[2]))
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                 table: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, norm: Optional[bool] = None, eps: float = 1e-6,
+                 layout: str = "half", q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
+    """RMS norm of every head of q [T, H, D] and k [T, K, D] (views with any
+    token and head strides), then the rotation of its first table.shape[1]
+    elements by positions [T] int32.
+
+    norm: None takes it from whether weights are given; True without weights
+    norms alone, False rotates alone. table None: no rotation. layout: "half"
+    pairs (i, i + rot / 2), "interleaved" pairs (2i, 2i + 1). k may be None.
+    q_out, k_out may be q and k themselves. Returns (q_out, k_out). A position
+    outside the table gives NaN rows."""
+    lib = load_library()
+    hq = _heads(q, "q")
+    hk = None if k is None else _heads(k, "k", _like_k(k, q), q.dtype, q.device)
+    cfg, pos, tab, wq, wk = _rope_call(q, k, positions, table, q_weight, k_weight, norm, eps, layout)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None and k is not None:
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    ho = _heads(q_out, "q_out", q.shape, q.dtype, q.device)
+    hko = None if k is None else _heads(k_out, "k_out", k.shape, q.dtype, q.device)
+    _check(lib, lib.qk_norm_rope(cfg, hq, hk, pos, tab, wq, wk, q.shape[0], ho, hko, _stream(q.device)))
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(q: Optional[torch.Tensor], k: Optional[torch.Tensor], g_q: torch.Tensor,
+                          g_k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                          table: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
+                          k_weight: Optional[torch.Tensor] = None, norm: Optional[bool] = None, eps: float = 1e-6,
+                          layout: str = "half") -> dict:
+    """Gradients of qk_norm_rope for the gradients g_q, g_k of its outputs; q and
+    k are that call's inputs (not needed without norm). Returns "q", "k" (the
+    inputs' dtype) and "q_weight", "k_weight" (fp32, None where no weight was
+    given)."""
+    lib = load_library()
+    hg = _heads(g_q, "g_q")
+    hgk = None if g_k is None else _heads(g_k, "g_k", _like_k(g_k, g_q), g_q.dtype, g_q.device)
+    cfg, pos, tab, wq, wk = _rope_call(g_q, g_k, positions, table, q_weight, k_weight, norm, eps, layout)
+    T, dev, hq, hk = g_q.shape[0], g_q.device, None, None
+    if cfg.norm:
+        hq = _heads(q, "q", g_q.shape, g_q.dtype, dev)
+        if g_k is not None:
+            hk = _heads(k, "k", g_k.shape, g_q.dtype, dev)
+    out = {"q": torch.empty(g_q.shape, dtype=g_q.dtype, device=dev),
+           "k": None if g_k is None else torch.empty(g_k.shape, dtype=g_q.dtype, device=dev),
+           "q_weight": None if q_weight is None else torch.empty(cfg.head_dim, dtype=torch.float32, device=dev),
+           "k_weight": None if k_weight is None else torch.empty(cfg.head_dim, dtype=torch.float32, device=dev)}
+    ws, need = None, 0
+    if q_weight is not None or k_weight is not None:
+        need = lib.qk_norm_rope_backward_workspace_size(cfg, T)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _check(lib, lib.qk_norm_rope_backward(
+        cfg, hq, hk, hg, hgk, pos, tab, wq, wk, T, _heads(out["q"], "g_q"),
+        None if g_k is None else _heads(out["k"], "g_k"), _ptr(out["q_weight"]), _ptr(out["k_weight"]), _ptr(ws),
+        need, _stream(dev)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit cache
+# ---------------------------------------------------------------------------
+
+class KVCache:
+    """A pool of pages of keys and values in int8 with one fp32 scale for each
+    page and head: keys [pages, kv_heads, page, head_dim], values [pages,
+    kv_heads, head_dim, page] (a channel's tokens contiguous), scales [pages,
+    kv_heads]. page 16, 32, 64 or 128; head_dim 64, 128 or 256.
+
+    Wraps tensors the caller owns; KVCache.empty allocates them. Which pages
+    belong to which sequence is the caller's, in the block tables it passes."""
+
+    def __init__(self, keys: torch.Tensor, values: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        if keys.dim() != 4 or not keys.is_cuda:
+            raise ValueError("keys must be [pages, kv_heads, page, head_dim] on the GPU")
+        n, h, p, d = keys.shape
+        dev = keys.device
+        _need_buffer(keys, "keys", None, torch.int8, dev)
+        _need_buffer(values, "values", (n, h, d, p), torch.int8, dev)
+        _need_buffer(k_scale, "k_scale", (n, h), torch.float32, dev)
+        _need_buffer(v_scale, "v_scale", (n, h), torch.float32, dev)
+        self.keys, self.values, self.k_scale, self.v_scale = keys, values, k_scale, v_scale
+        self.device, self.kv_heads, self.page, self.head_dim = dev, h, p, d
+        self._c = _Cache(keys.data_ptr(), values.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n, h, p, d)
+
+    @classmethod
+    def empty(cls, n_pages: int, kv_heads: int, head_dim: int, page: int = 64, device="cuda") -> "KVCache":
+        """An unused cache (contents undefined until tokens are appended)."""
+        i8 = dict(dtype=torch.int8, device=device)
+        f32 = dict(dtype=torch.float32, device=device)
+        return cls(torch.empty((n_pages, kv_heads, page, head_dim), **i8),
+                   torch.empty((n_pages, kv_heads, head_dim, page), **i8),
+                   torch.empty((n_pages, kv_heads), **f32), torch.empty((n_pages, kv_heads), **f32))
+
+
+class CacheBatch:
+    """The sequences of a call and its new tokens. Sequence b holds kv_lens[b]
+    tokens (the new ones included) in the pages block_table[b]; tokens cu[b] ..
+    cu[b + 1] of the call are its last. Without cu every sequence has one.
+
+    block_table [B, max_pages], kv_lens [B], cu [B + 1]: int32 on the GPU.
+    max_new: at least every sequence's count of new tokens. max_kv: about the
+    largest kv_lens (it splits the work and never changes what is computed).
+    """
+
+    def __init__(self, block_table: torch.Tensor, kv_lens: torch.Tensor, max_kv: int,
+                 cu: Optional[torch.Tensor] = None, max_new: int = 1):
+        if block_table.dim() != 2 or not block_table.is_cuda:
+            raise ValueError("block_table must be [B, max_pages] on the GPU")
+        B, pages = block_table.shape
+        dev = block_table.device
+        _need_buffer(block_table, "block_table", None, torch.int32, dev)
+        _need_buffer(kv_lens, "kv_lens", (B,), torch.int32, dev)
+        if cu is not None:
+            _need_buffer(cu, "cu", (B + 1,), torch.int32, dev)
+        self.block_table, self.kv_lens, self.cu, self.device = block_table, kv_lens, cu, dev
+        self.max_kv, self.max_new = max_kv, max_new
+        self._c = _Batch(block_table.data_ptr(), pages, kv_lens.data_ptr(), None if cu is None else cu.data_ptr(),
+                         B, pages, max_new, max_kv)
+
+
+def _same_device(cache: KVCache, batch: CacheBatch):
+    if cache.device != batch.device:
+        raise ValueError(f"the cache is on {cache.device}, the batch on {batch.device}")
+
+
+def kv_cache_append(cache: KVCache, batch: CacheBatch, k: torch.Tensor, v: torch.Tensor) -> None:
+    """Stores the keys and values k, v [T, kv_heads, head_dim] of the batch's
+    tokens, in place. A page and head whose new tokens exceed its scale gets a
+    larger one and its held entries are rounded again; a NaN or an infinity
+    makes the scale of its page and head NaN."""
+    lib = load_library()
+    _same_device(cache, batch)
+    shape = torch.Size((k.shape[0], cache.kv_heads, cache.head_dim))
+    hk = _heads(k, "k", shape, None, cache.device)
+    hv = _heads(v, "v", shape, k.dtype, cache.device)
+    _check(lib, lib.kv_cache_append(cache._c, batch._c, hk, hv, _DTYPES[k.dtype], k.shape[0], _stream(cache.device)))
+
+
+def kv_cache_read(cache: KVCache, batch: CacheBatch, total: int, dtype: torch.dtype = torch.bfloat16,
+                  k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None):
+    """The batch's `total` tokens out of the cache: (k, v), each [total,
+    kv_heads, head_dim], as the values the entries stand for."""
+    lib = load_library()
+    _same_device(cache, batch)
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype must be bfloat16 or float32 (got {dtype})")
+    shape = torch.Size((total, cache.kv_heads, cache.head_dim))
+    k = torch.empty(shape, dtype=dtype, device=cache.device) if k is None else k
+    v = torch.empty(shape, dtype=dtype, device=cache.device) if v is None else v
+    hk, hv = _heads(k, "k", shape, dtype, cache.device), _heads(v, "v", shape, dtype, cache.device)
+    _check(lib, lib.kv_cache_read(cache._c, batch._c, hk, hv, _DTYPES[dtype], total, _stream(cache.device)))
+    return k, v
+
+
+def cache_attention(cache: KVCache, batch: CacheBatch, q: torch.Tensor, scale: Optional[float] = None,
+                    window: int = 0, out: Optional[torch.Tensor] = None, return_lse: bool = False,
+                    workspace: Optional[torch.Tensor] = None):
+    """Causal attention of the batch's tokens q [T, heads, head_dim] over the
+    cache, which holds them already. window > 0: a token sees the last `window`
+    keys, its own among them. scale: head_dim^-0.5 by default. heads is a
+    multiple of the cache's kv_heads. Returns out [T, heads, head_dim], with
+    return_lse also the log of each row's sum, fp32 [T, heads]. A row that sees
+    no key gives zeros and -inf."""
+    lib = load_library()
+    _same_device(cache, batch)
+    hq = _heads(q, "q", None, None, cache.device)
+    T, heads, D = q.shape
+    if D != cache.head_dim:
+        raise ValueError(f"q has heads of {D}, the cache of {cache.head_dim}")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    ho = _heads(out, "out", q.shape, q.dtype, cache.device)
+    lse = torch.empty((T, heads), dtype=torch.float32, device=q.device) if return_lse else None
+    dt = _DTYPES[q.dtype]
+    if workspace is None:
+        need = lib.cache_attention_workspace_size(cache._c, batch._c, heads, dt, window, T)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    else:
+        _need_buffer(workspace, "workspace", None, torch.uint8, cache.device)
+        need = workspace.numel()
+    _check(lib, lib.cache_attention(cache._c, batch._c, hq, heads, dt, T, D ** -0.5 if scale is None else scale,
+                                    window, ho, _ptr(lse), _ptr(workspace), need, _stream(cache.device)))
+    return (out, lse) if return_lse else out

@@ -1,0 +1,104 @@
+// Host-side launchers of the attention-side operators. Each returns the
+// hipGetLastError() of its launches; callers have validated every argument.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "launch.hpp"
+
+namespace sffn {
+
+// A [T, heads, head_dim] view (strides in elements).
+struct Heads {
+    void* p;
+    int64_t st, sh;
+};
+
+// ---- head norms and rotary positions ----------------------------------------
+struct RopeArgs {
+    Dt dt;
+    int n_q, n_k, D, R, max_pos;    // R: rotated elements of each head
+    bool interleaved, norm;
+    float eps;
+    int64_t T;
+    Heads q, k;                     // forward: inputs; backward: the forward's inputs
+    Heads g_q, g_k;                 // backward: gradients of the outputs
+    Heads q_out, k_out;             // forward: outputs; backward: gradients of the inputs
+    const int32_t* pos;             // [T]
+    const float* table;             // [max_pos, R]: cos | sin
+    const void *q_w, *k_w;          // [D] or null (ones)
+    float *g_qw, *g_kw;             // backward: [D] fp32 or null
+    float* partial;                 // backward with norm: rope_partial_floats(...)
+};
+size_t rope_partial_floats(const RopeArgs& a);
+hipError_t launch_rope(const RopeArgs& a, hipStream_t s);
+hipError_t launch_rope_backward(const RopeArgs& a, hipStream_t s);
+
+// ---- 8-bit cache ----------------------------------------------------------------
+struct CacheArgs {
+    int8_t *keys, *values;          // [n_pages, Hkv, P, D], [n_pages, Hkv, D, P]
+    float *k_scale, *v_scale;       // [n_pages, Hkv]
+    int64_t n_pages;
+    int Hkv, P, D, shift;           // P = 1 << shift
+    const int32_t* table;           // [B, max_pages]
+    int64_t table_stride;
+    const int32_t* lens;            // [B]
+    const int32_t* cu;              // [B + 1] or null (token b belongs to sequence b)
+    int B, max_pages, max_new, max_kv;
+    int64_t T;
+    Dt dt;
+};
+// pages of one sequence that n new tokens can touch
+inline int64_t pages_touched(int64_t n, int P) { return n <= 0 ? 0 : (n + P - 2) / P + 1; }
+// workgroups of the append and of the read
+inline int64_t cache_copy_blocks(const CacheArgs& c) {
+    return (int64_t)c.B * pages_touched(c.max_new, c.P) * c.Hkv * 2;
+}
+hipError_t launch_cache_append(const CacheArgs& c, const Heads& k, const Heads& v, hipStream_t s);
+hipError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v, hipStream_t s);
+
+// ---- attention over the cache -----------------------------------------------------
+// How one call is cut up: row tiles of `rows` (token, head) rows for each
+// sequence and key head, and `splits` ranges of `chunk` keys (the last one
+// open) whose partial results a second kernel joins.
+struct AttnPlan {
+    bool few;                       // the 16-row kernel: every sequence's rows fit one tile
+    int waves;                      // of the row-tile kernel's workgroups (32 rows each)
+    int rows, splits;
+    int64_t row_tiles, chunk, blocks;
+    size_t ws_bytes;                // 0 with one split
+};
+
+inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
+    AttnPlan p{};
+    const int64_t G = Hq / c.Hkv, most = (int64_t)c.max_new * G;
+    p.few = most <= 16;
+    p.waves = c.D > 128 || c.dt == Dt::F32 || most <= 128 ? 4 : 8;
+    p.rows = p.few ? 16 : 32 * p.waves;
+    p.row_tiles = (most + p.rows - 1) / p.rows;
+    // keys that one row tile sees: all, or the window of its tokens
+    int64_t span = c.max_kv > 0 ? c.max_kv : 1;
+    if (window > 0) {
+        const int64_t seen = (int64_t)window + p.rows / G + 1 + 63;
+        if (seen < span) span = seen;
+    }
+    const int64_t whole = (int64_t)c.B * c.Hkv * p.row_tiles;
+    const int64_t want = (int64_t)compute_units() * (p.few ? 4 : 2), least = p.few ? 256 : 512;
+    int64_t splits = whole > 0 ? want / whole : 1;
+    const int64_t most_splits = (span + least - 1) / least;
+    if (splits > most_splits) splits = most_splits;
+    if (splits < 1) splits = 1;
+    const int64_t unit = p.few ? 256 : 64;
+    p.chunk = ((span + splits - 1) / splits + unit - 1) / unit * unit;
+    p.splits = (int)((span + p.chunk - 1) / p.chunk);
+    p.blocks = whole * p.splits;
+    if (p.splits > 1) p.ws_bytes = (size_t)c.T * Hq * p.splits * (c.D + 2) * 4;
+    return p;
+}
+
+hipError_t launch_cache_attention(const CacheArgs& c, const AttnPlan& plan, const Heads& q, int Hq, float scale,
+                                  int window, const Heads& out, float* lse, void* ws, hipStream_t s);
+
+}  // namespace sffn

@@ -1,0 +1,686 @@
+// Attention of new tokens over the paged 8-bit cache.
+//
+//   s_j = scale q . (k8_j sk_j),  o = sum_j p_j (v8_j sv_j) / sum_j p_j,  p_j = exp(s_j - max)
+//
+// One pass over the keys with the running maximum m and sum l of the softmax.
+// Entries are small integers, exact in bf16, so q . k8 on the bf16 matrix
+// cores (fp32 accumulation) loses nothing; the page's scale multiplies the
+// fp32 score, and the value's scale the weight p before it is rounded to bf16
+// (p sv, so that a page of small values keeps its relative precision). An fp32
+// q is taken as three bf16 pieces (24 bits), and so are the weights.
+//
+// Both kernels compute S^T = K Q^T and O^T = V^T P^T, which keeps a query row
+// in one matrix column: the lane that holds scores of a row holds that row's
+// weights in just the order in which the second product wants them, provided
+// the key a lane's matrix row stands for is chosen for it. So P never leaves
+// the registers, the softmax needs one or two lane exchanges a tile, and the
+// cache keeps its values transposed ([D][token]) to be that product's operand
+// as they lie.
+#include <math.h>
+
+#include "attn_launch.hpp"
+#include "common.hpp"
+
+namespace sffn {
+
+namespace {
+
+constexpr int kTile = 64;           // keys of one step
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct AttnArgs {
+    CacheArgs c;
+    Heads q, out;
+    int Hq, G, window, splits;
+    int64_t chunk, row_tiles;
+    float scale2;           // scale log2 e
+    float* lse;             // [T, Hq] or null
+    float* part_o;          // [T Hq, splits, D], unnormalised
+    float2* part_ml;        // [T Hq, splits]: maximum (base 2), sum; see finish_row
+};
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_huge_valf(); }
+
+// The rows and keys of one workgroup.
+struct Work {
+    int64_t first;          // first token of the call's
+    int64_t p0;             // position of that token
+    int64_t rows;           // (token, head) rows of the sequence and key head
+    int64_t r0;             // first row of this tile
+    int64_t k0, k1;         // keys of this split
+    int b, h, split;
+};
+
+// False when the tile has no rows.
+__device__ bool find_work(const AttnArgs& a, int tile_rows, Work& w) {
+    const CacheArgs& c = a.c;
+    int64_t id = blockIdx.x;
+    w.h = (int)(id % c.Hkv);
+    id /= c.Hkv;
+    w.b = (int)(id % c.B);
+    id /= c.B;
+    w.split = (int)(id % a.splits);
+    id /= a.splits;
+    const int64_t tile = a.row_tiles - 1 - id;      // the longest rows first
+    int64_t last = w.b + 1;
+    w.first = w.b;
+    if (c.cu) {
+        w.first = c.cu[w.b];
+        last = c.cu[w.b + 1];
+    }
+    if (w.first < 0 || last > c.T || last <= w.first) return false;
+    const int64_t n = last - w.first;
+    const int64_t L = c.lens[w.b] > 0 ? c.lens[w.b] : 0;
+    w.p0 = L - n;
+    w.rows = (n < c.max_new ? n : c.max_new) * a.G;
+    w.r0 = tile * tile_rows;
+    if (w.r0 >= w.rows) return false;
+    const int64_t r1 = w.r0 + tile_rows < w.rows ? w.r0 + tile_rows : w.rows;
+    const int64_t hi = w.p0 + (r1 - 1) / a.G + 1;
+    int64_t lo = a.window > 0 ? w.p0 + w.r0 / a.G - a.window + 1 : 0;
+    if (lo < 0) lo = 0;
+    w.k0 = lo / kTile * kTile + w.split * a.chunk;
+    w.k1 = w.split == a.splits - 1 || hi < w.k0 + a.chunk ? hi : w.k0 + a.chunk;
+    return true;
+}
+
+// Page id of the 16 tokens from `pos` on (pos a multiple of 16); -1 where none
+// of them is below `end` or the table names no page of the pool.
+__device__ __forceinline__ int32_t page_id(const CacheArgs& c, int b, int64_t pos, int64_t end) {
+    const int64_t idx = pos >> c.shift;
+    if (pos >= end || idx >= c.max_pages) return -1;
+    const int32_t id = c.table[(int64_t)b * c.table_stride + idx];
+    return id >= 0 && id < c.n_pages ? id : -1;
+}
+
+// Eight int8 as bf16 (exact).
+__device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t from = i < 2 ? lo : hi;
+        const float x = (float)(int8_t)(from >> (16 * (i & 1)));
+        const float y = (float)(int8_t)(from >> (16 * (i & 1) + 8));
+        w[i] = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
+    }
+    return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+}
+
+// Eight fp32 as NP bf16 pieces whose sum they are (NP = 3) or round to (NP = 1).
+template <int NP>
+__device__ __forceinline__ void pieces(const float* x, bf16x8* out) {
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __bf16 v = (__bf16)r[i];
+            out[p][i] = v;
+            if (p + 1 < NP) r[i] -= (float)v;
+        }
+}
+
+template <typename E, int NP>
+__device__ __forceinline__ void load_q(const E* p, bool valid, bf16x8* out) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    if (valid) Elem<E>::load8(p, x);
+    pieces<NP>(x, out);
+}
+
+__device__ __forceinline__ void store4(uint16_t* p, const float* v) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+__device__ __forceinline__ void store4(float* p, const float* v) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// How much a part with maximum m and sum l counts where the common maximum is
+// M. A part without finite scores has m = -inf: it counts nothing, unless a
+// NaN was among its scores.
+__device__ __forceinline__ float part_factor(float m, float l, float M) {
+    if (m == neg_inf()) return l != l ? 1.f : 0.f;
+    return __builtin_amdgcn_exp2f(m - M);
+}
+
+// 1 / l of a row's final sum. A row that saw keys (seen) with nothing but -inf
+// scores has no softmax: NaN; one that saw none gives zeros.
+__device__ __forceinline__ float row_inverse(float l, bool seen) {
+    if (l == 0.f) return seen ? __builtin_nanf("") : 0.f;
+    return 1.f / l;
+}
+__device__ __forceinline__ float row_lse(float M, float l, bool seen) {
+    if (l == 0.f) return seen ? __builtin_nanf("") : neg_inf();
+    return (M + __log2f(l)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (at most 16: single tokens, drafts): memory-bound, each key and value
+// is read once. Four waves take the split's 64-key steps in turn, each with its
+// own running softmax, straight from memory into matrix operands; they meet in
+// LDS at the end.
+//
+// v_mfma_f32_16x16x32_bf16: lane l holds operand row (A) or column (B) l % 16,
+// k = 8 (l / 16) .. + 7, and of the result column l % 16, rows 4 (l / 16) ..
+// + 3. With g = l / 16:
+//   S^T: step (c, u) takes d = 64 c + 16 g + 8 u .. + 7, so a lane's 16-byte
+//     load of a key is two steps' operand. Matrix row m of score tile t (of
+//     four) stands for key 16 (m / 4) + 4 t + m % 4, so that lane l gets keys
+//     16 g + 4 t + i (i < 4) of query row l % 16: sixteen consecutive ones.
+//   O^T: step u takes keys 16 g + 8 u .. + 7: the weights are in place, and a
+//     lane's 16-byte load of a value row [d][16 g ..] is two steps' operand.
+// ---------------------------------------------------------------------------
+template <typename E, int NP, int D>
+__global__ __launch_bounds__(256) void k_attend_few(const AttnArgs a) {
+    constexpr int KC = D / 64, DT = D / 16;
+    __shared__ float sm[4][16], sl[4][16];
+    __shared__ __align__(16) float so[4][16][D + 4];
+    const CacheArgs& c = a.c;
+    Work w;
+    if (!find_work(a, 16, w)) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int g = lane >> 4, n = lane & 15, gk = n >> 2;
+    const int64_t r = w.r0 + n;
+    const bool valid = r < w.rows;
+    const int64_t tok = valid ? r / a.G : 0;
+    const int head = w.h * a.G + (valid ? (int)(r - tok * a.G) : 0);
+    const int64_t pos = w.p0 + tok;
+
+    bf16x8 qf[KC][2][NP];
+    {
+        const E* q = static_cast<const E*>(a.q.p) + ((w.first + tok) * a.q.st + head * a.q.sh);
+#pragma unroll
+        for (int cc = 0; cc < KC; ++cc)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) load_q<E, NP>(q + 64 * cc + 16 * g + 8 * u, valid, qf[cc][u]);
+    }
+
+    const size_t page_bytes = (size_t)c.P * D;
+    uint4 kr[4][KC];
+    auto load_keys = [&](int32_t id, int64_t t0) {
+        const int8_t* p = c.keys + ((size_t)(id < 0 ? 0 : id) * c.Hkv + w.h) * page_bytes +
+                          (size_t)(((t0 + 16 * gk) & (c.P - 1)) + (n & 3)) * D + 16 * g;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int cc = 0; cc < KC; ++cc)
+                kr[t][cc] = *reinterpret_cast<const uint4*>(p + 4 * t * D + 64 * cc);
+    };
+
+    f32x4 o[DT];
+#pragma unroll
+    for (int i = 0; i < DT; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m = neg_inf(), l = 0.f;
+    const int64_t p_first = w.p0 + w.r0 / a.G;
+    const int64_t p_last = w.p0 + ((w.r0 + 16 < w.rows ? w.r0 + 16 : w.rows) - 1) / a.G;
+
+    int64_t t0 = w.k0 + kTile * wave;
+    int32_t id_k = page_id(c, w.b, t0 + 16 * gk, w.k1), id_v = page_id(c, w.b, t0 + 16 * g, w.k1);
+    if (t0 < w.k1) load_keys(id_k, t0);
+    for (; t0 < w.k1; t0 += 4 * kTile) {
+        // values and scales of this step, page ids of the next
+        uint4 vr[DT];
+        const int8_t* vp = c.values + ((size_t)(id_v < 0 ? 0 : id_v) * c.Hkv + w.h) * page_bytes +
+                           ((t0 + 16 * g) & (c.P - 1));
+#pragma unroll
+        for (int i = 0; i < DT; ++i) vr[i] = *reinterpret_cast<const uint4*>(vp + (size_t)(16 * i + n) * c.P);
+        const size_t srow = (size_t)(id_v < 0 ? 0 : id_v) * c.Hkv + w.h;
+        const float ks = id_v < 0 ? __builtin_nanf("") : c.k_scale[srow] * a.scale2;
+        const float vs = id_v < 0 ? __builtin_nanf("") : c.v_scale[srow];
+        const int64_t tn = t0 + 4 * kTile;
+        const int32_t next_k = page_id(c, w.b, tn + 16 * gk, w.k1), next_v = page_id(c, w.b, tn + 16 * g, w.k1);
+
+        f32x4 s[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int cc = 0; cc < KC; ++cc)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const bf16x8 kf = u ? widen(kr[t][cc].z, kr[t][cc].w) : widen(kr[t][cc].x, kr[t][cc].y);
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)
+                        s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[cc][u][p], s[t], 0, 0, 0);
+                }
+        }
+        if (tn < w.k1) load_keys(next_k, tn);
+        id_v = next_v;
+
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = s[e >> 2][e & 3] * ks;
+        // a key beyond the row's position or before its window has no weight,
+        // whatever is stored there (a select, not an addition)
+        if (t0 + kTile - 1 > p_first || t0 + kTile > w.k1 || (a.window > 0 && t0 <= p_last - a.window)) {
+            const int64_t up = (pos < w.k1 - 1 ? pos : w.k1 - 1) - t0, dn = a.window > 0 ? pos - a.window - t0 : -1;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int key = 16 * g + e;
+                if (key > up || key <= dn) x[e] = neg_inf();
+            }
+        }
+        float top = x[0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const float m_new = fmaxf(m, top);
+        const float m_use = m_new == neg_inf() ? 0.f : m_new;
+        const float alpha = __builtin_amdgcn_exp2f(m - m_use);
+        m = m_new;
+        l *= alpha;
+#pragma unroll
+        for (int i = 0; i < DT; ++i) o[i] *= alpha;
+        bf16x8 pf[2][NP];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            float pv[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float xe = x[8 * u + e];
+                const float p = __builtin_amdgcn_exp2f(xe - m_use);
+                l += p;
+                // a masked key's page may have any scale
+                pv[e] = xe == neg_inf() ? 0.f : p * vs;
+            }
+            pieces<NP>(pv, pf[u]);
+        }
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const bf16x8 vf = u ? widen(vr[i].z, vr[i].w) : widen(vr[i].x, vr[i].y);
+#pragma unroll
+                for (int p = 0; p < NP; ++p)
+                    o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[u][p], o[i], 0, 0, 0);
+            }
+    }
+
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    if (g == 0) {
+        sm[wave][n] = m;
+        sl[wave][n] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < DT; ++i) *reinterpret_cast<f32x4*>(&so[wave][n][16 * i + 4 * g]) = o[i];
+    __syncthreads();
+
+    // thread: row n2, D / 16 consecutive channels
+    const int n2 = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * (D / 16);
+    const int64_t r2 = w.r0 + n2;
+    if (r2 >= w.rows) return;
+    float M = neg_inf(), sum = 0.f, f[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) M = fmaxf(M, sm[v][n2]);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        f[v] = part_factor(sm[v][n2], sl[v][n2], M);
+        sum += f[v] * sl[v][n2];
+    }
+    float acc[D / 16];
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d) acc[d] = 0.f;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+        if (f[v] != 0.f)
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) acc[d] += f[v] * so[v][n2][d0 + d];
+    const int64_t tok2 = r2 / a.G, pos2 = w.p0 + tok2;
+    const int head2 = w.h * a.G + (int)(r2 - tok2 * a.G);
+    const int64_t row = (w.first + tok2) * a.Hq + head2;
+    // does this row see a key of this split?
+    const int64_t from = a.window > 0 && pos2 - a.window + 1 > w.k0 ? pos2 - a.window + 1 : w.k0;
+    const bool seen = from <= pos2 && from < w.k1;
+    if (a.splits == 1) {
+        const float inv = row_inverse(sum, seen);
+        E* out = static_cast<E*>(a.out.p) + ((w.first + tok2) * a.out.st + head2 * a.out.sh) + d0;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) acc[d] *= inv;
+#pragma unroll
+        for (int d = 0; d < D / 16; d += 4) store4(out + d, acc + d);
+        if (a.lse && d0 == 0) a.lse[row] = row_lse(M, sum, seen);
+    } else {
+        const int64_t part = row * a.splits + w.split;
+#pragma unroll
+        for (int d = 0; d < D / 16; d += 4) store4(a.part_o + part * D + d0 + d, acc + d);
+        if (d0 == 0) a.part_ml[part] = make_float2(M, sum == 0.f && seen ? -1.f : sum);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows (chunks of a prompt): NW waves of 32 rows each share 64-key steps,
+// widened to bf16 once for all of them on the way into LDS (double-buffered:
+// the next step's loads are in flight while this one is computed, one barrier
+// a step). Rows run over (token, head of the group), so every head that shares
+// the keys shares the tile.
+//
+// v_mfma_f32_32x32x16_bf16: lane l holds operand row or column l % 32, k = 8
+// (l / 32) .. + 7, and of the result column l % 32, rows 8 (i / 4) + 4 (l / 32)
+// + i % 4, i < 16. With half = l / 32, matrix row m of a 32-key score tile
+// stands for key 16 ((m / 4) % 2) + 4 (m / 8) + m % 4, so that lane l holds
+// keys 16 half + i: what the second product's steps u = 0, 1 take as k.
+//
+// LDS: keys [64][D] and values [D][64], bf16, 16-byte slots XOR-swizzled by
+// row so that the 16 rows of a read's quarter lie in other banks.
+// ---------------------------------------------------------------------------
+template <int D>
+__device__ __forceinline__ int key_slot(int token, int slot) {
+    // sixteen rows {16 a + 4 b + i} of a quarter: (token & 7) and bit 4 tell them apart
+    const int f = D == 64 ? ((token >> 1) & 3) | ((token >> 4) & 1) << 2 : (token & 7) | ((token >> 4) & 1) << 3;
+    return token * (2 * D) + ((slot ^ f) << 4);
+}
+__device__ __forceinline__ int value_slot(int d, int slot) { return d * (2 * kTile) + ((slot ^ ((d >> 1) & 7)) << 4); }
+
+template <typename E, int NP, int D, int NW>
+__global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttnArgs a) {
+    constexpr int NT = 64 * NW, KS = D / 16, DT = D / 32;
+    constexpr int CH = (4 * D + NT - 1) / NT;           // 16-byte pieces a thread loads of keys, and of values
+    constexpr int KB = kTile * D * 2, BUF = 2 * KB;     // bytes of the keys, of one buffer
+    __shared__ __align__(16) char lds[2 * BUF];
+    __shared__ float2 scales[2][4];
+    const CacheArgs& c = a.c;
+    Work w;
+    if (!find_work(a, 32 * NW, w)) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int col = lane & 31, half = lane >> 5;
+    const int64_t r = w.r0 + 32 * wave + col;
+    const bool valid = r < w.rows;
+    const int64_t tok = valid ? r / a.G : 0;
+    const int head = w.h * a.G + (valid ? (int)(r - tok * a.G) : 0);
+    const int64_t pos = w.p0 + tok;
+
+    bf16x8 qf[KS][NP];
+    {
+        const E* q = static_cast<const E*>(a.q.p) + ((w.first + tok) * a.q.st + head * a.q.sh);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) load_q<E, NP>(q + 16 * s + 8 * half, valid, qf[s]);
+    }
+    // positions of this wave's rows
+    const int64_t w0 = w.r0 + 32 * wave, w1 = w0 + 32 < w.rows ? w0 + 32 : w.rows;
+    const bool any = w0 < w.rows;
+    const int64_t p_first = w.p0 + w0 / a.G, p_last = w.p0 + (w1 - 1) / a.G;
+
+    // staging: piece i of this thread
+    const size_t page_bytes = (size_t)c.P * D;
+    uint4 kr[CH], vr[CH];
+    int32_t id_k[CH], id_v[CH];
+    float2 sc = make_float2(0.f, 0.f);
+    int32_t id_s = -1;
+    auto find_pages = [&](int64_t t0) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int p = tid + i * NT;
+            id_k[i] = page_id(c, w.b, t0 + (p / (D / 16) & 48), w.k1);
+            id_v[i] = page_id(c, w.b, t0 + 16 * (p & 3), w.k1);
+        }
+        if (tid < 4) id_s = page_id(c, w.b, t0 + 16 * tid, w.k1);
+    };
+    auto load = [&](int64_t t0) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int p = tid + i * NT;
+            if (4 * D % NT != 0 && p >= 4 * D) break;
+            const int64_t key = t0 + p / (D / 16);
+            kr[i] = *reinterpret_cast<const uint4*>(c.keys + ((size_t)(id_k[i] < 0 ? 0 : id_k[i]) * c.Hkv + w.h) * page_bytes +
+                                                    (size_t)(key & (c.P - 1)) * D + 16 * (p % (D / 16)));
+            vr[i] = *reinterpret_cast<const uint4*>(c.values + ((size_t)(id_v[i] < 0 ? 0 : id_v[i]) * c.Hkv + w.h) * page_bytes +
+                                                    (size_t)(p / 4) * c.P + ((t0 + 16 * (p & 3)) & (c.P - 1)));
+        }
+        if (tid < 4) {
+            const size_t srow = (size_t)(id_s < 0 ? 0 : id_s) * c.Hkv + w.h;
+            sc = id_s < 0 ? make_float2(__builtin_nanf(""), __builtin_nanf(""))
+                          : make_float2(c.k_scale[srow] * a.scale2, c.v_scale[srow]);
+        }
+    };
+    auto stage = [&](int buf) {
+        char* kb = lds + buf * BUF;
+        char* vb = kb + KB;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int p = tid + i * NT;
+            if (4 * D % NT != 0 && p >= 4 * D) break;
+            const int key = p / (D / 16), kslot = 2 * (p % (D / 16)), d = p / 4, vslot = 2 * (p & 3);
+            *reinterpret_cast<bf16x8*>(kb + key_slot<D>(key, kslot)) = widen(kr[i].x, kr[i].y);
+            *reinterpret_cast<bf16x8*>(kb + key_slot<D>(key, kslot + 1)) = widen(kr[i].z, kr[i].w);
+            *reinterpret_cast<bf16x8*>(vb + value_slot(d, vslot)) = widen(vr[i].x, vr[i].y);
+            *reinterpret_cast<bf16x8*>(vb + value_slot(d, vslot + 1)) = widen(vr[i].z, vr[i].w);
+        }
+        if (tid < 4) scales[buf][tid] = sc;
+    };
+
+    f32x16 o[DT];
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
+    float m = neg_inf(), l = 0.f;
+    const int key_row = 16 * ((col >> 2) & 1) + 4 * (col >> 3) + (col & 3);
+
+    if (w.k0 < w.k1) {
+        find_pages(w.k0);
+        load(w.k0);
+        find_pages(w.k0 + kTile);
+        stage(0);
+    }
+    __syncthreads();
+    int buf = 0;
+    for (int64_t t0 = w.k0; t0 < w.k1; t0 += kTile, buf ^= 1) {
+        const bool more = t0 + kTile < w.k1;
+        if (more) {
+            load(t0 + kTile);
+            find_pages(t0 + 2 * kTile);
+        }
+        // some row of this wave sees some key of this step
+        if (any && t0 <= p_last && (a.window == 0 || t0 + kTile - 1 > p_first - a.window)) {
+            const char* kb = lds + buf * BUF;
+            const char* vb = kb + KB;
+            f32x16 s[2];
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) s[tt][j] = 0.f;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const bf16x8 kf = *reinterpret_cast<const bf16x8*>(kb + key_slot<D>(32 * tt + key_row, 2 * k + half));
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)
+                        s[tt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[k][p], s[tt], 0, 0, 0);
+                }
+            }
+            float vs[2];
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+                const float2 f = scales[buf][2 * tt + half];
+                vs[tt] = f.y;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) s[tt][j] *= f.x;
+            }
+            if (t0 + kTile - 1 > p_first || t0 + kTile > w.k1 || (a.window > 0 && t0 <= p_last - a.window)) {
+                const int64_t up = (pos < w.k1 - 1 ? pos : w.k1 - 1) - t0, dn = a.window > 0 ? pos - a.window - t0 : -1;
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int key = 32 * tt + 16 * half + j;
+                        if (key > up || key <= dn) s[tt][j] = neg_inf();
+                    }
+            }
+            float top = neg_inf();
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) top = fmaxf(top, s[tt][j]);
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            const float m_new = fmaxf(m, top);
+            const float m_use = m_new == neg_inf() ? 0.f : m_new;
+            const float alpha = __builtin_amdgcn_exp2f(m - m_use);
+            m = m_new;
+            l *= alpha;
+#pragma unroll
+            for (int i = 0; i < DT; ++i) o[i] *= alpha;
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float pv[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float xe = s[tt][8 * u + e];
+                        const float p = __builtin_amdgcn_exp2f(xe - m_use);
+                        l += p;
+                        pv[e] = xe == neg_inf() ? 0.f : p * vs[tt];
+                    }
+                    bf16x8 pf[NP];
+                    pieces<NP>(pv, pf);
+#pragma unroll
+                    for (int i = 0; i < DT; ++i) {
+                        const bf16x8 vf = *reinterpret_cast<const bf16x8*>(vb + value_slot(32 * i + col, 4 * tt + 2 * half + u));
+#pragma unroll
+                        for (int p = 0; p < NP; ++p)
+                            o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[p], o[i], 0, 0, 0);
+                    }
+                }
+        }
+        if (more) stage(buf ^ 1);
+        __syncthreads();
+    }
+
+    l += __shfl_xor(l, 32, 64);
+    if (!valid) return;
+    const int64_t row = (w.first + tok) * a.Hq + head;
+    const int64_t from = a.window > 0 && pos - a.window + 1 > w.k0 ? pos - a.window + 1 : w.k0;
+    const bool seen = from <= pos && from < w.k1;
+    const float inv = a.splits == 1 ? row_inverse(l, seen) : 1.f;
+    const int64_t part = row * a.splits + w.split;
+    E* out = static_cast<E*>(a.out.p) + ((w.first + tok) * a.out.st + head * a.out.sh);
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int d = 32 * i + 8 * q + 4 * half;
+            const float v[4] = {o[i][4 * q] * inv, o[i][4 * q + 1] * inv, o[i][4 * q + 2] * inv, o[i][4 * q + 3] * inv};
+            if (a.splits == 1) store4(out + d, v);
+            else store4(a.part_o + part * D + d, v);
+        }
+    if (half != 0) return;
+    if (a.splits > 1) a.part_ml[part] = make_float2(m, l == 0.f && seen ? -1.f : l);
+    else if (a.lse) a.lse[row] = row_lse(m, l, seen);
+}
+
+// ---------------------------------------------------------------------------
+// Joins the splits of a row: a workgroup per row, wave v takes splits v, v + 4,
+// ..., lanes the channels; the waves meet in LDS (a fixed order).
+// A sum of -1 marks a split whose keys were seen but all scored -inf. Tokens of
+// no sequence, or beyond its first max_new, have no parts and are left alone.
+// ---------------------------------------------------------------------------
+template <typename E, int D>
+__global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a) {
+    constexpr int PL = D / 64;
+    __shared__ float so[4][D];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t row = blockIdx.x;
+    const int64_t t = row / a.Hq;
+    if (a.c.cu) {
+        int lo = 0, hi = a.c.B;             // cu[lo] <= t < cu[hi], where t is in a sequence
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (a.c.cu[mid] <= t) lo = mid;
+            else hi = mid;
+        }
+        const int64_t first = a.c.cu[lo], last = a.c.cu[hi];
+        if (first < 0 || last > a.c.T || t < first || t >= last || t - first >= a.c.max_new) return;
+    }
+    const float2* ml = a.part_ml + row * a.splits;
+    float M = neg_inf();
+    for (int s = lane; s < a.splits; s += 64) M = fmaxf(M, ml[s].x);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor(M, o, 64));
+    float sum = 0.f, marks = 0.f;
+    for (int s = lane; s < a.splits; s += 64) {
+        const float2 p = ml[s];
+        const float f = part_factor(p.x, p.y, M);
+        if (f != 0.f) sum += f * p.y;
+        else if (p.y < 0.f) marks = 1.f;
+    }
+    sum = wave_sum(sum);
+    marks = wave_sum(marks);
+    float acc[PL];
+#pragma unroll
+    for (int i = 0; i < PL; ++i) acc[i] = 0.f;
+    for (int s = wave; s < a.splits; s += 4) {
+        const float2 p = ml[s];
+        const float f = part_factor(p.x, p.y, M);
+        if (f == 0.f) continue;
+        const float* o = a.part_o + (row * a.splits + s) * D + lane;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) acc[i] += f * o[64 * i];
+    }
+#pragma unroll
+    for (int i = 0; i < PL; ++i) so[wave][lane + 64 * i] = acc[i];
+    __syncthreads();
+    const int h = (int)(row - t * a.Hq);
+    const float inv = row_inverse(sum, marks != 0.f);
+    E* out = static_cast<E*>(a.out.p) + (t * a.out.st + h * a.out.sh);
+    for (int d = threadIdx.x; d < D; d += 256)
+        Elem<E>::store1(out + d, (so[0][d] + so[1][d] + so[2][d] + so[3][d]) * inv);
+    if (a.lse && threadIdx.x == 0) a.lse[row] = row_lse(M, sum, marks != 0.f);
+}
+
+template <typename E, int NP, int D>
+hipError_t launch(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
+    const dim3 grid((unsigned)plan.blocks);
+    if (plan.few) {
+        k_attend_few<E, NP, D><<<grid, 256, 0, s>>>(a);
+    } else {
+        if constexpr (D <= 128 && NP == 1) {
+            if (plan.waves == 8) k_attend_rows<E, NP, D, 8><<<grid, 512, 0, s>>>(a);
+            else k_attend_rows<E, NP, D, 4><<<grid, 256, 0, s>>>(a);
+        } else {
+            k_attend_rows<E, NP, D, 4><<<grid, 256, 0, s>>>(a);
+        }
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || plan.splits == 1) return e;
+    k_attend_join<E, D><<<dim3((unsigned)(a.c.T * a.Hq)), 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <typename E, int NP>
+hipError_t launch_dim(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
+    switch (a.c.D) {
+        case 64: return launch<E, NP, 64>(a, plan, s);
+        case 128: return launch<E, NP, 128>(a, plan, s);
+        default: return launch<E, NP, 256>(a, plan, s);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_cache_attention(const CacheArgs& c, const AttnPlan& plan, const Heads& q, int Hq, float scale,
+                                  int window, const Heads& out, float* lse, void* ws, hipStream_t s) {
+    AttnArgs a{};
+    a.c = c;
+    a.q = q;
+    a.out = out;
+    a.Hq = Hq;
+    a.G = Hq / c.Hkv;
+    a.window = window;
+    a.splits = plan.splits;
+    a.chunk = plan.chunk;
+    a.row_tiles = plan.row_tiles;
+    a.scale2 = scale * kLog2e;
+    a.lse = lse;
+    if (plan.splits > 1) {
+        a.part_ml = static_cast<float2*>(ws);
+        a.part_o = static_cast<float*>(ws) + (size_t)c.T * Hq * plan.splits * 2;
+    }
+    return c.dt == Dt::BF16 ? launch_dim<uint16_t, 1>(a, plan, s) : launch_dim<float, 3>(a, plan, s);
+}
+
+}  // namespace sffn

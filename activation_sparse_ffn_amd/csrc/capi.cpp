@@ -12,16 +12,14 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <algorithm>
 #include <cstring>
 #include <mutex>
 #include <new>
-#include <string>
 
 #include "../../include/sparse_ffn.h"
 #include "launch.hpp"
+#include "status.hpp"
 
 namespace {
 
@@ -30,31 +28,14 @@ constexpr int64_t kSkinnyMaxTokens = 64;
 constexpr size_t kAlign = 256;
 constexpr int64_t kMaxGrid = (int64_t)1 << 31;
 
-thread_local std::string g_last_error;
-
-sffn_status_t fail(sffn_status_t st, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return st;
-}
+using sffn::aligned16;
+using sffn::as_int;
+using sffn::fail;
+using sffn::hip_status;
 
 size_t align_up(size_t n) { return (n + kAlign - 1) / kAlign * kAlign; }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 size_t elem_size(sffn_dtype_t dt) { return dt == SFFN_BF16 ? 2 : 4; }
-
-template <typename Enum>
-int as_int(const Enum& e) {
-    static_assert(sizeof(Enum) == sizeof(int), "enums of the C ABI are int-sized");
-    int v;
-    std::memcpy(&v, &e, sizeof v);
-    return v;
-}
 
 sffn_status_t check_config(const sffn_config_t* c) {
     if (!c) return fail(SFFN_ERR_INVALID_ARG, "config is null");
@@ -176,11 +157,6 @@ bool tokens_fit(const sffn_config_t& c, int64_t T) {
 }
 // the backward pass: T tokens padded to 64, transposed operands of T columns
 constexpr int64_t kMaxBackwardTokens = (int64_t)1 << 24;
-
-sffn_status_t hip_status(hipError_t e, const char* what) {
-    if (e == hipSuccess) return SFFN_OK;
-    return fail(SFFN_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
 
 template <typename P>
 P* at(void* base, size_t off) {
@@ -307,7 +283,7 @@ sffn_status_t sparse_ffn_create(const sffn_config_t* cfg, const void* w_gate, co
     h->has_bias = pred_bias != nullptr;
     h->profiling = false;
     *out = h;
-    g_last_error.clear();
+    sffn::last_error[0] = '\0';
     return SFFN_OK;
 }
 
@@ -565,6 +541,6 @@ const char* sparse_ffn_status_string(sffn_status_t status) {
     return "unknown status";
 }
 
-const char* sparse_ffn_last_error(void) { return g_last_error.c_str(); }
+const char* sparse_ffn_last_error(void) { return sffn::last_error; }
 
 }  // extern "C"
