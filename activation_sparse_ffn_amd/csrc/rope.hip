@@ -14,6 +14,8 @@
 // most one exchange away. A group takes several heads of one token in turn and
 // keeps that token's cos and sin (64 bytes a lane, four times a head's own
 // bytes) in registers.
+#include <type_traits>
+
 #include "attn_launch.hpp"
 #include "common.hpp"
 
@@ -270,8 +272,19 @@ __global__ __launch_bounds__(kThreads) void k_rope_sum(const float* __restrict__
 // any head_dim <= 512, any even R, any strides: a wave per head, lane l holds
 // elements l, l + 64, .... A pair's other element is read from memory as well,
 // before anything is written, so an output may be its own input.
+//
+// The gradient's difference u - x^ mean(u x^) cancels where u is nearly along
+// x^, as in heads of a few elements, which come here (with one element it
+// leaves eps r^2 of its terms). So this kernel takes r, x^, the mean and the
+// difference in 64 bits; it waits for memory either way.
 // ---------------------------------------------------------------------------
 constexpr int kPer = 8;     // 512 / 64
+
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, kWave);
+    return v;
+}
 
 template <typename E, bool BWD>
 __global__ __launch_bounds__(kThreads) void k_rope_any(const RopeArgs a) {
@@ -302,7 +315,8 @@ __global__ __launch_bounds__(kThreads) void k_rope_any(const RopeArgs a) {
         const float* row = a.table + (size_t)pos * a.R;
         // own[i], other[i]: element e and its pair's other one of what is turned
         float x[kPer], own[kPer], other[kPer], w[kPer], wo[kPer];
-        float sum = 0.f;
+        typedef std::conditional_t<BWD, double, float> Acc;
+        Acc sum = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int e = lane + 64 * i;
@@ -315,10 +329,14 @@ __global__ __launch_bounds__(kThreads) void k_rope_any(const RopeArgs a) {
             other[i] = to_f32<E>(tp[o]);
             if (a.norm) x[i] = BWD ? to_f32<E>(xp[e]) : own[i];
             if (wp) { w[i] = to_f32<E>(wp[e]); wo[i] = to_f32<E>(wp[o]); }
-            sum += x[i] * x[i];
+            sum += (Acc)x[i] * x[i];
         }
-        const float r = a.norm ? rsqrtf(wave_sum(sum) / (float)a.D + a.eps) : 1.f;
-        float dot = 0.f;
+        Acc r = 1;
+        if (a.norm) {
+            if constexpr (BWD) r = 1.0 / sqrt(wave_sum64(sum) / a.D + (double)a.eps);
+            else r = rsqrtf(wave_sum(sum) / (float)a.D + a.eps);
+        }
+        Acc dot = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int e = lane + 64 * i;
@@ -333,19 +351,22 @@ __global__ __launch_bounds__(kThreads) void k_rope_any(const RopeArgs a) {
             }
             if (!ok) v = __builtin_nanf("");
             if (BWD && a.norm) {
-                x[i] *= r;
-                if (is_q) sq[i] += v * x[i]; else sk[i] += v * x[i];
+                const Acc xh = x[i] * r;
+                const float gw = (float)(v * xh);
+                if (is_q) sq[i] += gw; else sk[i] += gw;
                 v *= w[i];
-                dot += v * x[i];
+                dot += v * xh;
             }
             own[i] = v;
         }
-        const float m = BWD && a.norm ? wave_sum(dot) / (float)a.D : 0.f;
+        Acc m = 0;
+        if constexpr (BWD)
+            if (a.norm) m = wave_sum64(dot) / a.D;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int e = lane + 64 * i;
             if (e >= a.D) continue;
-            const float v = BWD && a.norm ? r * (own[i] - x[i] * m) : own[i];
+            const float v = BWD && a.norm ? (float)(r * (own[i] - x[i] * r * m)) : own[i];
             Elem<E>::store1(static_cast<E*>(out.p) + at(out, t, hh) + e, v);
         }
     }
