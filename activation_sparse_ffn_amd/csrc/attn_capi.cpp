@@ -17,6 +17,10 @@ using sffn::hip_status;
 
 // Bounds that keep every size product below 2^63 and every grid below 2^31.
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;
+// Of the cache: new tokens of a call and tokens of a sequence, so that every
+// position, with a call's tokens added, fits 31 bits.
+constexpr int64_t kMaxNewTokens = (int64_t)1 << 28;
+constexpr int64_t kMaxCapacity = (int64_t)1 << 30;
 constexpr int64_t kMaxStride = (int64_t)1 << 42;
 constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
 constexpr int32_t kMaxHeads = 65536;
@@ -139,7 +143,9 @@ sffn_status_t check_cache(const sffn_kv_cache_t* c, const sffn_kv_batch_t* b, in
         return fail(SFFN_ERR_INVALID_ARG, "table_stride %lld does not fit rows of %d pages",
                     (long long)b->table_stride, b->max_pages);
     if (T < 0) return fail(SFFN_ERR_INVALID_ARG, "T must be >= 0 (got %lld)", (long long)T);
-    if (T > kMaxTokens) return fail(SFFN_ERR_UNSUPPORTED, "T = %lld is too large for one call", (long long)T);
+    if (T > kMaxNewTokens) return fail(SFFN_ERR_UNSUPPORTED, "T = %lld is too large for one call", (long long)T);
+    if ((int64_t)b->max_pages * c->page > kMaxCapacity)
+        return fail(SFFN_ERR_UNSUPPORTED, "max_pages %d of %d tokens are too many", b->max_pages, c->page);
     if (!b->cu && T != b->n_seqs)
         return fail(SFFN_ERR_INVALID_ARG, "without cu, T must be n_seqs (got %lld, %d)", (long long)T, b->n_seqs);
     if (!b->cu && T > 0 && b->max_new < 1)

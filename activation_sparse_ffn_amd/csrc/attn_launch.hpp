@@ -85,7 +85,7 @@ inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
         if (seen < span) span = seen;
     }
     const int64_t whole = (int64_t)c.B * c.Hkv * p.row_tiles;
-    const int64_t want = (int64_t)compute_units() * (p.few ? 4 : 2), least = p.few ? 256 : 512;
+    const int64_t want = (int64_t)compute_units() * (p.few ? 16 : 2), least = 512;
     int64_t splits = whole > 0 ? want / whole : 1;
     const int64_t most_splits = (span + least - 1) / least;
     if (splits > most_splits) splits = most_splits;

@@ -33,65 +33,90 @@ struct AttnArgs {
     CacheArgs c;
     Heads q, out;
     int Hq, G, window, splits;
-    int64_t chunk, row_tiles;
-    float scale2;           // scale log2 e
+    int chunk, row_tiles;
+    float scale2;           // |scale| log2 e; a negative scale turns q round
+    bool negate;
     float* lse;             // [T, Hq] or null
     float* part_o;          // [T Hq, splits, D], unnormalised
-    float2* part_ml;        // [T Hq, splits]: maximum (base 2), sum; see finish_row
+    float2* part_ml;        // [T Hq, splits]: reference maximum (base 2), sum; see row_inverse
 };
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_huge_valf(); }
 
-// The rows and keys of one workgroup.
+// The rows and keys of one workgroup. Positions fit 31 bits (the host bounds
+// the table's capacity and the call's tokens).
 struct Work {
-    int64_t first;          // first token of the call's
-    int64_t p0;             // position of that token
-    int64_t rows;           // (token, head) rows of the sequence and key head
-    int64_t r0;             // first row of this tile
-    int64_t k0, k1;         // keys of this split
+    int first;              // first token of the sequence's in the call
+    int p0;                 // position of that token
+    int rows;               // (token, head) rows of the sequence and key head
+    int r0;                 // first row of this tile
+    int k0, k1;             // keys of this split
     int b, h, split;
 };
 
 // False when the tile has no rows.
-__device__ bool find_work(const AttnArgs& a, int tile_rows, Work& w) {
+__device__ __forceinline__ bool find_work(const AttnArgs& a, int tile_rows, Work& w) {
     const CacheArgs& c = a.c;
-    int64_t id = blockIdx.x;
-    w.h = (int)(id % c.Hkv);
-    id /= c.Hkv;
-    w.b = (int)(id % c.B);
-    id /= c.B;
-    w.split = (int)(id % a.splits);
-    id /= a.splits;
-    const int64_t tile = a.row_tiles - 1 - id;      // the longest rows first
-    int64_t last = w.b + 1;
+    uint32_t id = blockIdx.x;
+    w.h = (int)(id % (uint32_t)c.Hkv);
+    id /= (uint32_t)c.Hkv;
+    w.b = (int)(id % (uint32_t)c.B);
+    id /= (uint32_t)c.B;
+    w.split = (int)(id % (uint32_t)a.splits);
+    id /= (uint32_t)a.splits;
+    const int tile = a.row_tiles - 1 - (int)id;     // the longest rows first
+    int last = w.b + 1;
     w.first = w.b;
     if (c.cu) {
         w.first = c.cu[w.b];
         last = c.cu[w.b + 1];
     }
     if (w.first < 0 || last > c.T || last <= w.first) return false;
-    const int64_t n = last - w.first;
-    const int64_t L = c.lens[w.b] > 0 ? c.lens[w.b] : 0;
+    const int n = last - w.first, capacity = c.max_pages << c.shift;
+    int L = c.lens[w.b];
+    if (L < 0) L = 0;
+    // more tokens than the table has room for: every row sees one of no page
+    if (L > capacity) L = capacity + n;
     w.p0 = L - n;
-    w.rows = (n < c.max_new ? n : c.max_new) * a.G;
-    w.r0 = tile * tile_rows;
-    if (w.r0 >= w.rows) return false;
-    const int64_t r1 = w.r0 + tile_rows < w.rows ? w.r0 + tile_rows : w.rows;
-    const int64_t hi = w.p0 + (r1 - 1) / a.G + 1;
-    int64_t lo = a.window > 0 ? w.p0 + w.r0 / a.G - a.window + 1 : 0;
-    if (lo < 0) lo = 0;
-    w.k0 = lo / kTile * kTile + w.split * a.chunk;
-    w.k1 = w.split == a.splits - 1 || hi < w.k0 + a.chunk ? hi : w.k0 + a.chunk;
+    const int64_t rows = (int64_t)(n < c.max_new ? n : c.max_new) * a.G, r0 = (int64_t)tile * tile_rows;
+    if (r0 >= rows) return false;
+    w.rows = (int)rows;
+    w.r0 = (int)r0;
+    const int r1 = w.rows - w.r0 < tile_rows ? w.rows : w.r0 + tile_rows;
+    const int hi = w.p0 + (r1 - 1) / a.G + 1;
+    int lo = 0;
+    if (a.window > 0) {
+        const int64_t from = (int64_t)w.p0 + w.r0 / a.G - a.window + 1;
+        if (from > 0) lo = (int)from;
+    }
+    const int64_t k0 = lo / kTile * kTile + (int64_t)w.split * a.chunk;
+    w.k0 = (int)(k0 < hi ? k0 : hi);
+    w.k1 = w.split == a.splits - 1 || hi < k0 + a.chunk ? hi : w.k0 + a.chunk;
     return true;
 }
 
 // Page id of the 16 tokens from `pos` on (pos a multiple of 16); -1 where none
 // of them is below `end` or the table names no page of the pool.
-__device__ __forceinline__ int32_t page_id(const CacheArgs& c, int b, int64_t pos, int64_t end) {
-    const int64_t idx = pos >> c.shift;
+__device__ __forceinline__ int page_id(const CacheArgs& c, int b, int pos, int end) {
+    const int idx = pos >> c.shift;
     if (pos >= end || idx >= c.max_pages) return -1;
-    const int32_t id = c.table[(int64_t)b * c.table_stride + idx];
-    return id >= 0 && id < c.n_pages ? id : -1;
+    const int id = c.table[(int64_t)b * c.table_stride + idx];
+    return id >= 0 && id < (int)c.n_pages ? id : -1;
+}
+
+// Whether the row at position p sees a key of [k0, k1).
+__device__ __forceinline__ bool row_sees(int p, int window, int k0, int k1) {
+    const int from = window > 0 && p - (window - 1) > k0 ? p - (window - 1) : k0;
+    return from <= p && from < k1;
+}
+
+// The last of the first `keys` keys from t0 on that a row at position p sees,
+// and the last one before those it sees, both relative to t0.
+__device__ __forceinline__ int last_seen(int p, int t0, int k1) { return (p < k1 - 1 ? p : k1 - 1) - t0; }
+__device__ __forceinline__ int before_seen(int p, int t0, int window) {
+    if (window == 0) return -1;
+    const int64_t d = (int64_t)p - window - t0;
+    return d < -1 ? -1 : (int)d;
 }
 
 // Eight int8 as bf16 (exact).
@@ -107,28 +132,43 @@ __device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
     return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
-// Eight fp32 as NP bf16 pieces whose sum they are (NP = 3) or round to (NP = 1).
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// Two fp32 rounded to bf16, to nearest even, as one word.
+__device__ __forceinline__ uint32_t round2(float x, float y) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{x, y}), bf16x2));
+}
+
+// Eight fp32 as NP bf16 pieces: their sum is x to 8 NP bits.
 template <int NP>
 __device__ __forceinline__ void pieces(const float* x, bf16x8* out) {
     float r[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = x[i];
 #pragma unroll
-    for (int p = 0; p < NP; ++p)
+    for (int p = 0; p < NP; ++p) {
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const __bf16 v = (__bf16)r[i];
-            out[p][i] = v;
-            if (p + 1 < NP) r[i] -= (float)v;
+        for (int i = 0; i < 4; ++i) {
+            w[i] = round2(r[2 * i], r[2 * i + 1]);
+            if (p + 1 < NP) {
+                r[2 * i] -= bf16_lo(w[i]);
+                r[2 * i + 1] -= bf16_hi(w[i]);
+            }
         }
+        out[p] = __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+    }
 }
 
 template <typename E, int NP>
-__device__ __forceinline__ void load_q(const E* p, bool valid, bf16x8* out) {
+__device__ __forceinline__ void load_q(const E* p, bool valid, bool negate, bf16x8* out) {
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = 0.f;
     if (valid) Elem<E>::load8(p, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = negate ? -x[i] : x[i];
     pieces<NP>(x, out);
 }
 
@@ -139,9 +179,15 @@ __device__ __forceinline__ void store4(float* p, const float* v) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
-// How much a part with maximum m and sum l counts where the common maximum is
-// M. A part without finite scores has m = -inf: it counts nothing, unless a
-// NaN was among its scores.
+// The running maximum m is a reference, not always the largest score: it moves
+// (and the sums are scaled) only when a row's scores pass it by more than
+// kSlack, which spares nearly every step the products over the whole output
+// tile. Weights then reach 2^kSlack, nothing to fp32 sums or to bf16's range.
+constexpr float kSlack = 8.f;
+
+// How much a part with reference m and sum l counts where the common one is M.
+// A part without finite scores has m = -inf: it counts nothing, unless a NaN
+// was among its scores.
 __device__ __forceinline__ float part_factor(float m, float l, float M) {
     if (m == neg_inf()) return l != l ? 1.f : 0.f;
     return __builtin_amdgcn_exp2f(m - M);
@@ -174,8 +220,8 @@ __device__ __forceinline__ float row_lse(float M, float l, bool seen) {
 //   O^T: step u takes keys 16 g + 8 u .. + 7: the weights are in place, and a
 //     lane's 16-byte load of a value row [d][16 g ..] is two steps' operand.
 // ---------------------------------------------------------------------------
-template <typename E, int NP, int D>
-__global__ __launch_bounds__(256) void k_attend_few(const AttnArgs a) {
+template <typename E, int NP, int PP, int D>
+__global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few(const AttnArgs a) {
     constexpr int KC = D / 64, DT = D / 16;
     __shared__ float sm[4][16], sl[4][16];
     __shared__ __align__(16) float so[4][16][D + 4];
@@ -184,55 +230,56 @@ __global__ __launch_bounds__(256) void k_attend_few(const AttnArgs a) {
     if (!find_work(a, 16, w)) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int g = lane >> 4, n = lane & 15, gk = n >> 2;
-    const int64_t r = w.r0 + n;
-    const bool valid = r < w.rows;
-    const int64_t tok = valid ? r / a.G : 0;
-    const int head = w.h * a.G + (valid ? (int)(r - tok * a.G) : 0);
-    const int64_t pos = w.p0 + tok;
+    const bool valid = w.r0 + n < w.rows;
+    const int tok = valid ? (w.r0 + n) / a.G : 0;
+    const int head = w.h * a.G + (valid ? w.r0 + n - tok * a.G : 0);
+    const int pos = w.p0 + tok;
 
-    bf16x8 qf[KC][2][NP];
-    {
-        const E* q = static_cast<const E*>(a.q.p) + ((w.first + tok) * a.q.st + head * a.q.sh);
-#pragma unroll
-        for (int cc = 0; cc < KC; ++cc)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) load_q<E, NP>(q + 64 * cc + 16 * g + 8 * u, valid, qf[cc][u]);
-    }
-
-    const size_t page_bytes = (size_t)c.P * D;
+    const uint32_t head_bytes = (uint32_t)c.P * D;      // of one page
+    const size_t page_bytes = (size_t)c.Hkv * head_bytes;
+    const int8_t* keys = c.keys + (size_t)w.h * head_bytes + (((16 * gk) & (c.P - 1)) + (n & 3)) * D + 16 * g;
+    const int8_t* values = c.values + (size_t)w.h * head_bytes + n * c.P + ((16 * g) & (c.P - 1));
+    const float *k_scale = c.k_scale + w.h, *v_scale = c.v_scale + w.h;
     uint4 kr[4][KC];
-    auto load_keys = [&](int32_t id, int64_t t0) {
-        const int8_t* p = c.keys + ((size_t)(id < 0 ? 0 : id) * c.Hkv + w.h) * page_bytes +
-                          (size_t)(((t0 + 16 * gk) & (c.P - 1)) + (n & 3)) * D + 16 * g;
+    auto load_keys = [&](int id, int t0) {
+        const int8_t* p = keys + (id < 0 ? 0 : id) * page_bytes + (t0 & (c.P - 1)) * D;
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int cc = 0; cc < KC; ++cc)
-                kr[t][cc] = *reinterpret_cast<const uint4*>(p + 4 * t * D + 64 * cc);
+            for (int cc = 0; cc < KC; ++cc) kr[t][cc] = *reinterpret_cast<const uint4*>(p + 4 * t * D + 64 * cc);
     };
 
+    int t0 = w.k0 + kTile * wave;
+    int id_k = page_id(c, w.b, t0 + 16 * gk, w.k1), id_v = page_id(c, w.b, t0 + 16 * g, w.k1);
+    if (t0 < w.k1) load_keys(id_k, t0);
+
+    bf16x8 qf[KC][2][NP];
+    {
+        const E* q = static_cast<const E*>(a.q.p) + ((int64_t)(w.first + tok) * a.q.st + head * a.q.sh);
+#pragma unroll
+        for (int cc = 0; cc < KC; ++cc)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) load_q<E, NP>(q + 64 * cc + 16 * g + 8 * u, valid, a.negate, qf[cc][u]);
+    }
     f32x4 o[DT];
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     float m = neg_inf(), l = 0.f;
-    const int64_t p_first = w.p0 + w.r0 / a.G;
-    const int64_t p_last = w.p0 + ((w.r0 + 16 < w.rows ? w.r0 + 16 : w.rows) - 1) / a.G;
+    const int p_first = w.p0 + w.r0 / a.G;
+    const int p_last = w.p0 + ((w.rows - w.r0 < 16 ? w.rows : w.r0 + 16) - 1) / a.G;
 
-    int64_t t0 = w.k0 + kTile * wave;
-    int32_t id_k = page_id(c, w.b, t0 + 16 * gk, w.k1), id_v = page_id(c, w.b, t0 + 16 * g, w.k1);
-    if (t0 < w.k1) load_keys(id_k, t0);
     for (; t0 < w.k1; t0 += 4 * kTile) {
         // values and scales of this step, page ids of the next
         uint4 vr[DT];
-        const int8_t* vp = c.values + ((size_t)(id_v < 0 ? 0 : id_v) * c.Hkv + w.h) * page_bytes +
-                           ((t0 + 16 * g) & (c.P - 1));
+        const size_t idv = id_v < 0 ? 0 : id_v;
+        const int8_t* vp = values + idv * page_bytes + (t0 & (c.P - 1));
 #pragma unroll
-        for (int i = 0; i < DT; ++i) vr[i] = *reinterpret_cast<const uint4*>(vp + (size_t)(16 * i + n) * c.P);
-        const size_t srow = (size_t)(id_v < 0 ? 0 : id_v) * c.Hkv + w.h;
-        const float ks = id_v < 0 ? __builtin_nanf("") : c.k_scale[srow] * a.scale2;
-        const float vs = id_v < 0 ? __builtin_nanf("") : c.v_scale[srow];
-        const int64_t tn = t0 + 4 * kTile;
-        const int32_t next_k = page_id(c, w.b, tn + 16 * gk, w.k1), next_v = page_id(c, w.b, tn + 16 * g, w.k1);
+        for (int i = 0; i < DT; ++i) vr[i] = *reinterpret_cast<const uint4*>(vp + 16 * i * c.P);
+        float ks = k_scale[idv * c.Hkv] * a.scale2, vs = v_scale[idv * c.Hkv];
+        if (id_v < 0) ks = vs = __builtin_nanf("");
+        const int tn = t0 + 4 * kTile;
+        id_k = page_id(c, w.b, tn + 16 * gk, w.k1);
+        id_v = page_id(c, w.b, tn + 16 * g, w.k1);
 
         f32x4 s[4];
 #pragma unroll
@@ -248,47 +295,46 @@ __global__ __launch_bounds__(256) void k_attend_few(const AttnArgs a) {
                         s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[cc][u][p], s[t], 0, 0, 0);
                 }
         }
-        if (tn < w.k1) load_keys(next_k, tn);
-        id_v = next_v;
+        if (tn < w.k1) load_keys(id_k, tn);
 
         float x[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] = s[e >> 2][e & 3] * ks;
         // a key beyond the row's position or before its window has no weight,
-        // whatever is stored there (a select, not an addition)
+        // whatever is stored there: a select, and a scale of 0 where the row
+        // sees none of the lane's sixteen (they share a page)
         if (t0 + kTile - 1 > p_first || t0 + kTile > w.k1 || (a.window > 0 && t0 <= p_last - a.window)) {
-            const int64_t up = (pos < w.k1 - 1 ? pos : w.k1 - 1) - t0, dn = a.window > 0 ? pos - a.window - t0 : -1;
+            const int up = last_seen(pos, t0, w.k1) - 16 * g, dn = before_seen(pos, t0, a.window) - 16 * g;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int key = 16 * g + e;
-                if (key > up || key <= dn) x[e] = neg_inf();
-            }
+            for (int e = 0; e < 16; ++e)
+                if (e > up || e <= dn) x[e] = neg_inf();
+            if (up < 0 || dn >= 15) vs = 0.f;
         }
         float top = x[0];
 #pragma unroll
         for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
         top = fmaxf(top, __shfl_xor(top, 16, 64));
         top = fmaxf(top, __shfl_xor(top, 32, 64));
-        const float m_new = fmaxf(m, top);
-        const float m_use = m_new == neg_inf() ? 0.f : m_new;
-        const float alpha = __builtin_amdgcn_exp2f(m - m_use);
-        m = m_new;
-        l *= alpha;
+        if (__any(top > m + kSlack)) {
+            const float to = fmaxf(m, top);
+            const float alpha = __builtin_amdgcn_exp2f(m - (to == neg_inf() ? 0.f : to));
+            m = to;
+            l *= alpha;
 #pragma unroll
-        for (int i = 0; i < DT; ++i) o[i] *= alpha;
-        bf16x8 pf[2][NP];
+            for (int i = 0; i < DT; ++i) o[i] *= alpha;
+        }
+        const float ref = m == neg_inf() ? 0.f : m;
+        bf16x8 pf[2][PP];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             float pv[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float xe = x[8 * u + e];
-                const float p = __builtin_amdgcn_exp2f(xe - m_use);
+                const float p = __builtin_amdgcn_exp2f(x[8 * u + e] - ref);
                 l += p;
-                // a masked key's page may have any scale
-                pv[e] = xe == neg_inf() ? 0.f : p * vs;
+                pv[e] = p * vs;
             }
-            pieces<NP>(pv, pf[u]);
+            pieces<PP>(pv, pf[u]);
         }
 #pragma unroll
         for (int i = 0; i < DT; ++i)
@@ -296,7 +342,7 @@ __global__ __launch_bounds__(256) void k_attend_few(const AttnArgs a) {
             for (int u = 0; u < 2; ++u) {
                 const bf16x8 vf = u ? widen(vr[i].z, vr[i].w) : widen(vr[i].x, vr[i].y);
 #pragma unroll
-                for (int p = 0; p < NP; ++p)
+                for (int p = 0; p < PP; ++p)
                     o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[u][p], o[i], 0, 0, 0);
             }
     }
@@ -313,7 +359,7 @@ __global__ __launch_bounds__(256) void k_attend_few(const AttnArgs a) {
 
     // thread: row n2, D / 16 consecutive channels
     const int n2 = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * (D / 16);
-    const int64_t r2 = w.r0 + n2;
+    const int r2 = w.r0 + n2;
     if (r2 >= w.rows) return;
     float M = neg_inf(), sum = 0.f, f[4];
 #pragma unroll
@@ -331,15 +377,12 @@ __global__ __launch_bounds__(256) void k_attend_few(const AttnArgs a) {
         if (f[v] != 0.f)
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) acc[d] += f[v] * so[v][n2][d0 + d];
-    const int64_t tok2 = r2 / a.G, pos2 = w.p0 + tok2;
-    const int head2 = w.h * a.G + (int)(r2 - tok2 * a.G);
-    const int64_t row = (w.first + tok2) * a.Hq + head2;
-    // does this row see a key of this split?
-    const int64_t from = a.window > 0 && pos2 - a.window + 1 > w.k0 ? pos2 - a.window + 1 : w.k0;
-    const bool seen = from <= pos2 && from < w.k1;
+    const int tok2 = r2 / a.G, head2 = w.h * a.G + r2 - tok2 * a.G;
+    const int64_t row = (int64_t)(w.first + tok2) * a.Hq + head2;
+    const bool seen = row_sees(w.p0 + tok2, a.window, w.k0, w.k1);
     if (a.splits == 1) {
         const float inv = row_inverse(sum, seen);
-        E* out = static_cast<E*>(a.out.p) + ((w.first + tok2) * a.out.st + head2 * a.out.sh) + d0;
+        E* out = static_cast<E*>(a.out.p) + ((int64_t)(w.first + tok2) * a.out.st + head2 * a.out.sh) + d0;
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) acc[d] *= inv;
 #pragma unroll
@@ -366,53 +409,40 @@ __global__ __launch_bounds__(256) void k_attend_few(const AttnArgs a) {
 // stands for key 16 ((m / 4) % 2) + 4 (m / 8) + m % 4, so that lane l holds
 // keys 16 half + i: what the second product's steps u = 0, 1 take as k.
 //
-// LDS: keys [64][D] and values [D][64], bf16, 16-byte slots XOR-swizzled by
-// row so that the 16 rows of a read's quarter lie in other banks.
+// LDS: keys [64][D] in matrix-row order and values [D][64], bf16, rows padded by
+// 16 bytes: a read's sixteen consecutive rows then start in other banks (68 and
+// 36 words apart), and every address of a step is one lane's base and a constant.
 // ---------------------------------------------------------------------------
-template <int D>
-__device__ __forceinline__ int key_slot(int token, int slot) {
-    // sixteen rows {16 a + 4 b + i} of a quarter: (token & 7) and bit 4 tell them apart
-    const int f = D == 64 ? ((token >> 1) & 3) | ((token >> 4) & 1) << 2 : (token & 7) | ((token >> 4) & 1) << 3;
-    return token * (2 * D) + ((slot ^ f) << 4);
-}
-__device__ __forceinline__ int value_slot(int d, int slot) { return d * (2 * kTile) + ((slot ^ ((d >> 1) & 7)) << 4); }
-
 template <typename E, int NP, int D, int NW>
 __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttnArgs a) {
     constexpr int NT = 64 * NW, KS = D / 16, DT = D / 32;
     constexpr int CH = (4 * D + NT - 1) / NT;           // 16-byte pieces a thread loads of keys, and of values
-    constexpr int KB = kTile * D * 2, BUF = 2 * KB;     // bytes of the keys, of one buffer
+    constexpr int KP = 2 * D + 16, VP = 2 * kTile + 16; // row pitches in bytes
+    constexpr int KB = kTile * KP, BUF = KB + D * VP;   // bytes of the keys, of one buffer
     __shared__ __align__(16) char lds[2 * BUF];
-    __shared__ float2 scales[2][4];
+    // of each 16 keys: the key scale (with the softmax's), log2 of the value
+    // scale, its reciprocal, and whether it is 0 (or too small for a logarithm)
+    __shared__ float4 scales[2][4];
     const CacheArgs& c = a.c;
     Work w;
     if (!find_work(a, 32 * NW, w)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int col = lane & 31, half = lane >> 5;
-    const int64_t r = w.r0 + 32 * wave + col;
+    const int r = w.r0 + 32 * wave + col;
     const bool valid = r < w.rows;
-    const int64_t tok = valid ? r / a.G : 0;
-    const int head = w.h * a.G + (valid ? (int)(r - tok * a.G) : 0);
-    const int64_t pos = w.p0 + tok;
+    const int tok = valid ? r / a.G : 0;
+    const int head = w.h * a.G + (valid ? r - tok * a.G : 0);
+    const int pos = w.p0 + tok;
 
-    bf16x8 qf[KS][NP];
-    {
-        const E* q = static_cast<const E*>(a.q.p) + ((w.first + tok) * a.q.st + head * a.q.sh);
-#pragma unroll
-        for (int s = 0; s < KS; ++s) load_q<E, NP>(q + 16 * s + 8 * half, valid, qf[s]);
-    }
-    // positions of this wave's rows
-    const int64_t w0 = w.r0 + 32 * wave, w1 = w0 + 32 < w.rows ? w0 + 32 : w.rows;
-    const bool any = w0 < w.rows;
-    const int64_t p_first = w.p0 + w0 / a.G, p_last = w.p0 + (w1 - 1) / a.G;
-
-    // staging: piece i of this thread
-    const size_t page_bytes = (size_t)c.P * D;
+    // staging: piece i of this thread is piece p = tid + i NT of the tile
+    const uint32_t head_bytes = (uint32_t)c.P * D;      // of one page
+    const size_t page_bytes = (size_t)c.Hkv * head_bytes;
+    const int8_t* keys = c.keys + (size_t)w.h * head_bytes;
+    const int8_t* values = c.values + (size_t)w.h * head_bytes;
     uint4 kr[CH], vr[CH];
-    int32_t id_k[CH], id_v[CH];
-    float2 sc = make_float2(0.f, 0.f);
-    int32_t id_s = -1;
-    auto find_pages = [&](int64_t t0) {
+    int id_k[CH], id_v[CH], id_s = -1;
+    float ks_in = 0.f, vs_in = 0.f;
+    auto find_pages = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int p = tid + i * NT;
@@ -421,21 +451,23 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttnArgs a) {
         }
         if (tid < 4) id_s = page_id(c, w.b, t0 + 16 * tid, w.k1);
     };
-    auto load = [&](int64_t t0) {
+    auto load = [&](int t0) {
+        const int in_page = t0 & (c.P - 1);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int p = tid + i * NT;
             if (4 * D % NT != 0 && p >= 4 * D) break;
-            const int64_t key = t0 + p / (D / 16);
-            kr[i] = *reinterpret_cast<const uint4*>(c.keys + ((size_t)(id_k[i] < 0 ? 0 : id_k[i]) * c.Hkv + w.h) * page_bytes +
-                                                    (size_t)(key & (c.P - 1)) * D + 16 * (p % (D / 16)));
-            vr[i] = *reinterpret_cast<const uint4*>(c.values + ((size_t)(id_v[i] < 0 ? 0 : id_v[i]) * c.Hkv + w.h) * page_bytes +
-                                                    (size_t)(p / 4) * c.P + ((t0 + 16 * (p & 3)) & (c.P - 1)));
+            const int key = p / (D / 16), piece = p % (D / 16);
+            kr[i] = *reinterpret_cast<const uint4*>(keys + (id_k[i] < 0 ? 0 : id_k[i]) * page_bytes +
+                                                    (((key & (c.P - 1)) + in_page) * D + 16 * piece));
+            vr[i] = *reinterpret_cast<const uint4*>(values + (id_v[i] < 0 ? 0 : id_v[i]) * page_bytes +
+                                                    ((p / 4) * c.P + ((16 * (p & 3)) & (c.P - 1)) + in_page));
         }
         if (tid < 4) {
             const size_t srow = (size_t)(id_s < 0 ? 0 : id_s) * c.Hkv + w.h;
-            sc = id_s < 0 ? make_float2(__builtin_nanf(""), __builtin_nanf(""))
-                          : make_float2(c.k_scale[srow] * a.scale2, c.v_scale[srow]);
+            ks_in = c.k_scale[srow] * a.scale2;
+            vs_in = c.v_scale[srow];
+            if (id_s < 0) ks_in = vs_in = __builtin_nanf("");
         }
     };
     auto stage = [&](int buf) {
@@ -445,14 +477,37 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttnArgs a) {
         for (int i = 0; i < CH; ++i) {
             const int p = tid + i * NT;
             if (4 * D % NT != 0 && p >= 4 * D) break;
-            const int key = p / (D / 16), kslot = 2 * (p % (D / 16)), d = p / 4, vslot = 2 * (p & 3);
-            *reinterpret_cast<bf16x8*>(kb + key_slot<D>(key, kslot)) = widen(kr[i].x, kr[i].y);
-            *reinterpret_cast<bf16x8*>(kb + key_slot<D>(key, kslot + 1)) = widen(kr[i].z, kr[i].w);
-            *reinterpret_cast<bf16x8*>(vb + value_slot(d, vslot)) = widen(vr[i].x, vr[i].y);
-            *reinterpret_cast<bf16x8*>(vb + value_slot(d, vslot + 1)) = widen(vr[i].z, vr[i].w);
+            const int key = p / (D / 16), piece = p % (D / 16);
+            const int row = (key & 32) | (key & 12) << 1 | (key & 16) >> 2 | (key & 3);
+            char* kt = kb + row * KP + 32 * piece;
+            char* vt = vb + (p / 4) * VP + 32 * (p & 3);
+            *reinterpret_cast<bf16x8*>(kt) = widen(kr[i].x, kr[i].y);
+            *reinterpret_cast<bf16x8*>(kt + 16) = widen(kr[i].z, kr[i].w);
+            *reinterpret_cast<bf16x8*>(vt) = widen(vr[i].x, vr[i].y);
+            *reinterpret_cast<bf16x8*>(vt + 16) = widen(vr[i].z, vr[i].w);
         }
-        if (tid < 4) scales[buf][tid] = sc;
+        if (tid < 4) {
+            const bool none = fabsf(vs_in) < 1.1754944e-38f;
+            scales[buf][tid] = make_float4(ks_in, none ? 0.f : __builtin_amdgcn_logf(vs_in), none ? 1.f : 1.f / vs_in,
+                                           none ? 1.f : 0.f);
+        }
     };
+
+    if (w.k0 < w.k1) {
+        find_pages(w.k0);
+        load(w.k0);
+        find_pages(w.k0 + kTile);
+    }
+    bf16x8 qf[KS][NP];
+    {
+        const E* q = static_cast<const E*>(a.q.p) + ((int64_t)(w.first + tok) * a.q.st + head * a.q.sh);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) load_q<E, NP>(q + 16 * s + 8 * half, valid, a.negate, qf[s]);
+    }
+    // positions of this wave's rows
+    const int w0 = w.r0 + 32 * wave, w1 = w.rows - w0 < 32 ? w.rows : w0 + 32;
+    const bool any = w0 < w.rows;
+    const int p_first = w.p0 + w0 / a.G, p_last = w.p0 + (w1 - 1) / a.G;
 
     f32x16 o[DT];
 #pragma unroll
@@ -460,17 +515,11 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttnArgs a) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
     float m = neg_inf(), l = 0.f;
-    const int key_row = 16 * ((col >> 2) & 1) + 4 * (col >> 3) + (col & 3);
 
-    if (w.k0 < w.k1) {
-        find_pages(w.k0);
-        load(w.k0);
-        find_pages(w.k0 + kTile);
-        stage(0);
-    }
+    if (w.k0 < w.k1) stage(0);
     __syncthreads();
     int buf = 0;
-    for (int64_t t0 = w.k0; t0 < w.k1; t0 += kTile, buf ^= 1) {
+    for (int t0 = w.k0; t0 < w.k1; t0 += kTile, buf ^= 1) {
         const bool more = t0 + kTile < w.k1;
         if (more) {
             load(t0 + kTile);
@@ -478,8 +527,8 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttnArgs a) {
         }
         // some row of this wave sees some key of this step
         if (any && t0 <= p_last && (a.window == 0 || t0 + kTile - 1 > p_first - a.window)) {
-            const char* kb = lds + buf * BUF;
-            const char* vb = kb + KB;
+            const char* kb = lds + buf * BUF + col * KP + 16 * half;
+            const char* vb = lds + buf * BUF + KB + col * VP + 32 * half;
             f32x16 s[2];
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
@@ -487,65 +536,87 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttnArgs a) {
                 for (int j = 0; j < 16; ++j) s[tt][j] = 0.f;
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
-                    const bf16x8 kf = *reinterpret_cast<const bf16x8*>(kb + key_slot<D>(32 * tt + key_row, 2 * k + half));
+                    const bf16x8 kf = *reinterpret_cast<const bf16x8*>(kb + tt * 32 * KP + 32 * k);
 #pragma unroll
                     for (int p = 0; p < NP; ++p)
                         s[tt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[k][p], s[tt], 0, 0, 0);
                 }
             }
-            float vs[2];
+            // the value scale vs goes into the exponent, p vs = 2^(x + log2 vs),
+            // and comes out of the sum of each 16 keys again
+            float4 f[2];
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt) {
-                const float2 f = scales[buf][2 * tt + half];
-                vs[tt] = f.y;
-#pragma unroll
-                for (int j = 0; j < 16; ++j) s[tt][j] *= f.x;
-            }
+            for (int tt = 0; tt < 2; ++tt) f[tt] = scales[buf][2 * tt + half];
             if (t0 + kTile - 1 > p_first || t0 + kTile > w.k1 || (a.window > 0 && t0 <= p_last - a.window)) {
-                const int64_t up = (pos < w.k1 - 1 ? pos : w.k1 - 1) - t0, dn = a.window > 0 ? pos - a.window - t0 : -1;
+                // as in k_attend_few: hidden keys by a select, and no scales
+                // where the row sees none of the lane's sixteen
+                const int up = last_seen(pos, t0, w.k1) - 16 * half, dn = before_seen(pos, t0, a.window) - 16 * half;
 #pragma unroll
-                for (int tt = 0; tt < 2; ++tt)
+                for (int tt = 0; tt < 2; ++tt) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const int key = 32 * tt + 16 * half + j;
-                        if (key > up || key <= dn) s[tt][j] = neg_inf();
+                        const int key = 32 * tt + j;
+                        s[tt][j] = key > up || key <= dn ? neg_inf() : s[tt][j] * f[tt].x;
                     }
+                    f[tt].x = 1.f;
+                    if (32 * tt > up || 32 * tt + 15 <= dn) f[tt] = make_float4(1.f, 0.f, 0.f, 0.f);
+                }
             }
-            float top = neg_inf();
+            float top[2];
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt)
+            for (int tt = 0; tt < 2; ++tt) {
+                top[tt] = s[tt][0];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) top = fmaxf(top, s[tt][j]);
-            top = fmaxf(top, __shfl_xor(top, 32, 64));
-            const float m_new = fmaxf(m, top);
-            const float m_use = m_new == neg_inf() ? 0.f : m_new;
-            const float alpha = __builtin_amdgcn_exp2f(m - m_use);
-            m = m_new;
-            l *= alpha;
+                for (int j = 1; j < 16; ++j) top[tt] = fmaxf(top[tt], s[tt][j]);
+            }
+            float most = fmaxf(top[0] * f[0].x, top[1] * f[1].x);
+            most = fmaxf(most, __shfl_xor(most, 32, 64));
+            if (__any(most > m + kSlack)) {
+                const float to = fmaxf(m, most);
+                const float alpha = __builtin_amdgcn_exp2f(m - (to == neg_inf() ? 0.f : to));
+                m = to;
+                l *= alpha;
 #pragma unroll
-            for (int i = 0; i < DT; ++i) o[i] *= alpha;
+                for (int i = 0; i < DT; ++i) o[i] *= alpha;
+            }
+            const float ref = m == neg_inf() ? 0.f : m;
+            bf16x8 pf[2][2][NP];
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt)
+            for (int tt = 0; tt < 2; ++tt) {
+                const float shift = f[tt].y - ref;
+                float sum = 0.f;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     float pv[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float xe = s[tt][8 * u + e];
-                        const float p = __builtin_amdgcn_exp2f(xe - m_use);
-                        l += p;
-                        pv[e] = xe == neg_inf() ? 0.f : p * vs[tt];
+                        pv[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[tt][8 * u + e], f[tt].x, shift));
+                        sum += pv[e];
                     }
-                    bf16x8 pf[NP];
-                    pieces<NP>(pv, pf);
+                    pieces<NP>(pv, pf[tt][u]);
+                }
+                l += sum * f[tt].z;
+            }
+            if (__any(f[0].w + f[1].w > 0.f)) {
 #pragma unroll
-                    for (int i = 0; i < DT; ++i) {
-                        const bf16x8 vf = *reinterpret_cast<const bf16x8*>(vb + value_slot(32 * i + col, 4 * tt + 2 * half + u));
+                for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
 #pragma unroll
                         for (int p = 0; p < NP; ++p)
-                            o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[p], o[i], 0, 0, 0);
+                            if (f[tt].w > 0.f) pf[tt][u][p] = __builtin_bit_cast(bf16x8, make_uint4(0, 0, 0, 0));
+            }
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < DT; ++i) {
+                        const bf16x8 vf = *reinterpret_cast<const bf16x8*>(vb + i * 32 * VP + 64 * tt + 16 * u);
+#pragma unroll
+                        for (int p = 0; p < NP; ++p)
+                            o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[tt][u][p], o[i], 0, 0, 0);
                     }
-                }
         }
         if (more) stage(buf ^ 1);
         __syncthreads();
@@ -553,12 +624,11 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttnArgs a) {
 
     l += __shfl_xor(l, 32, 64);
     if (!valid) return;
-    const int64_t row = (w.first + tok) * a.Hq + head;
-    const int64_t from = a.window > 0 && pos - a.window + 1 > w.k0 ? pos - a.window + 1 : w.k0;
-    const bool seen = from <= pos && from < w.k1;
+    const int64_t row = (int64_t)(w.first + tok) * a.Hq + head;
+    const bool seen = row_sees(pos, a.window, w.k0, w.k1);
     const float inv = a.splits == 1 ? row_inverse(l, seen) : 1.f;
     const int64_t part = row * a.splits + w.split;
-    E* out = static_cast<E*>(a.out.p) + ((w.first + tok) * a.out.st + head * a.out.sh);
+    E* out = static_cast<E*>(a.out.p) + ((int64_t)(w.first + tok) * a.out.st + head * a.out.sh);
 #pragma unroll
     for (int i = 0; i < DT; ++i)
 #pragma unroll
@@ -574,18 +644,18 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Joins the splits of a row: a workgroup per row, wave v takes splits v, v + 4,
-// ..., lanes the channels; the waves meet in LDS (a fixed order).
-// A sum of -1 marks a split whose keys were seen but all scored -inf. Tokens of
-// no sequence, or beyond its first max_new, have no parts and are left alone.
+// Joins the splits of a row: a workgroup per row; a thread takes four channels
+// of every SG-th split (four loads in flight), the SG sums meet in LDS in a
+// fixed order. A sum of -1 marks a split whose keys were seen but all scored
+// -inf. Tokens of no sequence, or beyond its first max_new, have no parts and
+// are left alone.
 // ---------------------------------------------------------------------------
 template <typename E, int D>
 __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a) {
-    constexpr int PL = D / 64;
-    __shared__ float so[4][D];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t row = blockIdx.x;
-    const int64_t t = row / a.Hq;
+    constexpr int CG = D / 4, SG = 256 / CG;
+    __shared__ float4 so[SG][CG];
+    const int lane = threadIdx.x & 63;
+    const int row = blockIdx.x, t = row / a.Hq;
     if (a.c.cu) {
         int lo = 0, hi = a.c.B;             // cu[lo] <= t < cu[hi], where t is in a sequence
         while (hi - lo > 1) {
@@ -593,10 +663,10 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a) {
             if (a.c.cu[mid] <= t) lo = mid;
             else hi = mid;
         }
-        const int64_t first = a.c.cu[lo], last = a.c.cu[hi];
+        const int first = a.c.cu[lo], last = a.c.cu[hi];
         if (first < 0 || last > a.c.T || t < first || t >= last || t - first >= a.c.max_new) return;
     }
-    const float2* ml = a.part_ml + row * a.splits;
+    const float2* ml = a.part_ml + (int64_t)row * a.splits;
     float M = neg_inf();
     for (int s = lane; s < a.splits; s += 64) M = fmaxf(M, ml[s].x);
 #pragma unroll
@@ -610,25 +680,50 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a) {
     }
     sum = wave_sum(sum);
     marks = wave_sum(marks);
-    float acc[PL];
+    const int cg = threadIdx.x % CG, sg = threadIdx.x / CG;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4* o = reinterpret_cast<const float4*>(a.part_o + (int64_t)row * a.splits * D) + cg;
+    for (int s = sg; s < a.splits; s += 4 * SG) {
+        float f[4];
+        float4 v[4];
 #pragma unroll
-    for (int i = 0; i < PL; ++i) acc[i] = 0.f;
-    for (int s = wave; s < a.splits; s += 4) {
-        const float2 p = ml[s];
-        const float f = part_factor(p.x, p.y, M);
-        if (f == 0.f) continue;
-        const float* o = a.part_o + (row * a.splits + s) * D + lane;
+        for (int i = 0; i < 4; ++i) {
+            const int si = s + i * SG;
+            f[i] = 0.f;
+            if (si < a.splits) {
+                const float2 p = ml[si];
+                f[i] = part_factor(p.x, p.y, M);
+            }
+            // a split that counts nothing may never have been written
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (f[i] != 0.f) v[i] = o[(int64_t)si * CG];
+        }
 #pragma unroll
-        for (int i = 0; i < PL; ++i) acc[i] += f * o[64 * i];
+        for (int i = 0; i < 4; ++i) {
+            acc.x += f[i] * v[i].x;
+            acc.y += f[i] * v[i].y;
+            acc.z += f[i] * v[i].z;
+            acc.w += f[i] * v[i].w;
+        }
     }
-#pragma unroll
-    for (int i = 0; i < PL; ++i) so[wave][lane + 64 * i] = acc[i];
+    so[sg][cg] = acc;
     __syncthreads();
-    const int h = (int)(row - t * a.Hq);
+    const int h = row - t * a.Hq;
     const float inv = row_inverse(sum, marks != 0.f);
-    E* out = static_cast<E*>(a.out.p) + (t * a.out.st + h * a.out.sh);
-    for (int d = threadIdx.x; d < D; d += 256)
-        Elem<E>::store1(out + d, (so[0][d] + so[1][d] + so[2][d] + so[3][d]) * inv);
+    if (threadIdx.x < CG) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < SG; ++i) {
+            const float4 p = so[i][threadIdx.x];
+            v[0] += p.x;
+            v[1] += p.y;
+            v[2] += p.z;
+            v[3] += p.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] *= inv;
+        store4(static_cast<E*>(a.out.p) + ((int64_t)t * a.out.st + h * a.out.sh) + 4 * threadIdx.x, v);
+    }
     if (a.lse && threadIdx.x == 0) a.lse[row] = row_lse(M, sum, marks != 0.f);
 }
 
@@ -636,7 +731,7 @@ template <typename E, int NP, int D>
 hipError_t launch(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
     const dim3 grid((unsigned)plan.blocks);
     if (plan.few) {
-        k_attend_few<E, NP, D><<<grid, 256, 0, s>>>(a);
+        k_attend_few<E, NP, NP == 1 ? 2 : 3, D><<<grid, 256, 0, s>>>(a);
     } else {
         if constexpr (D <= 128 && NP == 1) {
             if (plan.waves == 8) k_attend_rows<E, NP, D, 8><<<grid, 512, 0, s>>>(a);
@@ -672,9 +767,10 @@ hipError_t launch_cache_attention(const CacheArgs& c, const AttnPlan& plan, cons
     a.G = Hq / c.Hkv;
     a.window = window;
     a.splits = plan.splits;
-    a.chunk = plan.chunk;
-    a.row_tiles = plan.row_tiles;
-    a.scale2 = scale * kLog2e;
+    a.chunk = (int)plan.chunk;
+    a.row_tiles = (int)plan.row_tiles;
+    a.scale2 = fabsf(scale) * kLog2e;
+    a.negate = scale < 0.f;
     a.lse = lse;
     if (plan.splits > 1) {
         a.part_ml = static_cast<float2*>(ws);

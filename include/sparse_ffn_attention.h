@@ -96,7 +96,7 @@ sffn_status_t qk_norm_rope_backward(const sffn_rope_config_t* cfg, const sffn_he
  *   keys     int8 [n_pages, kv_heads, page, head_dim]
  *   values   int8 [n_pages, kv_heads, head_dim, page] (a channel's tokens are
  *            contiguous: the order the matrix cores take them in)
- *   k_scale, v_scale  fp32 [n_pages, kv_heads]
+ *   k_scale, v_scale  fp32 [n_pages, kv_heads], not negative
  * page 16, 32, 64 or 128; head_dim 64, 128 or 256; pointers 16-byte aligned. */
 typedef struct {
     int8_t* keys;
@@ -113,7 +113,8 @@ typedef struct {
  * the pages block_table[b][0 ..]; the call's tokens cu[b] .. cu[b + 1] - 1 are
  * its last ones (their keys and values included in kv_lens). With cu NULL
  * token b is the last token of sequence b.
- *   block_table [n_seqs] rows of max_pages int32 (row stride table_stride)
+ *   block_table [n_seqs] rows of max_pages int32 (row stride table_stride);
+ *               max_pages * page at most 2^30, T at most 2^28
  *   kv_lens [n_seqs] int32, cu [n_seqs + 1] int32 ascending from 0, or NULL
  *   max_new   >= every cu[b + 1] - cu[b]; tokens beyond it are not processed
  *   max_kv    about the largest kv_lens[b]: splits the work, never the result */
