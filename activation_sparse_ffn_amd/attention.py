@@ -15,6 +15,7 @@ the library's HIP kernels, asynchronously on torch's current stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional
 
@@ -78,10 +79,28 @@ def declare(lib):
 
 # ---------------------------------------------------------------------------
 # argument checks
+#
+# A call on one token is bound by what the host does before the launch (about 3
+# us of it are the launch), so the checks that pass are written to be short; the
+# messages are made only for those that do not.
 # ---------------------------------------------------------------------------
 
 def _heads(t: Optional[torch.Tensor], name: str, shape=None, dtype=None, device=None):
     """A [T, heads, head_dim] view on the GPU as the library takes it."""
+    if shape is None or type(t) is not torch.Tensor or t.shape != shape or t.dtype is not dtype or t.device != device \
+            or dtype not in _DTYPES or not t.is_cuda:
+        _check_heads(t, name, shape, dtype, device)
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if sd != 1 and D > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    # a dimension of one element may carry any stride
+    if H == 1:
+        sh = D
+    return _Heads(t.data_ptr(), st if T > 1 else sh * H, sh)
+
+
+def _check_heads(t, name, shape, dtype, device):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 3 or (shape is not None and t.shape != shape):
@@ -91,19 +110,20 @@ def _heads(t: Optional[torch.Tensor], name: str, shape=None, dtype=None, device=
         raise ValueError(f"{name} must be {dtype or 'bfloat16 or float32'} (got {t.dtype})")
     if not t.is_cuda or (device is not None and t.device != device):
         raise ValueError(f"{name} must be on {device or 'the GPU'} (got {t.device})")
-    T, H, D = t.shape
-    st, sh, sd = t.stride()
-    if sd != 1 and D > 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    # a dimension of one element may carry any stride
-    sh = sh if H > 1 else D
-    return _Heads(t.data_ptr(), st if T > 1 else sh * H, sh)
 
 
-def _vector(t: Optional[torch.Tensor], name: str, shape, dtype, device):
-    if t is not None:
+def _new_heads(t: torch.Tensor):
+    """A contiguous [T, heads, head_dim] tensor made here."""
+    _, H, D = t.shape
+    return _Heads(t.data_ptr(), H * D, D)
+
+
+def _address(t: torch.Tensor, name: str, shape, dtype, device) -> int:
+    """The address of a contiguous tensor (shape None: any)."""
+    if type(t) is not torch.Tensor or t.dtype is not dtype or t.device != device or not t.is_contiguous() \
+            or (shape is not None and t.shape != shape):
         _need_buffer(t, name, shape, dtype, device)
-    return _ptr(t)
+    return t.data_ptr()
 
 
 # ---------------------------------------------------------------------------
@@ -147,35 +167,44 @@ def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, scaling: Optio
     return (torch.cat([angle.cos(), angle.sin()], 1) * amplitude).float().to(device)
 
 
+@functools.lru_cache(maxsize=256)
+def _rope_config(n_q, n_k, dim, rot, max_pos, dtype, layout, norm, eps):
+    """The library's config, a constant of its arguments."""
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError("layout must be 'half' or 'interleaved'")
+    return _RopeConfig(n_q, n_k, dim, rot, max_pos, _DTYPES[dtype], ROPE_LAYOUTS[layout], norm, eps)
+
+
 def _rope_call(x, other, positions, table, q_weight, k_weight, norm, eps, layout):
     """The config and shared pointers of a call on q (or its gradient) `x` and
     k `other` (or None)."""
     T, n_q, D = x.shape
-    if layout not in ROPE_LAYOUTS:
-        raise ValueError("layout must be 'half' or 'interleaved'")
+    dev, dtype = x.device, x.dtype
+    wq = None if q_weight is None else _address(q_weight, "q_weight", (D,), dtype, dev)
+    wk = None if k_weight is None else _address(k_weight, "k_weight", (D,), dtype, dev)
+    weighted = wq is not None or wk is not None
     if norm is None:
-        norm = q_weight is not None or k_weight is not None
-    if not norm and (q_weight is not None or k_weight is not None):
+        norm = weighted
+    elif weighted and not norm:
         raise ValueError("weights are given but norm is False")
-    dev = x.device
-    rot = 0
+    rot = max_pos = 0
+    pos = tab = None
     if table is not None:
         if table.dim() != 2:
             raise ValueError("table must be [max_pos, rot_dim] float32")
-        rot = table.shape[1]
-        _need_buffer(table, "table", None, torch.float32, dev)
-        _need_buffer(positions, "positions", (T,), torch.int32, dev)
-    cfg = _RopeConfig(n_q, 0 if other is None else other.shape[1], D, rot, table.shape[0] if rot else 0,
-                      _DTYPES[x.dtype], ROPE_LAYOUTS[layout], int(norm), eps)
-    return (cfg, _ptr(positions) if rot else None, _ptr(table) if rot else None,
-            _vector(q_weight, "q_weight", (D,), x.dtype, dev), _vector(k_weight, "k_weight", (D,), x.dtype, dev))
+        max_pos, rot = table.shape
+        tab = _address(table, "table", None, torch.float32, dev)
+        pos = _address(positions, "positions", (T,), torch.int32, dev)
+    cfg = _rope_config(n_q, 0 if other is None else other.shape[1], D, rot, max_pos, dtype, layout, int(norm), eps)
+    return cfg, pos, tab, wq, wk
 
 
 def _like_k(k, q):
     """The shape k must have: q's with its own count of heads."""
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be [T, heads, head_dim]")
-    return torch.Size((q.shape[0], k.shape[1], q.shape[2]))
+    T, _, D = q.shape
+    return (T, k.shape[1], D)
 
 
 def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
@@ -193,15 +222,22 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional
     outside the table gives NaN rows."""
     lib = load_library()
     hq = _heads(q, "q")
-    hk = None if k is None else _heads(k, "k", _like_k(k, q), q.dtype, q.device)
+    dtype, dev = q.dtype, q.device
+    hk = None if k is None else _heads(k, "k", _like_k(k, q), dtype, dev)
     cfg, pos, tab, wq, wk = _rope_call(q, k, positions, table, q_weight, k_weight, norm, eps, layout)
+    hko = None
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k_out is None and k is not None:
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    ho = _heads(q_out, "q_out", q.shape, q.dtype, q.device)
-    hko = None if k is None else _heads(k_out, "k_out", k.shape, q.dtype, q.device)
-    _check(lib, lib.qk_norm_rope(cfg, hq, hk, pos, tab, wq, wk, q.shape[0], ho, hko, _stream(q.device)))
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        ho = _new_heads(q_out)
+    else:
+        ho = _heads(q_out, "q_out", q.shape, dtype, dev)
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+            hko = _new_heads(k_out)
+        else:
+            hko = _heads(k_out, "k_out", k.shape, dtype, dev)
+    _check(lib, lib.qk_norm_rope(cfg, hq, hk, pos, tab, wq, wk, q.shape[0], ho, hko, _stream(dev)))
     return q_out, k_out
 
 
@@ -216,26 +252,31 @@ def qk_norm_rope_backward(q: Optional[torch.Tensor], k: Optional[torch.Tensor], 
     given)."""
     lib = load_library()
     hg = _heads(g_q, "g_q")
-    hgk = None if g_k is None else _heads(g_k, "g_k", _like_k(g_k, g_q), g_q.dtype, g_q.device)
+    T, _, D = g_q.shape
+    dtype, dev = g_q.dtype, g_q.device
+    hgk = None if g_k is None else _heads(g_k, "g_k", _like_k(g_k, g_q), dtype, dev)
     cfg, pos, tab, wq, wk = _rope_call(g_q, g_k, positions, table, q_weight, k_weight, norm, eps, layout)
-    T, dev, hq, hk = g_q.shape[0], g_q.device, None, None
+    hq = hk = hok = gk = ws = gwq = gwk = None
+    need = 0
     if cfg.norm:
-        hq = _heads(q, "q", g_q.shape, g_q.dtype, dev)
+        hq = _heads(q, "q", g_q.shape, dtype, dev)
         if g_k is not None:
-            hk = _heads(k, "k", g_k.shape, g_q.dtype, dev)
-    out = {"q": torch.empty(g_q.shape, dtype=g_q.dtype, device=dev),
-           "k": None if g_k is None else torch.empty(g_k.shape, dtype=g_q.dtype, device=dev),
-           "q_weight": None if q_weight is None else torch.empty(cfg.head_dim, dtype=torch.float32, device=dev),
-           "k_weight": None if k_weight is None else torch.empty(cfg.head_dim, dtype=torch.float32, device=dev)}
-    ws, need = None, 0
-    if q_weight is not None or k_weight is not None:
+            hk = _heads(k, "k", g_k.shape, dtype, dev)
+    gq = torch.empty_like(g_q, memory_format=torch.contiguous_format)
+    if g_k is not None:
+        gk = torch.empty_like(g_k, memory_format=torch.contiguous_format)
+        hok = _new_heads(gk)
+    if wq is not None:
+        gwq = g_q.new_empty(D, dtype=torch.float32)
+    if wk is not None:
+        gwk = g_q.new_empty(D, dtype=torch.float32)
+    if gwq is not None or gwk is not None:
         need = lib.qk_norm_rope_backward_workspace_size(cfg, T)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        ws = g_q.new_empty(need, dtype=torch.uint8) if need else None
     _check(lib, lib.qk_norm_rope_backward(
-        cfg, hq, hk, hg, hgk, pos, tab, wq, wk, T, _heads(out["q"], "g_q"),
-        None if g_k is None else _heads(out["k"], "g_k"), _ptr(out["q_weight"]), _ptr(out["k_weight"]), _ptr(ws),
-        need, _stream(dev)))
-    return out
+        cfg, hq, hk, hg, hgk, pos, tab, wq, wk, T, _new_heads(gq), hok, _ptr(gwq), _ptr(gwk), _ptr(ws), need,
+        _stream(dev)))
+    return {"q": gq, "k": gk, "q_weight": gwq, "k_weight": gwk}
 
 
 # ---------------------------------------------------------------------------
@@ -256,13 +297,12 @@ class KVCache:
             raise ValueError("keys must be [pages, kv_heads, page, head_dim] on the GPU")
         n, h, p, d = keys.shape
         dev = keys.device
-        _need_buffer(keys, "keys", None, torch.int8, dev)
-        _need_buffer(values, "values", (n, h, d, p), torch.int8, dev)
-        _need_buffer(k_scale, "k_scale", (n, h), torch.float32, dev)
-        _need_buffer(v_scale, "v_scale", (n, h), torch.float32, dev)
+        self._c = _Cache(_address(keys, "keys", None, torch.int8, dev),
+                         _address(values, "values", (n, h, d, p), torch.int8, dev),
+                         _address(k_scale, "k_scale", (n, h), torch.float32, dev),
+                         _address(v_scale, "v_scale", (n, h), torch.float32, dev), n, h, p, d)
         self.keys, self.values, self.k_scale, self.v_scale = keys, values, k_scale, v_scale
         self.device, self.kv_heads, self.page, self.head_dim = dev, h, p, d
-        self._c = _Cache(keys.data_ptr(), values.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n, h, p, d)
 
     @classmethod
     def empty(cls, n_pages: int, kv_heads: int, head_dim: int, page: int = 64, device="cuda") -> "KVCache":
@@ -290,18 +330,16 @@ class CacheBatch:
             raise ValueError("block_table must be [B, max_pages] on the GPU")
         B, pages = block_table.shape
         dev = block_table.device
-        _need_buffer(block_table, "block_table", None, torch.int32, dev)
-        _need_buffer(kv_lens, "kv_lens", (B,), torch.int32, dev)
-        if cu is not None:
-            _need_buffer(cu, "cu", (B + 1,), torch.int32, dev)
+        self._c = _Batch(_address(block_table, "block_table", None, torch.int32, dev), pages,
+                         _address(kv_lens, "kv_lens", (B,), torch.int32, dev),
+                         None if cu is None else _address(cu, "cu", (B + 1,), torch.int32, dev),
+                         B, pages, max_new, max_kv)
         self.block_table, self.kv_lens, self.cu, self.device = block_table, kv_lens, cu, dev
         self.max_kv, self.max_new = max_kv, max_new
-        self._c = _Batch(block_table.data_ptr(), pages, kv_lens.data_ptr(), None if cu is None else cu.data_ptr(),
-                         B, pages, max_new, max_kv)
 
 
 def _same_device(cache: KVCache, batch: CacheBatch):
-    if cache.device != batch.device:
+    if cache.device is not batch.device and cache.device != batch.device:
         raise ValueError(f"the cache is on {cache.device}, the batch on {batch.device}")
 
 
@@ -312,10 +350,11 @@ def kv_cache_append(cache: KVCache, batch: CacheBatch, k: torch.Tensor, v: torch
     makes the scale of its page and head NaN."""
     lib = load_library()
     _same_device(cache, batch)
-    shape = torch.Size((k.shape[0], cache.kv_heads, cache.head_dim))
-    hk = _heads(k, "k", shape, None, cache.device)
-    hv = _heads(v, "v", shape, k.dtype, cache.device)
-    _check(lib, lib.kv_cache_append(cache._c, batch._c, hk, hv, _DTYPES[k.dtype], k.shape[0], _stream(cache.device)))
+    T, dtype = k.shape[0], k.dtype
+    shape = (T, cache.kv_heads, cache.head_dim)
+    hk = _heads(k, "k", shape, dtype, cache.device)
+    hv = _heads(v, "v", shape, dtype, cache.device)
+    _check(lib, lib.kv_cache_append(cache._c, batch._c, hk, hv, _DTYPES[dtype], T, _stream(cache.device)))
 
 
 def kv_cache_read(cache: KVCache, batch: CacheBatch, total: int, dtype: torch.dtype = torch.bfloat16,
@@ -326,9 +365,9 @@ def kv_cache_read(cache: KVCache, batch: CacheBatch, total: int, dtype: torch.dt
     _same_device(cache, batch)
     if dtype not in _DTYPES:
         raise ValueError(f"dtype must be bfloat16 or float32 (got {dtype})")
-    shape = torch.Size((total, cache.kv_heads, cache.head_dim))
-    k = torch.empty(shape, dtype=dtype, device=cache.device) if k is None else k
-    v = torch.empty(shape, dtype=dtype, device=cache.device) if v is None else v
+    shape = (total, cache.kv_heads, cache.head_dim)
+    k = cache.keys.new_empty(shape, dtype=dtype) if k is None else k
+    v = cache.keys.new_empty(shape, dtype=dtype) if v is None else v
     hk, hv = _heads(k, "k", shape, dtype, cache.device), _heads(v, "v", shape, dtype, cache.device)
     _check(lib, lib.kv_cache_read(cache._c, batch._c, hk, hv, _DTYPES[dtype], total, _stream(cache.device)))
     return k, v
@@ -350,13 +389,15 @@ def cache_attention(cache: KVCache, batch: CacheBatch, q: torch.Tensor, scale: O
     if D != cache.head_dim:
         raise ValueError(f"q has heads of {D}, the cache of {cache.head_dim}")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    ho = _heads(out, "out", q.shape, q.dtype, cache.device)
-    lse = torch.empty((T, heads), dtype=torch.float32, device=q.device) if return_lse else None
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        ho = _new_heads(out)
+    else:
+        ho = _heads(out, "out", q.shape, q.dtype, cache.device)
+    lse = q.new_empty((T, heads), dtype=torch.float32) if return_lse else None
     dt = _DTYPES[q.dtype]
     if workspace is None:
         need = lib.cache_attention_workspace_size(cache._c, batch._c, heads, dt, window, T)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        workspace = q.new_empty(need, dtype=torch.uint8) if need else None
     else:
         _need_buffer(workspace, "workspace", None, torch.uint8, cache.device)
         need = workspace.numel()
