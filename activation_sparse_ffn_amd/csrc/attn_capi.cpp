@@ -160,7 +160,8 @@ sffn_status_t check_cache_pointers(const sffn_kv_cache_t* c, const sffn_kv_batch
         if (!ptrs[i]) return fail(SFFN_ERR_INVALID_ARG, "%s is null", names[i]);
         if (!aligned16(ptrs[i])) return fail(SFFN_ERR_INVALID_ARG, "%s is not 16-byte aligned", names[i]);
     }
-    if (!b->kv_lens || (!b->block_table && b->max_pages > 0))
+    if (b->max_pages < 1) return fail(SFFN_ERR_INVALID_ARG, "max_pages must be positive (got %d)", b->max_pages);
+    if (!b->kv_lens || !b->block_table)
         return fail(SFFN_ERR_INVALID_ARG, "block_table and kv_lens must not be null");
     for (const void* p : {(const void*)b->block_table, (const void*)b->kv_lens, (const void*)b->cu})
         if (reinterpret_cast<uintptr_t>(p) % 4 != 0)

@@ -95,13 +95,26 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int tile_rows, Work
     return true;
 }
 
-// Page id of the 16 tokens from `pos` on (pos a multiple of 16); -1 where none
-// of them is below `end` or the table names no page of the pool.
-__device__ __forceinline__ int page_id(const CacheArgs& c, int b, int pos, int end) {
+// The table's entry for the page of position `pos` (the last one behind the
+// table's end). It is loaded a step before it is used and checked only then, so
+// that nothing waits for it: known_page says whether it names a page of the
+// pool, page_in one that is safe to read in any case (a row that sees a key of
+// an unknown page gets its NaN from the scales).
+__device__ __forceinline__ uint32_t page_entry(const CacheArgs& c, const int32_t* row, int pos) {
     const int idx = pos >> c.shift;
-    if (pos >= end || idx >= c.max_pages) return -1;
-    const int id = c.table[(int64_t)b * c.table_stride + idx];
-    return id >= 0 && id < (int)c.n_pages ? id : -1;
+    return (uint32_t)row[idx < c.max_pages ? idx : c.max_pages - 1];
+}
+__device__ __forceinline__ bool known_page(const CacheArgs& c, uint32_t entry, int pos) {
+    return entry < (uint32_t)c.n_pages && (pos >> c.shift) < c.max_pages;
+}
+__device__ __forceinline__ uint32_t page_in(const CacheArgs& c, uint32_t entry) {
+    return entry < (uint32_t)c.n_pages ? entry : (uint32_t)c.n_pages - 1;
+}
+
+// Larger of the two halves' values, in every lane.
+__device__ __forceinline__ float max_halves(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 // Whether the row at position p sees a key of [k0, k1).
@@ -236,13 +249,14 @@ __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few
     const int pos = w.p0 + tok;
 
     const uint32_t head_bytes = (uint32_t)c.P * D;      // of one page
-    const size_t page_bytes = (size_t)c.Hkv * head_bytes;
+    const uint32_t page_bytes = c.Hkv * head_bytes;
+    const int32_t* table = c.table + (int64_t)w.b * c.table_stride;
     const int8_t* keys = c.keys + (size_t)w.h * head_bytes + (((16 * gk) & (c.P - 1)) + (n & 3)) * D + 16 * g;
     const int8_t* values = c.values + (size_t)w.h * head_bytes + n * c.P + ((16 * g) & (c.P - 1));
     const float *k_scale = c.k_scale + w.h, *v_scale = c.v_scale + w.h;
     uint4 kr[4][KC];
-    auto load_keys = [&](int id, int t0) {
-        const int8_t* p = keys + (id < 0 ? 0 : id) * page_bytes + (t0 & (c.P - 1)) * D;
+    auto load_keys = [&](uint32_t entry, int t0) {
+        const int8_t* p = keys + (uint64_t)page_in(c, entry) * page_bytes + (t0 & (c.P - 1)) * D;
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -250,8 +264,8 @@ __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few
     };
 
     int t0 = w.k0 + kTile * wave;
-    int id_k = page_id(c, w.b, t0 + 16 * gk, w.k1), id_v = page_id(c, w.b, t0 + 16 * g, w.k1);
-    if (t0 < w.k1) load_keys(id_k, t0);
+    uint32_t entry_k = page_entry(c, table, t0 + 16 * gk), entry_v = page_entry(c, table, t0 + 16 * g);
+    if (t0 < w.k1) load_keys(entry_k, t0);
 
     bf16x8 qf[KC][2][NP];
     {
@@ -271,15 +285,15 @@ __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few
     for (; t0 < w.k1; t0 += 4 * kTile) {
         // values and scales of this step, page ids of the next
         uint4 vr[DT];
-        const size_t idv = id_v < 0 ? 0 : id_v;
-        const int8_t* vp = values + idv * page_bytes + (t0 & (c.P - 1));
+        const uint32_t page = page_in(c, entry_v);
+        const int8_t* vp = values + (uint64_t)page * page_bytes + (t0 & (c.P - 1));
 #pragma unroll
         for (int i = 0; i < DT; ++i) vr[i] = *reinterpret_cast<const uint4*>(vp + 16 * i * c.P);
-        float ks = k_scale[idv * c.Hkv] * a.scale2, vs = v_scale[idv * c.Hkv];
-        if (id_v < 0) ks = vs = __builtin_nanf("");
+        float ks = k_scale[(size_t)page * c.Hkv], vs = v_scale[(size_t)page * c.Hkv];
+        const bool known = known_page(c, entry_v, t0 + 16 * g);
         const int tn = t0 + 4 * kTile;
-        id_k = page_id(c, w.b, tn + 16 * gk, w.k1);
-        id_v = page_id(c, w.b, tn + 16 * g, w.k1);
+        entry_k = page_entry(c, table, tn + 16 * gk);
+        entry_v = page_entry(c, table, tn + 16 * g);
 
         f32x4 s[4];
 #pragma unroll
@@ -295,8 +309,10 @@ __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few
                         s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[cc][u][p], s[t], 0, 0, 0);
                 }
         }
-        if (tn < w.k1) load_keys(id_k, tn);
+        if (tn < w.k1) load_keys(entry_k, tn);
 
+        ks = known ? ks * a.scale2 : __builtin_nanf("");
+        vs = known ? vs : __builtin_nanf("");
         float x[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] = s[e >> 2][e & 3] * ks;
@@ -314,7 +330,7 @@ __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few
 #pragma unroll
         for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
         top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        top = max_halves(top);
         if (__any(top > m + kSlack)) {
             const float to = fmaxf(m, top);
             const float alpha = __builtin_amdgcn_exp2f(m - (to == neg_inf() ? 0.f : to));
@@ -398,10 +414,19 @@ __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few
 
 // ---------------------------------------------------------------------------
 // Many rows (chunks of a prompt): NW waves of 32 rows each share 64-key steps,
-// widened to bf16 once for all of them on the way into LDS (double-buffered:
-// the next step's loads are in flight while this one is computed, one barrier
-// a step). Rows run over (token, head of the group), so every head that shares
-// the keys shares the tile.
+// widened to bf16 once for all of them on the way into LDS. Rows run over
+// (token, head of the group), so every head that shares the keys shares the tile.
+//
+// A step of a wave is two phases of about equal length: M(t), the matrix
+// products O += P(t - 1) V(t - 1) and S = K(t) Q, and V(t), the softmax of S
+// and this thread's share of widening later tiles. With eight waves the second
+// four (the second wave of every SIMD) run one phase behind, so that one wave of
+// a SIMD keeps the matrix cores busy while the other computes weights; barriers
+// between phases hold them there. In phase order: K(t) is read in phases 2t and
+// 2t + 1, V(t) in 2t + 2 and 2t + 3, the scales of t in 2t + 1 and 2t + 2; the
+// first four waves write their half of K(t + 1) and V(t) in phase 2t + 1, the
+// others theirs of K(t + 2) and V(t + 1) in phase 2t + 2: always after the last
+// read of what the (double) buffer held and before its first use.
 //
 // v_mfma_f32_32x32x16_bf16: lane l holds operand row or column l % 32, k = 8
 // (l / 32) .. + 7, and of the result column l % 32, rows 8 (i / 4) + 4 (l / 32)
@@ -414,7 +439,7 @@ __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few
 // 36 words apart), and every address of a step is one lane's base and a constant.
 // ---------------------------------------------------------------------------
 template <typename E, int NP, int D, int NW>
-__global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttnArgs a) {
+__global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) void k_attend_rows(const AttnArgs a) {
     constexpr int NT = 64 * NW, KS = D / 16, DT = D / 32;
     constexpr int CH = (4 * D + NT - 1) / NT;           // 16-byte pieces a thread loads of keys, and of values
     constexpr int KP = 2 * D + 16, VP = 2 * kTile + 16; // row pitches in bytes
@@ -436,67 +461,91 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttnArgs a) {
 
     // staging: piece i of this thread is piece p = tid + i NT of the tile
     const uint32_t head_bytes = (uint32_t)c.P * D;      // of one page
-    const size_t page_bytes = (size_t)c.Hkv * head_bytes;
+    const uint32_t page_bytes = c.Hkv * head_bytes;
+    const int32_t* table = c.table + (int64_t)w.b * c.table_stride;
     const int8_t* keys = c.keys + (size_t)w.h * head_bytes;
     const int8_t* values = c.values + (size_t)w.h * head_bytes;
     uint4 kr[CH], vr[CH];
-    int id_k[CH], id_v[CH], id_s = -1;
+    uint32_t entry_k[CH], entry_v[CH], entry_s = 0;
     float ks_in = 0.f, vs_in = 0.f;
-    auto find_pages = [&](int t0) {
+    bool known = false;
+    // t0: first key of the tile (tiles past the last one load what is never used)
+    auto key_pages = [&](int t0) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) entry_k[i] = page_entry(c, table, t0 + ((tid + i * NT) / (D / 16) & 48));
+        if (tid < 4) entry_s = page_entry(c, table, t0 + 16 * tid);
+    };
+    auto value_pages = [&](int t0) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) entry_v[i] = page_entry(c, table, t0 + 16 * ((tid + i * NT) & 3));
+    };
+    auto load_keys = [&](int t0) {
+        const int in_page = t0 & (c.P - 1);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            const int p = tid + i * NT;
-            id_k[i] = page_id(c, w.b, t0 + (p / (D / 16) & 48), w.k1);
-            id_v[i] = page_id(c, w.b, t0 + 16 * (p & 3), w.k1);
+            const int p = tid + i * NT, key = p / (D / 16), piece = p % (D / 16);
+            if (4 * D % NT != 0 && p >= 4 * D) break;
+            kr[i] = *reinterpret_cast<const uint4*>(keys + (uint64_t)page_in(c, entry_k[i]) * page_bytes +
+                                                    (uint32_t)(((key & (c.P - 1)) + in_page) * D + 16 * piece));
         }
-        if (tid < 4) id_s = page_id(c, w.b, t0 + 16 * tid, w.k1);
+        if (tid < 4) {
+            const size_t srow = (size_t)page_in(c, entry_s) * c.Hkv + w.h;
+            ks_in = c.k_scale[srow];
+            vs_in = c.v_scale[srow];
+            known = known_page(c, entry_s, t0 + 16 * tid);
+        }
     };
-    auto load = [&](int t0) {
+    auto load_values = [&](int t0) {
         const int in_page = t0 & (c.P - 1);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int p = tid + i * NT;
             if (4 * D % NT != 0 && p >= 4 * D) break;
-            const int key = p / (D / 16), piece = p % (D / 16);
-            kr[i] = *reinterpret_cast<const uint4*>(keys + (id_k[i] < 0 ? 0 : id_k[i]) * page_bytes +
-                                                    (((key & (c.P - 1)) + in_page) * D + 16 * piece));
-            vr[i] = *reinterpret_cast<const uint4*>(values + (id_v[i] < 0 ? 0 : id_v[i]) * page_bytes +
-                                                    ((p / 4) * c.P + ((16 * (p & 3)) & (c.P - 1)) + in_page));
-        }
-        if (tid < 4) {
-            const size_t srow = (size_t)(id_s < 0 ? 0 : id_s) * c.Hkv + w.h;
-            ks_in = c.k_scale[srow] * a.scale2;
-            vs_in = c.v_scale[srow];
-            if (id_s < 0) ks_in = vs_in = __builtin_nanf("");
+            vr[i] = *reinterpret_cast<const uint4*>(values + (uint64_t)page_in(c, entry_v[i]) * page_bytes +
+                                                    (uint32_t)((p / 4) * c.P + ((16 * (p & 3)) & (c.P - 1)) + in_page));
         }
     };
-    auto stage = [&](int buf) {
-        char* kb = lds + buf * BUF;
-        char* vb = kb + KB;
+    auto stage_keys = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const int p = tid + i * NT, key = p / (D / 16), piece = p % (D / 16);
+            if (4 * D % NT != 0 && p >= 4 * D) break;
+            const int row = (key & 32) | (key & 12) << 1 | (key & 16) >> 2 | (key & 3);
+            char* to = lds + buf * BUF + row * KP + 32 * piece;
+            *reinterpret_cast<bf16x8*>(to) = widen(kr[i].x, kr[i].y);
+            *reinterpret_cast<bf16x8*>(to + 16) = widen(kr[i].z, kr[i].w);
+        }
+        if (tid < 4) {
+            const float ks = known ? ks_in * a.scale2 : __builtin_nanf(""), vs = known ? vs_in : __builtin_nanf("");
+            const bool none = fabsf(vs) < 1.1754944e-38f;
+            scales[buf][tid] = make_float4(ks, none ? 0.f : __builtin_amdgcn_logf(vs), none ? 1.f : 1.f / vs,
+                                           none ? 1.f : 0.f);
+        }
+    };
+    auto stage_values = [&](int buf) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             const int p = tid + i * NT;
             if (4 * D % NT != 0 && p >= 4 * D) break;
-            const int key = p / (D / 16), piece = p % (D / 16);
-            const int row = (key & 32) | (key & 12) << 1 | (key & 16) >> 2 | (key & 3);
-            char* kt = kb + row * KP + 32 * piece;
-            char* vt = vb + (p / 4) * VP + 32 * (p & 3);
-            *reinterpret_cast<bf16x8*>(kt) = widen(kr[i].x, kr[i].y);
-            *reinterpret_cast<bf16x8*>(kt + 16) = widen(kr[i].z, kr[i].w);
-            *reinterpret_cast<bf16x8*>(vt) = widen(vr[i].x, vr[i].y);
-            *reinterpret_cast<bf16x8*>(vt + 16) = widen(vr[i].z, vr[i].w);
-        }
-        if (tid < 4) {
-            const bool none = fabsf(vs_in) < 1.1754944e-38f;
-            scales[buf][tid] = make_float4(ks_in, none ? 0.f : __builtin_amdgcn_logf(vs_in), none ? 1.f : 1.f / vs_in,
-                                           none ? 1.f : 0.f);
+            char* to = lds + buf * BUF + KB + (p / 4) * VP + 32 * (p & 3);
+            *reinterpret_cast<bf16x8*>(to) = widen(vr[i].x, vr[i].y);
+            *reinterpret_cast<bf16x8*>(to + 16) = widen(vr[i].z, vr[i].w);
         }
     };
+    // LDS written by this wave is visible after it; loads stay in flight
+    auto phase_end = [&]() {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
 
+    // the tiles this wave has staged before its first step: K(0 .. late), V(.. late - 1)
+    const int late = NW == 8 && wave >= 4 ? 1 : 0;
     if (w.k0 < w.k1) {
-        find_pages(w.k0);
-        load(w.k0);
-        find_pages(w.k0 + kTile);
+        key_pages(w.k0);
+        load_keys(w.k0);
+        key_pages(w.k0 + kTile);
+        value_pages(w.k0);
     }
     bf16x8 qf[KS][NP];
     {
@@ -516,20 +565,48 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttnArgs a) {
         for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
     float m = neg_inf(), l = 0.f;
 
-    if (w.k0 < w.k1) stage(0);
-    __syncthreads();
+    bf16x8 pf[2][2][NP];
+    bool seen_last = false;     // whether this wave's rows saw keys of the tile before
+    auto values_product = [&](int buf) {
+        const char* vb = lds + buf * BUF + KB + col * VP + 32 * half;
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < DT; ++i) {
+                    const bf16x8 vf = *reinterpret_cast<const bf16x8*>(vb + i * 32 * VP + 64 * tt + 16 * u);
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)
+                        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[tt][u][p], o[i], 0, 0, 0);
+                }
+    };
+    if (w.k0 < w.k1) {
+        stage_keys(0);
+        load_values(w.k0);
+        load_keys(w.k0 + kTile);
+        value_pages(w.k0 + kTile);
+        key_pages(w.k0 + 2 * kTile);
+        if (late) {
+            stage_keys(1);
+            stage_values(0);
+            load_values(w.k0 + kTile);
+            load_keys(w.k0 + 2 * kTile);
+            value_pages(w.k0 + 2 * kTile);
+            key_pages(w.k0 + 3 * kTile);
+        }
+        phase_end();
+        if (late) phase_end();
+    }
     int buf = 0;
     for (int t0 = w.k0; t0 < w.k1; t0 += kTile, buf ^= 1) {
-        const bool more = t0 + kTile < w.k1;
-        if (more) {
-            load(t0 + kTile);
-            find_pages(t0 + 2 * kTile);
-        }
+        // M(t)
+        if (seen_last) values_product(buf ^ 1);
         // some row of this wave sees some key of this step
-        if (any && t0 <= p_last && (a.window == 0 || t0 + kTile - 1 > p_first - a.window)) {
+        const bool seen_now = any && t0 <= p_last && (a.window == 0 || t0 + kTile - 1 > p_first - a.window);
+        f32x16 s[2];
+        if (seen_now) {
             const char* kb = lds + buf * BUF + col * KP + 16 * half;
-            const char* vb = lds + buf * BUF + KB + col * VP + 32 * half;
-            f32x16 s[2];
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
 #pragma unroll
@@ -542,6 +619,16 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttnArgs a) {
                         s[tt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[k][p], s[tt], 0, 0, 0);
                 }
             }
+        }
+        phase_end();
+        // V(t)
+        stage_keys(buf ^ 1 ^ late);
+        stage_values(buf ^ late);
+        load_keys(t0 + (2 + late) * kTile);
+        load_values(t0 + (1 + late) * kTile);
+        key_pages(t0 + (3 + late) * kTile);
+        value_pages(t0 + (2 + late) * kTile);
+        if (seen_now) {
             // the value scale vs goes into the exponent, p vs = 2^(x + log2 vs),
             // and comes out of the sum of each 16 keys again
             float4 f[2];
@@ -570,7 +657,7 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttnArgs a) {
                 for (int j = 1; j < 16; ++j) top[tt] = fmaxf(top[tt], s[tt][j]);
             }
             float most = fmaxf(top[0] * f[0].x, top[1] * f[1].x);
-            most = fmaxf(most, __shfl_xor(most, 32, 64));
+            most = max_halves(most);
             if (__any(most > m + kSlack)) {
                 const float to = fmaxf(m, most);
                 const float alpha = __builtin_amdgcn_exp2f(m - (to == neg_inf() ? 0.f : to));
@@ -580,7 +667,6 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttnArgs a) {
                 for (int i = 0; i < DT; ++i) o[i] *= alpha;
             }
             const float ref = m == neg_inf() ? 0.f : m;
-            bf16x8 pf[2][2][NP];
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
                 const float shift = f[tt].y - ref;
@@ -606,21 +692,12 @@ __global__ __launch_bounds__(64 * NW) void k_attend_rows(const AttnArgs a) {
                         for (int p = 0; p < NP; ++p)
                             if (f[tt].w > 0.f) pf[tt][u][p] = __builtin_bit_cast(bf16x8, make_uint4(0, 0, 0, 0));
             }
-#pragma unroll
-            for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int i = 0; i < DT; ++i) {
-                        const bf16x8 vf = *reinterpret_cast<const bf16x8*>(vb + i * 32 * VP + 64 * tt + 16 * u);
-#pragma unroll
-                        for (int p = 0; p < NP; ++p)
-                            o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[tt][u][p], o[i], 0, 0, 0);
-                    }
         }
-        if (more) stage(buf ^ 1);
-        __syncthreads();
+        seen_last = seen_now;
+        phase_end();
     }
+    if (NW == 8 && w.k0 < w.k1 && !late) phase_end();
+    if (seen_last) values_product(buf ^ 1);
 
     l += __shfl_xor(l, 32, 64);
     if (!valid) return;
