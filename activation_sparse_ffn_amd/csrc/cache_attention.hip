@@ -18,6 +18,8 @@
 // as they lie.
 #include <math.h>
 
+#include <type_traits>
+
 #include "attn_launch.hpp"
 #include "common.hpp"
 
@@ -100,7 +102,9 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int tile_rows, Work
 // that nothing waits for it: known_page says whether it names a page of the
 // pool, page_in one that is safe to read in any case (a row that sees a key of
 // an unknown page gets its NaN from the scales).
-__device__ __forceinline__ uint32_t page_entry(const CacheArgs& c, const int32_t* row, int pos) {
+typedef const __attribute__((address_space(4))) int32_t* ConstTable;    // read by scalar loads
+template <typename Row>
+__device__ __forceinline__ uint32_t page_entry(const CacheArgs& c, Row row, int pos) {
     const int idx = pos >> c.shift;
     return (uint32_t)row[idx < c.max_pages ? idx : c.max_pages - 1];
 }
@@ -418,15 +422,17 @@ __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few
 // (token, head of the group), so every head that shares the keys shares the tile.
 //
 // A step of a wave is two phases of about equal length: M(t), the matrix
-// products O += P(t - 1) V(t - 1) and S = K(t) Q, and V(t), the softmax of S
-// and this thread's share of widening later tiles. With eight waves the second
-// four (the second wave of every SIMD) run one phase behind, so that one wave of
-// a SIMD keeps the matrix cores busy while the other computes weights; barriers
-// between phases hold them there. In phase order: K(t) is read in phases 2t and
-// 2t + 1, V(t) in 2t + 2 and 2t + 3, the scales of t in 2t + 1 and 2t + 2; the
-// first four waves write their half of K(t + 1) and V(t) in phase 2t + 1, the
-// others theirs of K(t + 2) and V(t + 1) in phase 2t + 2: always after the last
-// read of what the (double) buffer held and before its first use.
+// products O += P(t - 1) V(t - 1) and S = K(t) Q with this thread's share of
+// widening later tiles in their shadow, and V(t), the softmax of S. With eight
+// waves the second four (the second wave of every SIMD) run one phase behind, so
+// that one wave of a SIMD keeps the matrix cores busy while the other computes
+// weights; barriers between phases hold them there. Counting phases, K(t) is
+// read in 2t and 2t + 1, V(t) in 2t + 2 and 2t + 3, the scales of t in 2t + 1 and
+// 2t + 2; the first four waves write their part of K(t + 1), V(t) and the scales
+// of t in phase 2t, the others theirs in 2t + 1: always after the last read of
+// what the (double) buffer held and before its first use.
+//
+// What a wave loads lies in one page, so page entries and addresses are scalar.
 //
 // v_mfma_f32_32x32x16_bf16: lane l holds operand row or column l % 32, k = 8
 // (l / 32) .. + 7, and of the result column l % 32, rows 8 (i / 4) + 4 (l / 32)
@@ -451,7 +457,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     const CacheArgs& c = a.c;
     Work w;
     if (!find_work(a, 32 * NW, w)) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
     const int r = w.r0 + 32 * wave + col;
     const bool valid = r < w.rows;
@@ -459,12 +465,25 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     const int head = w.h * a.G + (valid ? r - tok * a.G : 0);
     const int pos = w.p0 + tok;
 
-    // staging: piece i of this thread is piece p = tid + i NT of the tile
+    // Staging: wave part i of this wave, (wave + i NW) of the tile's D / 16, is 64
+    // pieces of 16 bytes of the keys (token-major) and of the values (16 keys of
+    // a channel, channels first), all of the same 16 keys.
     const uint32_t head_bytes = (uint32_t)c.P * D;      // of one page
     const uint32_t page_bytes = c.Hkv * head_bytes;
-    const int32_t* table = c.table + (int64_t)w.b * c.table_stride;
+    const ConstTable table = (ConstTable)(uintptr_t)(c.table + (int64_t)w.b * c.table_stride);
     const int8_t* keys = c.keys + (size_t)w.h * head_bytes;
     const int8_t* values = c.values + (size_t)w.h * head_bytes;
+    uint32_t off_k[CH], off_v[CH];      // in the page; P = 128 adds 64 tokens for its second half
+    int to_k[CH], to_v[CH];             // in LDS
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int p = tid + i * NT, key = p / (D / 16) & 63, piece = p % (D / 16), d = p % D, g = p / D & 3;
+        off_k[i] = (key & (c.P - 1)) * D + 16 * piece;
+        off_v[i] = d * c.P + ((16 * g) & (c.P - 1));
+        to_k[i] = ((key & 32) | (key & 12) << 1 | (key & 16) >> 2 | (key & 3)) * KP + 32 * piece;
+        to_v[i] = KB + d * VP + 32 * g;
+    }
+    auto active = [&](int i) { return 4 * D % NT == 0 || (wave + i * NW) * 64 < 4 * D; };
     uint4 kr[CH], vr[CH];
     uint32_t entry_k[CH], entry_v[CH], entry_s = 0;
     float ks_in = 0.f, vs_in = 0.f;
@@ -472,64 +491,57 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     // t0: first key of the tile (tiles past the last one load what is never used)
     auto key_pages = [&](int t0) {
 #pragma unroll
-        for (int i = 0; i < CH; ++i) entry_k[i] = page_entry(c, table, t0 + ((tid + i * NT) / (D / 16) & 48));
-        if (tid < 4) entry_s = page_entry(c, table, t0 + 16 * tid);
+        for (int i = 0; i < CH; ++i) entry_k[i] = page_entry(c, table, t0 + 16 * ((wave + i * NW) * 64 / D & 3));
     };
     auto value_pages = [&](int t0) {
 #pragma unroll
-        for (int i = 0; i < CH; ++i) entry_v[i] = page_entry(c, table, t0 + 16 * ((tid + i * NT) & 3));
+        for (int i = 0; i < CH; ++i) entry_v[i] = page_entry(c, table, t0 + 16 * ((wave + i * NW) * 64 / D & 3));
+        if (wave == 0 && tid < 4) entry_s = page_entry(c, c.table + (int64_t)w.b * c.table_stride, t0 + 16 * tid);
     };
     auto load_keys = [&](int t0) {
-        const int in_page = t0 & (c.P - 1);
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int p = tid + i * NT, key = p / (D / 16), piece = p % (D / 16);
-            if (4 * D % NT != 0 && p >= 4 * D) break;
-            kr[i] = *reinterpret_cast<const uint4*>(keys + (uint64_t)page_in(c, entry_k[i]) * page_bytes +
-                                                    (uint32_t)(((key & (c.P - 1)) + in_page) * D + 16 * piece));
-        }
-        if (tid < 4) {
+        for (int i = 0; i < CH; ++i)
+            if (active(i))
+                kr[i] = *reinterpret_cast<const uint4*>(keys + (uint64_t)page_in(c, entry_k[i]) * page_bytes +
+                                                        (t0 & (c.P - 1)) * D + off_k[i]);
+    };
+    auto load_values = [&](int t0) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+            if (active(i))
+                vr[i] = *reinterpret_cast<const uint4*>(values + (uint64_t)page_in(c, entry_v[i]) * page_bytes +
+                                                        (t0 & (c.P - 1)) + off_v[i]);
+        if (wave == 0 && tid < 4) {
             const size_t srow = (size_t)page_in(c, entry_s) * c.Hkv + w.h;
             ks_in = c.k_scale[srow];
             vs_in = c.v_scale[srow];
             known = known_page(c, entry_s, t0 + 16 * tid);
         }
     };
-    auto load_values = [&](int t0) {
-        const int in_page = t0 & (c.P - 1);
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int p = tid + i * NT;
-            if (4 * D % NT != 0 && p >= 4 * D) break;
-            vr[i] = *reinterpret_cast<const uint4*>(values + (uint64_t)page_in(c, entry_v[i]) * page_bytes +
-                                                    (uint32_t)((p / 4) * c.P + ((16 * (p & 3)) & (c.P - 1)) + in_page));
-        }
-    };
     auto stage_keys = [&](int buf) {
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int p = tid + i * NT, key = p / (D / 16), piece = p % (D / 16);
-            if (4 * D % NT != 0 && p >= 4 * D) break;
-            const int row = (key & 32) | (key & 12) << 1 | (key & 16) >> 2 | (key & 3);
-            char* to = lds + buf * BUF + row * KP + 32 * piece;
-            *reinterpret_cast<bf16x8*>(to) = widen(kr[i].x, kr[i].y);
-            *reinterpret_cast<bf16x8*>(to + 16) = widen(kr[i].z, kr[i].w);
-        }
-        if (tid < 4) {
+        for (int i = 0; i < CH; ++i)
+            if (active(i)) {
+                char* to = lds + buf * BUF + to_k[i];
+                *reinterpret_cast<bf16x8*>(to) = widen(kr[i].x, kr[i].y);
+                *reinterpret_cast<bf16x8*>(to + 16) = widen(kr[i].z, kr[i].w);
+            }
+    };
+    auto stage_values = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+            if (active(i)) {
+                char* to = lds + buf * BUF + to_v[i];
+                *reinterpret_cast<bf16x8*>(to) = widen(vr[i].x, vr[i].y);
+                *reinterpret_cast<bf16x8*>(to + 16) = widen(vr[i].z, vr[i].w);
+            }
+    };
+    auto stage_scales = [&](int buf) {
+        if (wave == 0 && tid < 4) {
             const float ks = known ? ks_in * a.scale2 : __builtin_nanf(""), vs = known ? vs_in : __builtin_nanf("");
             const bool none = fabsf(vs) < 1.1754944e-38f;
             scales[buf][tid] = make_float4(ks, none ? 0.f : __builtin_amdgcn_logf(vs), none ? 1.f : 1.f / vs,
                                            none ? 1.f : 0.f);
-        }
-    };
-    auto stage_values = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const int p = tid + i * NT;
-            if (4 * D % NT != 0 && p >= 4 * D) break;
-            char* to = lds + buf * BUF + KB + (p / 4) * VP + 32 * (p & 3);
-            *reinterpret_cast<bf16x8*>(to) = widen(vr[i].x, vr[i].y);
-            *reinterpret_cast<bf16x8*>(to + 16) = widen(vr[i].z, vr[i].w);
         }
     };
     // LDS written by this wave is visible after it; loads stay in flight
@@ -539,13 +551,14 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    // the tiles this wave has staged before its first step: K(0 .. late), V(.. late - 1)
-    const int late = NW == 8 && wave >= 4 ? 1 : 0;
+    const bool late = NW == 8 && wave >= 4;
     if (w.k0 < w.k1) {
         key_pages(w.k0);
-        load_keys(w.k0);
-        key_pages(w.k0 + kTile);
         value_pages(w.k0);
+        load_keys(w.k0);
+        load_values(w.k0);
+        key_pages(w.k0 + kTile);
+        value_pages(w.k0 + kTile);
     }
     bf16x8 qf[KS][NP];
     {
@@ -555,7 +568,6 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     }
     // positions of this wave's rows
     const int w0 = w.r0 + 32 * wave, w1 = w.rows - w0 < 32 ? w.rows : w0 + 32;
-    const bool any = w0 < w.rows;
     const int p_first = w.p0 + w0 / a.G, p_last = w.p0 + (w1 - 1) / a.G;
 
     f32x16 o[DT];
@@ -566,138 +578,157 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     float m = neg_inf(), l = 0.f;
 
     bf16x8 pf[2][2][NP];
-    bool seen_last = false;     // whether this wave's rows saw keys of the tile before
-    auto values_product = [&](int buf) {
-        const char* vb = lds + buf * BUF + KB + col * VP + 32 * half;
+    f32x16 s[2];
+    // Phase M of the step at t0: O += P V of the tile before (in buffer `buf` ^ 1;
+    // not in the first step), S = K Q of this one and the staging (not in what
+    // follows the last step). A product's operand is read from LDS kAhead products before it is used; the
+    // staging's arithmetic goes between the products, which leave seven of eight
+    // issue slots free.
+    auto phase_m = [&](auto with_values, auto with_keys, int buf, int t0) {
+        constexpr int NV = with_values.value ? 4 * DT : 0, NK = with_keys.value ? 2 * KS : 0, N = NV + NK;
+        constexpr int kAhead = N < 4 ? N : 4;
+        const char* vb = lds + (buf ^ 1) * BUF + KB + col * VP + 32 * half;
+        const char* kb = lds + buf * BUF + col * KP + 16 * half;
+        auto read = [&](int i) {
+            // values: (tile half, step, channel tile); keys: (16 channels, tile half)
+            const char* p = i < NV ? vb + i % DT * 32 * VP + 64 * (i / (2 * DT)) + 16 * (i / DT % 2)
+                                   : kb + (i - NV) % 2 * 32 * KP + 32 * ((i - NV) / 2);
+            return *reinterpret_cast<const bf16x8*>(p);
+        };
+        bf16x8 f[kAhead + 1];
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt)
+        for (int i = 0; i < kAhead; ++i) f[i] = read(i);
+        if (with_keys.value)
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < DT; ++i) {
-                    const bf16x8 vf = *reinterpret_cast<const bf16x8*>(vb + i * 32 * VP + 64 * tt + 16 * u);
-#pragma unroll
-                    for (int p = 0; p < NP; ++p)
-                        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, pf[tt][u][p], o[i], 0, 0, 0);
-                }
-    };
-    if (w.k0 < w.k1) {
-        stage_keys(0);
-        load_values(w.k0);
-        load_keys(w.k0 + kTile);
-        value_pages(w.k0 + kTile);
-        key_pages(w.k0 + 2 * kTile);
-        if (late) {
-            stage_keys(1);
-            stage_values(0);
-            load_values(w.k0 + kTile);
-            load_keys(w.k0 + 2 * kTile);
-            value_pages(w.k0 + 2 * kTile);
-            key_pages(w.k0 + 3 * kTile);
-        }
-        phase_end();
-        if (late) phase_end();
-    }
-    int buf = 0;
-    for (int t0 = w.k0; t0 < w.k1; t0 += kTile, buf ^= 1) {
-        // M(t)
-        if (seen_last) values_product(buf ^ 1);
-        // some row of this wave sees some key of this step
-        const bool seen_now = any && t0 <= p_last && (a.window == 0 || t0 + kTile - 1 > p_first - a.window);
-        f32x16 s[2];
-        if (seen_now) {
-            const char* kb = lds + buf * BUF + col * KP + 16 * half;
-#pragma unroll
-            for (int tt = 0; tt < 2; ++tt) {
+            for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) s[tt][j] = 0.f;
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    const bf16x8 kf = *reinterpret_cast<const bf16x8*>(kb + tt * 32 * KP + 32 * k);
+        for (int i = 0; i < N; ++i) {
+            if (i < NV) {
+#pragma unroll
+                for (int p = 0; p < NP; ++p)
+                    o[i % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        f[i % kAhead], pf[i / (2 * DT)][i / DT % 2][p], o[i % DT], 0, 0, 0);
+            } else {
+                const int tt = (i - NV) % 2, k = (i - NV) / 2;
+#pragma unroll
+                for (int p = 0; p < NP; ++p)
+                    s[tt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % kAhead], qf[k][p], s[tt], 0, 0, 0);
+            }
+            if (i + kAhead < N) f[i % kAhead] = read(i + kAhead);
+        }
+        if (with_keys.value) {
+            stage_keys(buf ^ 1);
+            stage_values(buf);
+            load_keys(t0 + 2 * kTile);
+            load_values(t0 + kTile);
+            key_pages(t0 + 3 * kTile);
+            value_pages(t0 + 2 * kTile);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);     // LDS reads
+#pragma unroll
+        for (int i = 0; i < N - kAhead; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, NP, 0);       // matrix products
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x2, 3, 0);        // arithmetic
+        }
+        __builtin_amdgcn_sched_group_barrier(0x8, kAhead * NP, 0);
+    };
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    if (w.k0 < w.k1) {
+        stage_keys(0);
+        load_keys(w.k0 + kTile);
+        key_pages(w.k0 + 2 * kTile);
+        phase_end();
+        if (late) phase_end();
+    }
+    // Phase V of the step at t0. A wave whose rows see none of the tile's keys
+    // goes through it like the others (all keys are hidden): few tiles of a row
+    // tile are such, and every wave meets every barrier.
+    auto phase_v = [&](int buf, int t0) {
+        // the value scale vs goes into the exponent, p vs = 2^(x + log2 vs),
+        // and comes out of the sum of each 16 keys again
+        float4 f[2];
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) f[tt] = scales[buf][2 * tt + half];
+        if (t0 + kTile - 1 > p_first || t0 + kTile > w.k1 || (a.window > 0 && t0 <= p_last - a.window)) {
+            // as in k_attend_few: hidden keys by a select, and no scales
+            // where the row sees none of the lane's sixteen
+            const int up = last_seen(pos, t0, w.k1) - 16 * half, dn = before_seen(pos, t0, a.window) - 16 * half;
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int key = 32 * tt + j;
+                    s[tt][j] = key > up || key <= dn ? neg_inf() : s[tt][j] * f[tt].x;
+                }
+                f[tt].x = 1.f;
+                if (32 * tt > up || 32 * tt + 15 <= dn) f[tt] = make_float4(1.f, 0.f, 0.f, 0.f);
+            }
+        }
+        float top[2];
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            top[tt] = s[tt][0];
+#pragma unroll
+            for (int j = 1; j < 16; ++j) top[tt] = fmaxf(top[tt], s[tt][j]);
+        }
+        float most = fmaxf(top[0] * f[0].x, top[1] * f[1].x);
+        most = max_halves(most);
+        if (__any(most > m + kSlack)) {
+            const float to = fmaxf(m, most);
+            const float alpha = __builtin_amdgcn_exp2f(m - (to == neg_inf() ? 0.f : to));
+            m = to;
+            l *= alpha;
+#pragma unroll
+            for (int i = 0; i < DT; ++i) o[i] *= alpha;
+        }
+        const float ref = m == neg_inf() ? 0.f : m;
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            const float shift = f[tt].y - ref;
+            float sum = 0.f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float pv[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    pv[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[tt][8 * u + e], f[tt].x, shift));
+                    sum += pv[e];
+                }
+                pieces<NP>(pv, pf[tt][u]);
+            }
+            l += sum * f[tt].z;
+        }
+        if (__any(f[0].w + f[1].w > 0.f)) {
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int p = 0; p < NP; ++p)
-                        s[tt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[k][p], s[tt], 0, 0, 0);
-                }
-            }
+                        if (f[tt].w > 0.f) pf[tt][u][p] = __builtin_bit_cast(bf16x8, make_uint4(0, 0, 0, 0));
         }
+    };
+    if (w.k0 < w.k1) {
+        stage_scales(0);
+        phase_m(no, yes, 0, w.k0);
         phase_end();
-        // V(t)
-        stage_keys(buf ^ 1 ^ late);
-        stage_values(buf ^ late);
-        load_keys(t0 + (2 + late) * kTile);
-        load_values(t0 + (1 + late) * kTile);
-        key_pages(t0 + (3 + late) * kTile);
-        value_pages(t0 + (2 + late) * kTile);
-        if (seen_now) {
-            // the value scale vs goes into the exponent, p vs = 2^(x + log2 vs),
-            // and comes out of the sum of each 16 keys again
-            float4 f[2];
-#pragma unroll
-            for (int tt = 0; tt < 2; ++tt) f[tt] = scales[buf][2 * tt + half];
-            if (t0 + kTile - 1 > p_first || t0 + kTile > w.k1 || (a.window > 0 && t0 <= p_last - a.window)) {
-                // as in k_attend_few: hidden keys by a select, and no scales
-                // where the row sees none of the lane's sixteen
-                const int up = last_seen(pos, t0, w.k1) - 16 * half, dn = before_seen(pos, t0, a.window) - 16 * half;
-#pragma unroll
-                for (int tt = 0; tt < 2; ++tt) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int key = 32 * tt + j;
-                        s[tt][j] = key > up || key <= dn ? neg_inf() : s[tt][j] * f[tt].x;
-                    }
-                    f[tt].x = 1.f;
-                    if (32 * tt > up || 32 * tt + 15 <= dn) f[tt] = make_float4(1.f, 0.f, 0.f, 0.f);
-                }
-            }
-            float top[2];
-#pragma unroll
-            for (int tt = 0; tt < 2; ++tt) {
-                top[tt] = s[tt][0];
-#pragma unroll
-                for (int j = 1; j < 16; ++j) top[tt] = fmaxf(top[tt], s[tt][j]);
-            }
-            float most = fmaxf(top[0] * f[0].x, top[1] * f[1].x);
-            most = max_halves(most);
-            if (__any(most > m + kSlack)) {
-                const float to = fmaxf(m, most);
-                const float alpha = __builtin_amdgcn_exp2f(m - (to == neg_inf() ? 0.f : to));
-                m = to;
-                l *= alpha;
-#pragma unroll
-                for (int i = 0; i < DT; ++i) o[i] *= alpha;
-            }
-            const float ref = m == neg_inf() ? 0.f : m;
-#pragma unroll
-            for (int tt = 0; tt < 2; ++tt) {
-                const float shift = f[tt].y - ref;
-                float sum = 0.f;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float pv[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        pv[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[tt][8 * u + e], f[tt].x, shift));
-                        sum += pv[e];
-                    }
-                    pieces<NP>(pv, pf[tt][u]);
-                }
-                l += sum * f[tt].z;
-            }
-            if (__any(f[0].w + f[1].w > 0.f)) {
-#pragma unroll
-                for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int p = 0; p < NP; ++p)
-                            if (f[tt].w > 0.f) pf[tt][u][p] = __builtin_bit_cast(bf16x8, make_uint4(0, 0, 0, 0));
-            }
+        phase_v(0, w.k0);
+        phase_end();
+        int buf = 1;
+        for (int t0 = w.k0 + kTile; t0 < w.k1; t0 += kTile, buf ^= 1) {
+            stage_scales(buf);
+            phase_m(yes, yes, buf, t0);
+            phase_end();
+            phase_v(buf, t0);
+            phase_end();
         }
-        seen_last = seen_now;
-        phase_end();
+        if (NW == 8 && !late) phase_end();
+        phase_m(yes, no, buf, w.k1);
     }
-    if (NW == 8 && w.k0 < w.k1 && !late) phase_end();
-    if (seen_last) values_product(buf ^ 1);
 
     l += __shfl_xor(l, 32, 64);
     if (!valid) return;
