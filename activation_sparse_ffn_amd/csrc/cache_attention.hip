@@ -498,19 +498,17 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
         for (int i = 0; i < CH; ++i) entry_v[i] = page_entry(c, table, t0 + 16 * ((wave + i * NW) * 64 / D & 3));
         if (wave == 0 && tid < 4) entry_s = page_entry(c, c.table + (int64_t)w.b * c.table_stride, t0 + 16 * tid);
     };
-    auto load_keys = [&](int t0) {
-#pragma unroll
-        for (int i = 0; i < CH; ++i)
-            if (active(i))
-                kr[i] = *reinterpret_cast<const uint4*>(keys + (uint64_t)page_in(c, entry_k[i]) * page_bytes +
-                                                        (t0 & (c.P - 1)) * D + off_k[i]);
+    auto load_keys = [&](int i, int t0) {
+        if (active(i))
+            kr[i] = *reinterpret_cast<const uint4*>(keys + (uint64_t)page_in(c, entry_k[i]) * page_bytes +
+                                                    (t0 & (c.P - 1)) * D + off_k[i]);
     };
-    auto load_values = [&](int t0) {
-#pragma unroll
-        for (int i = 0; i < CH; ++i)
-            if (active(i))
-                vr[i] = *reinterpret_cast<const uint4*>(values + (uint64_t)page_in(c, entry_v[i]) * page_bytes +
-                                                        (t0 & (c.P - 1)) + off_v[i]);
+    auto load_values = [&](int i, int t0) {
+        if (active(i))
+            vr[i] = *reinterpret_cast<const uint4*>(values + (uint64_t)page_in(c, entry_v[i]) * page_bytes +
+                                                    (t0 & (c.P - 1)) + off_v[i]);
+    };
+    auto load_scales = [&](int t0) {
         if (wave == 0 && tid < 4) {
             const size_t srow = (size_t)page_in(c, entry_s) * c.Hkv + w.h;
             ks_in = c.k_scale[srow];
@@ -518,30 +516,26 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
             known = known_page(c, entry_s, t0 + 16 * tid);
         }
     };
-    auto stage_keys = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < CH; ++i)
-            if (active(i)) {
-                char* to = lds + buf * BUF + to_k[i];
-                *reinterpret_cast<bf16x8*>(to) = widen(kr[i].x, kr[i].y);
-                *reinterpret_cast<bf16x8*>(to + 16) = widen(kr[i].z, kr[i].w);
-            }
+    auto stage_keys = [&](int i, int buf) {
+        if (active(i)) {
+            char* to = lds + buf * BUF + to_k[i];
+            *reinterpret_cast<bf16x8*>(to) = widen(kr[i].x, kr[i].y);
+            *reinterpret_cast<bf16x8*>(to + 16) = widen(kr[i].z, kr[i].w);
+        }
     };
-    auto stage_values = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < CH; ++i)
-            if (active(i)) {
-                char* to = lds + buf * BUF + to_v[i];
-                *reinterpret_cast<bf16x8*>(to) = widen(vr[i].x, vr[i].y);
-                *reinterpret_cast<bf16x8*>(to + 16) = widen(vr[i].z, vr[i].w);
-            }
+    auto stage_values = [&](int i, int buf) {
+        if (active(i)) {
+            char* to = lds + buf * BUF + to_v[i];
+            *reinterpret_cast<bf16x8*>(to) = widen(vr[i].x, vr[i].y);
+            *reinterpret_cast<bf16x8*>(to + 16) = widen(vr[i].z, vr[i].w);
+        }
     };
     auto stage_scales = [&](int buf) {
         if (wave == 0 && tid < 4) {
             const float ks = known ? ks_in * a.scale2 : __builtin_nanf(""), vs = known ? vs_in : __builtin_nanf("");
             const bool none = fabsf(vs) < 1.1754944e-38f;
-            scales[buf][tid] = make_float4(ks, none ? 0.f : __builtin_amdgcn_logf(vs), none ? 1.f : 1.f / vs,
-                                           none ? 1.f : 0.f);
+            scales[buf][tid] = make_float4(ks, none ? 0.f : __builtin_amdgcn_logf(vs),
+                                           none ? 1.f : __builtin_amdgcn_rcpf(vs), none ? 1.f : 0.f);
         }
     };
     // LDS written by this wave is visible after it; loads stay in flight
@@ -555,8 +549,12 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     if (w.k0 < w.k1) {
         key_pages(w.k0);
         value_pages(w.k0);
-        load_keys(w.k0);
-        load_values(w.k0);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            load_keys(i, w.k0);
+            load_values(i, w.k0);
+        }
+        load_scales(w.k0);
         key_pages(w.k0 + kTile);
         value_pages(w.k0 + kTile);
     }
@@ -581,12 +579,14 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     f32x16 s[2];
     // Phase M of the step at t0: O += P V of the tile before (in buffer `buf` ^ 1;
     // not in the first step), S = K Q of this one and the staging (not in what
-    // follows the last step). A product's operand is read from LDS kAhead products before it is used; the
-    // staging's arithmetic goes between the products, which leave seven of eight
-    // issue slots free.
+    // follows the last step). The products go in groups of four (128 cycles):
+    // before each the operands of the next group are read from LDS, and into some
+    // of them goes a piece of the staging, whose arithmetic fits the issue slots
+    // that the products leave free. The phase has priority over the softmax of the
+    // SIMD's other wave: a product that starts late is lost, a weight is not.
     auto phase_m = [&](auto with_values, auto with_keys, int buf, int t0) {
         constexpr int NV = with_values.value ? 4 * DT : 0, NK = with_keys.value ? 2 * KS : 0, N = NV + NK;
-        constexpr int kAhead = N < 4 ? N : 4;
+        constexpr int GS = 4, NG = N / GS;
         const char* vb = lds + (buf ^ 1) * BUF + KB + col * VP + 32 * half;
         const char* kb = lds + buf * BUF + col * KP + 16 * half;
         auto read = [&](int i) {
@@ -595,51 +595,72 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
                                    : kb + (i - NV) % 2 * 32 * KP + 32 * ((i - NV) / 2);
             return *reinterpret_cast<const bf16x8*>(p);
         };
-        bf16x8 f[kAhead + 1];
+        bf16x8 f[2][GS];
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) f[i] = read(i);
+        for (int i = 0; i < GS; ++i) f[0][i] = read(i);
         if (with_keys.value)
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) s[tt][j] = 0.f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (i < NV) {
+        for (int g = 0; g < NG; ++g) {
+            if (g + 1 < NG)
 #pragma unroll
-                for (int p = 0; p < NP; ++p)
-                    o[i % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        f[i % kAhead], pf[i / (2 * DT)][i / DT % 2][p], o[i % DT], 0, 0, 0);
-            } else {
-                const int tt = (i - NV) % 2, k = (i - NV) / 2;
+                for (int i = 0; i < GS; ++i) f[(g + 1) & 1][i] = read((g + 1) * GS + i);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int p = 0; p < NP; ++p)
-                    s[tt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % kAhead], qf[k][p], s[tt], 0, 0, 0);
+            for (int j = 0; j < GS; ++j) {
+                const int i = g * GS + j;
+                if (i < NV) {
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)
+                        o[i % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                            f[g & 1][j], pf[i / (2 * DT)][i / DT % 2][p], o[i % DT], 0, 0, 0);
+                } else {
+                    const int tt = (i - NV) % 2, k = (i - NV) / 2;
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)
+                        s[tt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[g & 1][j], qf[k][p], s[tt], 0, 0, 0);
+                }
             }
-            if (i + kAhead < N) f[i % kAhead] = read(i + kAhead);
+            if (with_keys.value)
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                    if (g == (2 * i + 1) * NG / (2 * CH + 1)) {
+                        stage_keys(i, buf ^ 1);
+                        load_keys(i, t0 + 2 * kTile);
+                    }
+                    if (g == (2 * i + 2) * NG / (2 * CH + 1)) {
+                        stage_values(i, buf);
+                        load_values(i, t0 + kTile);
+                    }
+                }
+            // one product, then a share of the arithmetic, four times
+#pragma unroll
+            for (int j = 0; j < GS; ++j) {
+                __builtin_amdgcn_sched_group_barrier(0x8, NP, 0);
+                __builtin_amdgcn_sched_group_barrier(0x2, 7, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
         if (with_keys.value) {
-            stage_keys(buf ^ 1);
-            stage_values(buf);
-            load_keys(t0 + 2 * kTile);
-            load_values(t0 + kTile);
+            stage_scales(buf);
+            load_scales(t0 + kTile);
             key_pages(t0 + 3 * kTile);
             value_pages(t0 + 2 * kTile);
         }
-        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);     // LDS reads
-#pragma unroll
-        for (int i = 0; i < N - kAhead; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x8, NP, 0);       // matrix products
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x2, 3, 0);        // arithmetic
-        }
-        __builtin_amdgcn_sched_group_barrier(0x8, kAhead * NP, 0);
+        __builtin_amdgcn_s_setprio(0);
     };
     constexpr std::true_type yes{};
     constexpr std::false_type no{};
     if (w.k0 < w.k1) {
-        stage_keys(0);
-        load_keys(w.k0 + kTile);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            stage_keys(i, 0);
+            load_keys(i, w.k0 + kTile);
+        }
         key_pages(w.k0 + 2 * kTile);
         phase_end();
         if (late) phase_end();
@@ -713,14 +734,12 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
         }
     };
     if (w.k0 < w.k1) {
-        stage_scales(0);
         phase_m(no, yes, 0, w.k0);
         phase_end();
         phase_v(0, w.k0);
         phase_end();
         int buf = 1;
         for (int t0 = w.k0 + kTile; t0 < w.k1; t0 += kTile, buf ^= 1) {
-            stage_scales(buf);
             phase_m(yes, yes, buf, t0);
             phase_end();
             phase_v(buf, t0);
