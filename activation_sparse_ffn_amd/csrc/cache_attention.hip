@@ -20,8 +20,8 @@
 
 #include <type_traits>
 
+#include "attn_common.hpp"
 #include "attn_launch.hpp"
-#include "common.hpp"
 
 namespace sffn {
 
@@ -149,14 +149,6 @@ __device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
     return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-
-// Two fp32 rounded to bf16, to nearest even, as one word.
-__device__ __forceinline__ uint32_t round2(float x, float y) {
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{x, y}), bf16x2));
-}
-
 // Eight fp32 as NP bf16 pieces: their sum is x to 8 NP bits.
 template <int NP>
 __device__ __forceinline__ void pieces(const float* x, bf16x8* out) {
@@ -187,13 +179,6 @@ __device__ __forceinline__ void load_q(const E* p, bool valid, bool negate, bf16
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = negate ? -x[i] : x[i];
     pieces<NP>(x, out);
-}
-
-__device__ __forceinline__ void store4(uint16_t* p, const float* v) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-}
-__device__ __forceinline__ void store4(float* p, const float* v) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
 // The running maximum m is a reference, not always the largest score: it moves

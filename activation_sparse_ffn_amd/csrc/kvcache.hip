@@ -10,10 +10,14 @@
 //
 // Memory-bound and small: a workgroup takes one page of one head, of keys or
 // of values, so that the maximum, the rescaling and the store are one kernel
-// and no two workgroups share a scale. The new values pass through LDS to be
-// turned into token order; held entries are touched only where the scale grew.
+// and no two workgroups share a scale; what it costs is the chain lengths ->
+// table -> rows -> maximum -> store, so a thread's loads are all in flight at once
+// and stay in registers for the rounding. A thread's piece is four tokens of
+// eight channels: four tokens of a channel are one word of the values' order
+// ([D][P]), which they reach through LDS in whole words. Held entries are touched
+// only where the scale grew.
+#include "attn_common.hpp"
 #include "attn_launch.hpp"
-#include "common.hpp"
 
 namespace sffn {
 
@@ -35,12 +39,12 @@ struct PageJob {
 
 // Fills the job of this workgroup; false if it has nothing to do.
 __device__ bool page_job(const CacheArgs& c, int per_seq, PageJob& j) {
-    int64_t id = blockIdx.x;
+    uint32_t id = blockIdx.x;
     j.values = id & 1;
     id >>= 1;
-    j.h = (int)(id % c.Hkv);
-    id /= c.Hkv;
-    const int b = (int)(id / per_seq), nth = (int)(id % per_seq);
+    j.h = (int)(id % (uint32_t)c.Hkv);
+    id /= (uint32_t)c.Hkv;
+    const int b = (int)(id / (uint32_t)per_seq), nth = (int)(id % (uint32_t)per_seq);
     int64_t first = b, last = b + 1;
     if (c.cu) {
         first = c.cu[b];
@@ -69,25 +73,61 @@ __device__ __forceinline__ int8_t requantise(int8_t q, float ratio) {
     return (int8_t)(int)rintf((float)q * ratio);
 }
 
+// rint(x / s), clamped. The quotient is taken as x (1 / s), which is within 2^-22
+// of it, and by a division only where that could round the other way.
+__device__ __forceinline__ int quantise(float x, float s, float inverse, bool divide) {
+    const float t = x * inverse;
+    float q = rintf(t);
+    if (divide || fabsf(t - q) > 0.4999f) q = rintf(x / s);
+    return (int)fminf(fmaxf(q, -127.f), 127.f);
+}
+
+// LDS row pitch of the values' tile [D][P], in bytes: one word more than the
+// page, so that the rows of eight channels apart lie in other banks.
+__device__ __forceinline__ int tile_pitch(int P) { return P + 4; }
+constexpr int kTileBytes = kMaxDim * (kMaxPage + 4);
+
 template <typename E>
 __global__ __launch_bounds__(kThreads) void k_cache_append(const CacheArgs c, const Heads k, const Heads v,
                                                            int per_seq) {
     __shared__ uint32_t wave_max[kThreads / 64];
-    __shared__ __align__(16) int8_t tile[kMaxPage * kMaxDim];   // values: new entries [token][D]
+    __shared__ uint32_t tile[kTileBytes / 4];       // values: new entries, four tokens a word
     PageJob j;
     if (!page_job(c, per_seq, j) || !j.known) return;
     const Heads& in = j.values ? v : k;
     const E* x = static_cast<const E*>(in.p) + (j.t0 * in.st + (int64_t)j.h * in.sh);
-    const int chunks = c.D / 8, n = j.m * chunks;
+    // piece i: slots 4 g .. 4 g + 3 of the page, channels 8 (i % chunks) ..
+    const int chunks = c.D / 8, g0 = j.held / 4, n = ((j.held + j.m + 3) / 4 - g0) * chunks;
+    auto load = [&](int i, Raw<E>* raw) {
+        const int tok = 4 * (g0 + i / chunks) - j.held, d = 8 * (i % chunks);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (tok + q >= 0 && tok + q < j.m) raw[q].load(x + (int64_t)(tok + q) * in.st + d);
+    };
 
     // max |x| as bits: larger finite values have larger bits, and infinities
     // and NaN the largest
     uint32_t most = 0;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        float e[8];
-        Elem<E>::load8(x + (int64_t)(i / chunks) * in.st + 8 * (i % chunks), e);
+    auto widest = [&](int i, const Raw<E>* raw) {
+        const int tok = 4 * (g0 + i / chunks) - j.held;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) most = max(most, __float_as_uint(e[q]) & 0x7fffffffu);
+        for (int q = 0; q < 4; ++q) {
+            if (tok + q < 0 || tok + q >= j.m) continue;
+            float e[8];
+            raw[q].decode(e);
+#pragma unroll
+            for (int p = 0; p < 8; ++p) most = max(most, __float_as_uint(e[p]) & 0x7fffffffu);
+        }
+    };
+    Raw<E> first[4];        // the thread's first piece: its only one for 64 tokens of 128 channels
+    if ((int)threadIdx.x < n) {
+        load(threadIdx.x, first);
+        widest(threadIdx.x, first);
+    }
+    for (int i = threadIdx.x + kThreads; i < n; i += kThreads) {
+        Raw<E> raw[4];
+        load(i, raw);
+        widest(i, raw);
     }
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) most = max(most, (uint32_t)__shfl_xor((int)most, o, 64));
@@ -112,8 +152,11 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(const CacheArgs c, co
     // (the barrier above is behind every thread's read of the old scale)
     if (threadIdx.x == 0) *scale = s;
     const bool regrown = ratio < 1.f;
+    const bool divide = s < 1e-30f;         // 1 / s might overflow
+    const float inverse = 1.f / s;
 
     int8_t* pool = (j.values ? c.values : c.keys) + j.row * c.P * c.D;
+    const int pitch = tile_pitch(c.P) / 4;
     if (!j.values && regrown)
         for (int i = threadIdx.x; i < j.held * (c.D / 16); i += kThreads) {
             union { uint4 w; int8_t b[16]; } u;
@@ -122,19 +165,37 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(const CacheArgs c, co
             for (int q = 0; q < 16; ++q) u.b[q] = requantise(u.b[q], ratio);
             *reinterpret_cast<uint4*>(pool + 16 * (int64_t)i) = u.w;
         }
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const int tok = i / chunks, d = 8 * (i % chunks);
-        float e[8];
-        Elem<E>::load8(x + (int64_t)tok * in.st + d, e);
-        union { uint2 w; int8_t b[8]; } u;
+    auto round = [&](int i, const Raw<E>* raw) {
+        const int g = g0 + i / chunks, tok = 4 * g - j.held, d = 8 * (i % chunks);
+        uint32_t word[8] = {};              // of each channel: its four tokens
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            // s == 0: a maximum so small that its scale rounds to zero
-            const float r = s > 0.f ? rintf(e[q] / s) : 0.f;
-            u.b[q] = (int8_t)(int)fminf(fmaxf(r, -127.f), 127.f);
+        for (int q = 0; q < 4; ++q) {
+            if (tok + q < 0 || tok + q >= j.m) continue;
+            float e[8];
+            raw[q].decode(e);
+            uint32_t b[8];
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+                // a scale of 0 (a maximum too small for one) or NaN holds zeros
+                b[p] = s > 0.f ? (uint32_t)quantise(e[p], s, inverse, divide) & 255u : 0u;
+            if (!j.values) {
+                const uint2 w = make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24,
+                                           b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
+                *reinterpret_cast<uint2*>(pool + (int64_t)(4 * g + q) * c.D + d) = w;
+            } else {
+#pragma unroll
+                for (int p = 0; p < 8; ++p) word[p] |= b[p] << (8 * q);
+            }
         }
-        if (!j.values) *reinterpret_cast<uint2*>(pool + (int64_t)(j.held + tok) * c.D + d) = u.w;
-        else *reinterpret_cast<uint2*>(tile + tok * c.D + d) = u.w;
+        if (j.values)
+#pragma unroll
+            for (int p = 0; p < 8; ++p) tile[(d + p) * pitch + g] = word[p];
+    };
+    if ((int)threadIdx.x < n) round(threadIdx.x, first);
+    for (int i = threadIdx.x + kThreads; i < n; i += kThreads) {
+        Raw<E> raw[4];
+        load(i, raw);
+        round(i, raw);
     }
     if (!j.values) return;
     __syncthreads();
@@ -145,42 +206,36 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(const CacheArgs c, co
     for (int i = threadIdx.x; i < np * c.D; i += kThreads) {
         const int d = i / np, t0 = 16 * (p0 + i % np);
         int8_t* to = pool + (int64_t)d * c.P + t0;
-        union { uint4 w; int8_t b[16]; } u;
-        u.w = make_uint4(0, 0, 0, 0);
-        if (t0 < j.held || t0 + 16 > end) u.w = *reinterpret_cast<const uint4*>(to);
+        uint4 was = make_uint4(0, 0, 0, 0);
+        if (t0 < j.held || t0 + 16 > end) was = *reinterpret_cast<const uint4*>(to);
+        uint32_t w[4] = {was.x, was.y, was.z, was.w};
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-            const int tok = t0 + q - j.held;
-            if (tok < 0) {
-                if (regrown) u.b[q] = requantise(u.b[q], ratio);
-            } else if (tok < j.m) {
-                u.b[q] = tile[tok * c.D + d];
+        for (int q = 0; q < 4; ++q) {
+            const int t = t0 + 4 * q;
+            if (regrown && t < j.held) {
+                uint32_t r = 0;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const int8_t old_q = (int8_t)(w[q] >> (8 * p));
+                    r |= (uint32_t)(uint8_t)(t + p < j.held ? requantise(old_q, ratio) : old_q) << (8 * p);
+                }
+                w[q] = r;
             }
+            // bytes of the word that are new tokens
+            uint32_t fresh = 0;
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                if (t + p >= j.held && t + p < end) fresh |= 255u << (8 * p);
+            if (fresh != 0) w[q] = (w[q] & ~fresh) | (tile[d * pitch + t / 4] & fresh);
         }
-        *reinterpret_cast<uint4*>(to) = u.w;
+        *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
-
-template <typename E> struct Store8;
-template <> struct Store8<uint16_t> {
-    static __device__ __forceinline__ void put(uint16_t* p, const float* v) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    }
-};
-template <> struct Store8<float> {
-    static __device__ __forceinline__ void put(float* p, const float* v) {
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    }
-};
 
 template <typename E>
 __global__ __launch_bounds__(kThreads) void k_cache_read(const CacheArgs c, const Heads k, const Heads v,
                                                          int per_seq) {
-    // values: the page's pieces [D][P]; 16 bytes more a row than the longest
-    // page, so that a column's bytes lie in other banks
-    __shared__ __align__(16) int8_t tile[kMaxDim * (kMaxPage + 16)];
+    __shared__ uint32_t tile[kTileBytes / 4];       // values: the page's rows [D][P]
     PageJob j;
     if (!page_job(c, per_seq, j)) return;
     const Heads& out = j.values ? v : k;
@@ -189,37 +244,54 @@ __global__ __launch_bounds__(kThreads) void k_cache_read(const CacheArgs c, cons
     const float none[8] = {__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""),
                            __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
     for (int64_t i = threadIdx.x; i < j.early * chunks; i += kThreads)
-        Store8<E>::put(y + (i / chunks - j.early) * out.st + 8 * (i % chunks), none);
+        store8(y + (i / chunks - j.early) * out.st + 8 * (i % chunks), none);
     if (!j.known) {
         for (int i = threadIdx.x; i < j.m * chunks; i += kThreads)
-            Store8<E>::put(y + (int64_t)(i / chunks) * out.st + 8 * (i % chunks), none);
+            store8(y + (int64_t)(i / chunks) * out.st + 8 * (i % chunks), none);
         return;
     }
     const float s = (j.values ? c.v_scale : c.k_scale)[j.row];
     const int8_t* pool = (j.values ? c.values : c.keys) + j.row * c.P * c.D;
-    const int pitch = c.P + 16;
-    if (j.values) {
-        const int p0 = j.held / 16, np = (j.held + j.m + 15) / 16 - p0;
-        for (int i = threadIdx.x; i < np * c.D; i += kThreads) {
-            const int d = i / np, t0 = 16 * (p0 + i % np);
-            *reinterpret_cast<uint4*>(tile + d * pitch + t0) =
-                *reinterpret_cast<const uint4*>(pool + (int64_t)d * c.P + t0);
-        }
-        __syncthreads();
-    }
-    for (int i = threadIdx.x; i < j.m * chunks; i += kThreads) {
-        const int tok = i / chunks, d = 8 * (i % chunks);
-        union { uint2 w; int8_t b[8]; } u;
-        if (j.values) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) u.b[q] = tile[(d + q) * pitch + j.held + tok];
-        } else {
+    if (!j.values) {
+#pragma unroll 4
+        for (int i = threadIdx.x; i < j.m * chunks; i += kThreads) {
+            const int tok = i / chunks, d = 8 * (i % chunks);
+            union { uint2 w; int8_t b[8]; } u;
             u.w = *reinterpret_cast<const uint2*>(pool + (int64_t)(j.held + tok) * c.D + d);
-        }
-        float e[8];
+            float e[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) e[q] = (float)u.b[q] * s;
-        Store8<E>::put(y + (int64_t)tok * out.st + d, e);
+            for (int q = 0; q < 8; ++q) e[q] = (float)u.b[q] * s;
+            store8(y + (int64_t)tok * out.st + d, e);
+        }
+        return;
+    }
+    const int pitch = tile_pitch(c.P) / 4;
+    const int p0 = j.held / 16, np = (j.held + j.m + 15) / 16 - p0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < np * c.D; i += kThreads) {
+        const int d = i / np, t0 = 16 * (p0 + i % np);
+        const uint4 w = *reinterpret_cast<const uint4*>(pool + (int64_t)d * c.P + t0);
+        uint32_t* to = tile + d * pitch + t0 / 4;
+        to[0] = w.x;
+        to[1] = w.y;
+        to[2] = w.z;
+        to[3] = w.w;
+    }
+    __syncthreads();
+    const int g0 = j.held / 4, n = ((j.held + j.m + 3) / 4 - g0) * chunks;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const int g = g0 + i / chunks, tok = 4 * g - j.held, d = 8 * (i % chunks);
+        uint32_t word[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p) word[p] = tile[(d + p) * pitch + g];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (tok + q < 0 || tok + q >= j.m) continue;
+            float e[8];
+#pragma unroll
+            for (int p = 0; p < 8; ++p) e[p] = (float)(int8_t)(word[p] >> (8 * q)) * s;
+            store8(y + (int64_t)(tok + q) * out.st + d, e);
+        }
     }
 }
 

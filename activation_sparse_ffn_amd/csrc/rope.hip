@@ -16,8 +16,8 @@
 // bytes) in registers.
 #include <type_traits>
 
+#include "attn_common.hpp"
 #include "attn_launch.hpp"
-#include "common.hpp"
 
 namespace sffn {
 
@@ -28,15 +28,6 @@ constexpr int kThreads = 256;
 template <typename E> __device__ __forceinline__ float to_f32(E v);
 template <> __device__ __forceinline__ float to_f32<uint16_t>(uint16_t v) { return bf16_to_f32(v); }
 template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
-
-__device__ __forceinline__ void store8(uint16_t* p, const float* v) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-}
-__device__ __forceinline__ void store8(float* p, const float* v) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
 
 template <int LH>
 __device__ __forceinline__ float group_sum(float v) {
@@ -108,10 +99,19 @@ __device__ __forceinline__ size_t at(const Heads& v, int64_t t, int h) {
     return (size_t)(t * v.st + (int64_t)h * v.sh);
 }
 
+// Row of head h (q's heads, then k's) of token t in the views of q and k.
+template <typename E>
+__device__ __forceinline__ E* row_of(const RopeArgs& a, const Heads& q, const Heads& k, int64_t t, int h) {
+    const bool is_q = h < a.n_q;
+    return static_cast<E*>(is_q ? q.p : k.p) + (is_q ? at(q, t, h) : at(k, t, h - a.n_q));
+}
+
 // ---------------------------------------------------------------------------
 // forward, 16-byte accesses: D and the strides multiples of eight, R of 16
 // (half layout) or 8 (interleaved), 16-byte aligned data. Group g of the grid
-// takes heads s, s + per, ... of token t, where g = t per + s.
+// takes heads s, s + per, ... of token t, where g = t per + s, the next head's
+// load in flight. (Four heads' loads at once cost more in waves than they gave:
+// 24.9 against 22.4 us for a 4096-token chunk of 40 heads of 128.)
 // ---------------------------------------------------------------------------
 template <typename E, int LH>
 __global__ __launch_bounds__(kThreads) void k_rope(const RopeArgs a, int per) {
@@ -129,15 +129,16 @@ __global__ __launch_bounds__(kThreads) void k_rope(const RopeArgs a, int per) {
         ok = pos >= 0 && pos < a.max_pos;
         ang = load_angles(a, ok ? pos : 0, c8, 1.f);
     }
+    Raw<E> next;
+    if (have) next.load(row_of<E>(a, a.q, a.k, t, s) + 8 * c8);
     for (int h = s; h < heads; h += per) {
         const bool is_q = h < a.n_q;
-        const int hh = is_q ? h : h - a.n_q;
-        const Heads& in = is_q ? a.q : a.k;
-        const Heads& out = is_q ? a.q_out : a.k_out;
+        const Raw<E> raw = next;
+        if (have && h + per < heads) next.load(row_of<E>(a, a.q, a.k, t, h + per) + 8 * c8);
         float n[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) n[i] = 0.f;
-        if (have) Elem<E>::load8(static_cast<const E*>(in.p) + at(in, t, hh) + 8 * c8, n);
+        if (have) raw.decode(n);
         if (a.norm) {
             float w[8];
 #pragma unroll
@@ -155,7 +156,7 @@ __global__ __launch_bounds__(kThreads) void k_rope(const RopeArgs a, int per) {
         if (!ok)
 #pragma unroll
             for (int i = 0; i < 8; ++i) n[i] = __builtin_nanf("");
-        if (have) store8(static_cast<E*>(out.p) + at(out, t, hh) + 8 * c8, n);
+        if (have) store8(row_of<E>(a, a.q_out, a.k_out, t, h) + 8 * c8, n);
     }
 }
 
@@ -192,20 +193,23 @@ __global__ __launch_bounds__(kThreads) void k_rope_backward(const RopeArgs a, in
             ok = pos >= 0 && pos < a.max_pos;
             ang = load_angles(a, ok ? pos : 0, c8, -1.f);
         }
+        Raw<E> next_g, next_x;
+        auto load = [&](int h) {
+            if (!have) return;
+            next_g.load(row_of<E>(a, a.g_q, a.g_k, t, h) + 8 * c8);
+            if (a.norm) next_x.load(row_of<E>(a, a.q, a.k, t, h) + 8 * c8);
+        };
+        load((int)(g - t * per));
         for (int h = (int)(g - t * per); h < heads; h += per) {
             const bool is_q = h < a.n_q;
-            const int hh = is_q ? h : h - a.n_q;
-            const Heads& gin = is_q ? a.g_q : a.g_k;
-            const Heads& out = is_q ? a.q_out : a.k_out;
+            const Raw<E> raw_g = next_g, raw_x = next_x;
+            if (h + per < heads) load(h + per);
             float gn[8], x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) gn[i] = x[i] = 0.f;
             if (have) {
-                Elem<E>::load8(static_cast<const E*>(gin.p) + at(gin, t, hh) + 8 * c8, gn);
-                if (a.norm) {
-                    const Heads& in = is_q ? a.q : a.k;
-                    Elem<E>::load8(static_cast<const E*>(in.p) + at(in, t, hh) + 8 * c8, x);
-                }
+                raw_g.decode(gn);
+                if (a.norm) raw_x.decode(x);
             }
             turn<LH>(a, ang, c8, gn);
             if (!ok)
@@ -229,7 +233,7 @@ __global__ __launch_bounds__(kThreads) void k_rope_backward(const RopeArgs a, in
 #pragma unroll
                 for (int i = 0; i < 8; ++i) gn[i] = r * (gn[i] - x[i] * m);
             }
-            if (have) store8(static_cast<E*>(out.p) + at(out, t, hh) + 8 * c8, gn);
+            if (have) store8(row_of<E>(a, a.q_out, a.k_out, t, h) + 8 * c8, gn);
         }
     }
     if (!a.norm || !a.partial) return;
@@ -248,21 +252,34 @@ __global__ __launch_bounds__(kThreads) void k_rope_backward(const RopeArgs a, in
     }
 }
 
-// Columns of partial [n, 2 D] summed: 16 threads a column, each every 16th row,
-// joined in order.
-__global__ __launch_bounds__(kThreads) void k_rope_sum(const float* __restrict__ partial, int n, int D, float* g_qw,
-                                                       float* g_kw) {
-    __shared__ float lds[16][17];
+// Columns of partial [n, 2 D] summed: 64 threads a column, each every 64th row
+// with eight loads in flight, joined in order. (With 16 threads a column and one
+// load at a time the 1024 rows of a 4096-token chunk took 20 us, now 4.6.)
+constexpr int kSumRows = 64;
+
+__global__ __launch_bounds__(16 * kSumRows) void k_rope_sum(const float* __restrict__ partial, int n, int D,
+                                                            float* g_qw, float* g_kw) {
+    __shared__ float lds[kSumRows][17];
     const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
     const int col = blockIdx.x * 16 + c;
     float sum = 0.f;
-    if (col < 2 * D)
-        for (int i = r; i < n; i += 16) sum += partial[(size_t)i * 2 * D + col];
+    if (col < 2 * D && r < n)
+        sum = sum_splits_in_order(partial + (size_t)r * 2 * D + col, (n - r + kSumRows - 1) / kSumRows,
+                                  (int64_t)kSumRows * 2 * D);
     lds[r][c] = sum;
+    __syncthreads();
+    if (r < 8) {
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kSumRows / 8; ++i) sum += lds[r + 8 * i][c];
+    }
+    __syncthreads();
+    if (r < 8) lds[r][c] = sum;
     __syncthreads();
     if (r == 0 && col < 2 * D) {
         sum = 0.f;
-        for (int i = 0; i < 16; ++i) sum += lds[i][c];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += lds[i][c];
         float* to = col < D ? g_qw : g_kw;
         if (to) to[col < D ? col : col - D] = sum;
     }
@@ -460,7 +477,7 @@ hipError_t launch_rope_backward(const RopeArgs& a, hipStream_t s) {
     if (!wide(a)) e = launch_any<true>(a, s);
     else e = a.dt == Dt::BF16 ? launch_wide_backward<uint16_t>(a, s) : launch_wide_backward<float>(a, s);
     if (e != hipSuccess || !a.norm || !a.partial) return e;
-    k_rope_sum<<<dim3((2 * a.D + 15) / 16), kThreads, 0, s>>>(a.partial, (int)backward_blocks(a), a.D, a.g_qw, a.g_kw);
+    k_rope_sum<<<dim3((2 * a.D + 15) / 16), 16 * kSumRows, 0, s>>>(a.partial, (int)backward_blocks(a), a.D, a.g_qw, a.g_kw);
     return hipGetLastError();
 }
 
