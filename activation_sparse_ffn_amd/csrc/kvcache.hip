@@ -24,7 +24,6 @@ namespace sffn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxPage = 128, kMaxDim = 256;
 
 // What one workgroup works on: the call's tokens that lie in one page.
 struct PageJob {
@@ -73,29 +72,68 @@ __device__ __forceinline__ int8_t requantise(int8_t q, float ratio) {
     return (int8_t)(int)rintf((float)q * ratio);
 }
 
-// rint(x / s), clamped. The quotient is taken as x (1 / s), which is within 2^-22
-// of it, and by a division only where that could round the other way.
-__device__ __forceinline__ int quantise(float x, float s, float inverse, bool divide) {
-    const float t = x * inverse;
-    float q = rintf(t);
-    if (divide || fabsf(t - q) > 0.4999f) q = rintf(x / s);
-    return (int)fminf(fmaxf(q, -127.f), 127.f);
+// rint(x / s) of eight values, |x| <= 127 s but for the rounding of s, in the low
+// bytes of b. x (1 / s) + 1.5 2^23 holds the rounded quotient in its low bits; 1 /
+// s is within 2^-24 of itself, so that is rint(x / s) unless the quotient lies
+// within 2^-15 of a half. Where one of the eight does (or s is so small that 1 / s
+// might overflow; the quotient may then pass 127 too) all eight are divided.
+__device__ __forceinline__ void quantise8(const float* x, float s, float inverse, uint32_t* b) {
+    const float magic = 12582912.f;
+    float off = 0.f;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        const float y = __builtin_fmaf(x[p], inverse, magic);
+        off = fmaxf(off, fabsf(__builtin_fmaf(x[p], inverse, magic - y)));
+        b[p] = __float_as_uint(y);
+    }
+    if (off > 0.4999f || s < 1e-30f) {
+#pragma unroll
+        for (int p = 0; p < 8; ++p) b[p] = (uint32_t)(int)fminf(fmaxf(rintf(x[p] / s), -127.f), 127.f);
+    }
+}
+
+// The low bytes of four words as one.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0c0c0400u), hi = __builtin_amdgcn_perm(d, c, 0x04000c0cu);
+    return lo | hi;
 }
 
 // LDS row pitch of the values' tile [D][P], in bytes: one word more than the
 // page, so that the rows of eight channels apart lie in other banks.
 __device__ __forceinline__ int tile_pitch(int P) { return P + 4; }
-constexpr int kTileBytes = kMaxDim * (kMaxPage + 4);
+// It is allotted at the launch, for the cache's own sizes: with room for the
+// largest page and head four workgroups would fill a compute unit, and the 65
+// pages of a chunk that starts inside one (1040 workgroups) take two rounds.
+inline size_t tile_bytes(const CacheArgs& c) { return (size_t)c.D * (c.P + 4); }
+
+// The largest |x| of eight elements, as the bits of an fp32.
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t raw_most(const Raw<uint16_t>& r) {
+    const uint32_t w[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
+    return (uint32_t)max(m.x, m.y) << 16;
+}
+__device__ __forceinline__ uint32_t raw_most(const Raw<float>& r) {
+    const float x[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+    return m;
+}
 
 template <typename E>
 __global__ __launch_bounds__(kThreads) void k_cache_append(const CacheArgs c, const Heads k, const Heads v,
                                                            int per_seq) {
     __shared__ uint32_t wave_max[kThreads / 64];
-    __shared__ uint32_t tile[kTileBytes / 4];       // values: new entries, four tokens a word
+    extern __shared__ uint32_t tile[];      // values: new entries, four tokens a word
     PageJob j;
     if (!page_job(c, per_seq, j) || !j.known) return;
     const Heads& in = j.values ? v : k;
     const E* x = static_cast<const E*>(in.p) + (j.t0 * in.st + (int64_t)j.h * in.sh);
+    float* scale = (j.values ? c.v_scale : c.k_scale) + j.row;
+    const float old = *scale;
     // piece i: slots 4 g .. 4 g + 3 of the page, channels 8 (i % chunks) ..
     const int chunks = c.D / 8, g0 = j.held / 4, n = ((j.held + j.m + 3) / 4 - g0) * chunks;
     auto load = [&](int i, Raw<E>* raw) {
@@ -113,10 +151,7 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(const CacheArgs c, co
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             if (tok + q < 0 || tok + q >= j.m) continue;
-            float e[8];
-            raw[q].decode(e);
-#pragma unroll
-            for (int p = 0; p < 8; ++p) most = max(most, __float_as_uint(e[p]) & 0x7fffffffu);
+            most = max(most, raw_most(raw[q]));
         }
     };
     Raw<E> first[4];        // the thread's first piece: its only one for 64 tokens of 128 channels
@@ -132,8 +167,6 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(const CacheArgs c, co
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) most = max(most, (uint32_t)__shfl_xor((int)most, o, 64));
     if ((threadIdx.x & 63) == 0) wave_max[threadIdx.x >> 6] = most;
-    float* scale = (j.values ? c.v_scale : c.k_scale) + j.row;
-    const float old = *scale;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kThreads / 64; ++w) most = max(most, wave_max[w]);
@@ -152,7 +185,6 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(const CacheArgs c, co
     // (the barrier above is behind every thread's read of the old scale)
     if (threadIdx.x == 0) *scale = s;
     const bool regrown = ratio < 1.f;
-    const bool divide = s < 1e-30f;         // 1 / s might overflow
     const float inverse = 1.f / s;
 
     int8_t* pool = (j.values ? c.values : c.keys) + j.row * c.P * c.D;
@@ -167,29 +199,21 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(const CacheArgs c, co
         }
     auto round = [&](int i, const Raw<E>* raw) {
         const int g = g0 + i / chunks, tok = 4 * g - j.held, d = 8 * (i % chunks);
-        uint32_t word[8] = {};              // of each channel: its four tokens
+        uint32_t b[4][8] = {};  // zeros under a scale of 0 (a maximum too small for one) or NaN
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             if (tok + q < 0 || tok + q >= j.m) continue;
             float e[8];
             raw[q].decode(e);
-            uint32_t b[8];
-#pragma unroll
-            for (int p = 0; p < 8; ++p)
-                // a scale of 0 (a maximum too small for one) or NaN holds zeros
-                b[p] = s > 0.f ? (uint32_t)quantise(e[p], s, inverse, divide) & 255u : 0u;
-            if (!j.values) {
-                const uint2 w = make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24,
-                                           b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
-                *reinterpret_cast<uint2*>(pool + (int64_t)(4 * g + q) * c.D + d) = w;
-            } else {
-#pragma unroll
-                for (int p = 0; p < 8; ++p) word[p] |= b[p] << (8 * q);
-            }
+            if (s > 0.f) quantise8(e, s, inverse, b[q]);
+            if (!j.values)
+                *reinterpret_cast<uint2*>(pool + (int64_t)(4 * g + q) * c.D + d) =
+                    make_uint2(low_bytes(b[q][0], b[q][1], b[q][2], b[q][3]),
+                               low_bytes(b[q][4], b[q][5], b[q][6], b[q][7]));
         }
         if (j.values)
 #pragma unroll
-            for (int p = 0; p < 8; ++p) tile[(d + p) * pitch + g] = word[p];
+            for (int p = 0; p < 8; ++p) tile[(d + p) * pitch + g] = low_bytes(b[0][p], b[1][p], b[2][p], b[3][p]);
     };
     if ((int)threadIdx.x < n) round(threadIdx.x, first);
     for (int i = threadIdx.x + kThreads; i < n; i += kThreads) {
@@ -206,8 +230,12 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(const CacheArgs c, co
     for (int i = threadIdx.x; i < np * c.D; i += kThreads) {
         const int d = i / np, t0 = 16 * (p0 + i % np);
         int8_t* to = pool + (int64_t)d * c.P + t0;
-        uint4 was = make_uint4(0, 0, 0, 0);
-        if (t0 < j.held || t0 + 16 > end) was = *reinterpret_cast<const uint4*>(to);
+        const uint32_t* from = tile + d * pitch + t0 / 4;
+        if (t0 >= j.held && t0 + 16 <= end) {
+            *reinterpret_cast<uint4*>(to) = make_uint4(from[0], from[1], from[2], from[3]);
+            continue;
+        }
+        const uint4 was = *reinterpret_cast<const uint4*>(to);
         uint32_t w[4] = {was.x, was.y, was.z, was.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -226,7 +254,7 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(const CacheArgs c, co
 #pragma unroll
             for (int p = 0; p < 4; ++p)
                 if (t + p >= j.held && t + p < end) fresh |= 255u << (8 * p);
-            if (fresh != 0) w[q] = (w[q] & ~fresh) | (tile[d * pitch + t / 4] & fresh);
+            if (fresh != 0) w[q] = (w[q] & ~fresh) | (from[q] & fresh);
         }
         *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
     }
@@ -235,7 +263,7 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(const CacheArgs c, co
 template <typename E>
 __global__ __launch_bounds__(kThreads) void k_cache_read(const CacheArgs c, const Heads k, const Heads v,
                                                          int per_seq) {
-    __shared__ uint32_t tile[kTileBytes / 4];       // values: the page's rows [D][P]
+    extern __shared__ uint32_t tile[];      // values: the page's rows [D][P]
     PageJob j;
     if (!page_job(c, per_seq, j)) return;
     const Heads& out = j.values ? v : k;
@@ -300,16 +328,16 @@ __global__ __launch_bounds__(kThreads) void k_cache_read(const CacheArgs c, cons
 hipError_t launch_cache_append(const CacheArgs& c, const Heads& k, const Heads& v, hipStream_t s) {
     const int per_seq = (int)pages_touched(c.max_new, c.P);
     const dim3 grid((unsigned)cache_copy_blocks(c));
-    if (c.dt == Dt::BF16) k_cache_append<uint16_t><<<grid, kThreads, 0, s>>>(c, k, v, per_seq);
-    else k_cache_append<float><<<grid, kThreads, 0, s>>>(c, k, v, per_seq);
+    if (c.dt == Dt::BF16) k_cache_append<uint16_t><<<grid, kThreads, tile_bytes(c), s>>>(c, k, v, per_seq);
+    else k_cache_append<float><<<grid, kThreads, tile_bytes(c), s>>>(c, k, v, per_seq);
     return hipGetLastError();
 }
 
 hipError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v, hipStream_t s) {
     const int per_seq = (int)pages_touched(c.max_new, c.P);
     const dim3 grid((unsigned)cache_copy_blocks(c));
-    if (c.dt == Dt::BF16) k_cache_read<uint16_t><<<grid, kThreads, 0, s>>>(c, k, v, per_seq);
-    else k_cache_read<float><<<grid, kThreads, 0, s>>>(c, k, v, per_seq);
+    if (c.dt == Dt::BF16) k_cache_read<uint16_t><<<grid, kThreads, tile_bytes(c), s>>>(c, k, v, per_seq);
+    else k_cache_read<float><<<grid, kThreads, tile_bytes(c), s>>>(c, k, v, per_seq);
     return hipGetLastError();
 }
 
