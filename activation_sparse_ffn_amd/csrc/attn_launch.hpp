@@ -60,11 +60,13 @@ hipError_t launch_cache_append(const CacheArgs& c, const Heads& k, const Heads& 
 hipError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v, hipStream_t s);
 
 // ---- attention over the cache -----------------------------------------------------
-// How one call is cut up: row tiles of `rows` (token, head) rows for each
-// sequence and key head, and `splits` ranges of `chunk` keys (the last one
-// open) whose partial results a second kernel joins.
+// How one call is cut up. Few rows (every sequence's fit a tile of 16): `blocks`
+// workgroups share the work evenly and a row has up to `splits` parts. Otherwise:
+// row tiles of `rows` (token, head) rows for each sequence and key head, and
+// `splits` ranges of `chunk` keys (the last one open). With more than one split
+// partial results go to the workspace and a second kernel joins them.
 struct AttnPlan {
-    bool few;                       // the 16-row kernel: every sequence's rows fit one tile
+    bool few;
     int waves;                      // of the row-tile kernel's workgroups (32 rows each)
     int rows, splits;
     int64_t row_tiles, chunk, blocks;
@@ -85,16 +87,24 @@ inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
         if (seen < span) span = seen;
     }
     const int64_t whole = (int64_t)c.B * c.Hkv * p.row_tiles;
-    const int64_t want = (int64_t)compute_units() * (p.few ? 16 : 2), least = 512;
-    int64_t splits = whole > 0 ? want / whole : 1;
-    const int64_t most_splits = (span + least - 1) / least;
-    if (splits > most_splits) splits = most_splits;
-    if (splits < 1) splits = 1;
-    const int64_t unit = p.few ? 256 : 64;
-    p.chunk = ((span + splits - 1) / splits + unit - 1) / unit * unit;
-    p.splits = (int)((span + p.chunk - 1) / p.chunk);
-    p.blocks = whole * p.splits;
-    if (p.splits > 1) p.ws_bytes = (size_t)c.T * Hq * p.splits * (c.D + 2) * 4;
+    if (p.few) {
+        // no share is less than 8 steps of 64 keys (see k_attend_few); the chip
+        // holds one workgroup a compute unit of the largest kinds, else two
+        const int64_t steps = (span + 63) / 64, held = c.D > 128 || c.dt == Dt::F32 ? 1 : 2;
+        p.splits = steps <= 8 ? 1 : (int)(steps / 8 + 2);
+        const int64_t most_blocks = whole * ((steps + 7) / 8);
+        p.blocks = (int64_t)compute_units() * held;
+        if (most_blocks < p.blocks) p.blocks = most_blocks;
+    } else {
+        int64_t splits = whole > 0 ? (int64_t)compute_units() * 2 / whole : 1;
+        const int64_t most_splits = (span + 511) / 512;
+        if (splits > most_splits) splits = most_splits;
+        if (splits < 1) splits = 1;
+        p.chunk = ((span + splits - 1) / splits + 63) / 64 * 64;
+        p.splits = (int)((span + p.chunk - 1) / p.chunk);
+        p.blocks = whole * p.splits;
+    }
+    if (p.splits > 1) p.ws_bytes = (size_t)c.T * Hq * ((size_t)p.splits * (c.D + 2) + 1) * 4;
     return p;
 }
 

@@ -40,60 +40,90 @@ struct AttnArgs {
     bool negate;
     float* lse;             // [T, Hq] or null
     float* part_o;          // [T Hq, splits, D], unnormalised
+    int* parts;             // [T Hq]: parts of each row (few rows: as many as its keys' shares)
     float2* part_ml;        // [T Hq, splits]: reference maximum (base 2), sum; see row_inverse
 };
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_huge_valf(); }
 
-// The rows and keys of one workgroup. Positions fit 31 bits (the host bounds
-// the table's capacity and the call's tokens).
-struct Work {
+// The new tokens of a sequence. Positions fit 31 bits (the host bounds the
+// table's capacity and the call's tokens).
+struct Sequence {
     int first;              // first token of the sequence's in the call
     int p0;                 // position of that token
-    int rows;               // (token, head) rows of the sequence and key head
-    int r0;                 // first row of this tile
-    int k0, k1;             // keys of this split
-    int b, h, split;
+    int64_t rows;           // (token, head) rows of the sequence and a key head
 };
 
+// False when the sequence has no new tokens.
+__device__ __forceinline__ bool find_sequence(const AttnArgs& a, int b, Sequence& q) {
+    const CacheArgs& c = a.c;
+    int last = b + 1;
+    q.first = b;
+    if (c.cu) {
+        q.first = c.cu[b];
+        last = c.cu[b + 1];
+    }
+    if (q.first < 0 || last > c.T || last <= q.first) return false;
+    const int n = last - q.first, capacity = c.max_pages << c.shift;
+    int L = c.lens[b];
+    if (L < 0) L = 0;
+    // more tokens than the table has room for: every row sees one of no page
+    if (L > capacity) L = capacity + n;
+    q.p0 = L - n;
+    q.rows = (int64_t)(n < c.max_new ? n : c.max_new) * a.G;
+    return true;
+}
+
+// Keys [lo, hi) that rows r0 .. r1 - 1 of a sequence see, lo a multiple of kTile.
+__device__ __forceinline__ void keys_seen(const AttnArgs& a, const Sequence& q, int r0, int r1, int& lo, int& hi) {
+    hi = q.p0 + (r1 - 1) / a.G + 1;
+    lo = 0;
+    if (a.window > 0) {
+        const int64_t from = (int64_t)q.p0 + r0 / a.G - a.window + 1;
+        if (from > 0) lo = (int)from / kTile * kTile;
+    }
+    if (hi < lo) hi = lo;
+}
+
+// The rows and keys of one piece of work.
+struct Work {
+    int first, p0;          // as in Sequence
+    int rows;
+    int r0;                 // first row of this tile
+    int k0, k1;             // keys
+    int b, h;
+    int part;               // of the rows' parts
+};
+
+// Work of a workgroup of k_attend_rows: a row tile and a range of a.chunk keys.
 // False when the tile has no rows.
 __device__ __forceinline__ bool find_work(const AttnArgs& a, int tile_rows, Work& w) {
     const CacheArgs& c = a.c;
     uint32_t id = blockIdx.x;
     w.h = (int)(id % (uint32_t)c.Hkv);
     id /= (uint32_t)c.Hkv;
-    w.b = (int)(id % (uint32_t)c.B);
+    const uint32_t turn = id % (uint32_t)c.B;
     id /= (uint32_t)c.B;
-    w.split = (int)(id % (uint32_t)a.splits);
+    w.part = (int)(id % (uint32_t)a.splits);
     id /= (uint32_t)a.splits;
     const int tile = a.row_tiles - 1 - (int)id;     // the longest rows first
-    int last = w.b + 1;
-    w.first = w.b;
-    if (c.cu) {
-        w.first = c.cu[w.b];
-        last = c.cu[w.b + 1];
-    }
-    if (w.first < 0 || last > c.T || last <= w.first) return false;
-    const int n = last - w.first, capacity = c.max_pages << c.shift;
-    int L = c.lens[w.b];
-    if (L < 0) L = 0;
-    // more tokens than the table has room for: every row sees one of no page
-    if (L > capacity) L = capacity + n;
-    w.p0 = L - n;
-    const int64_t rows = (int64_t)(n < c.max_new ? n : c.max_new) * a.G, r0 = (int64_t)tile * tile_rows;
-    if (r0 >= rows) return false;
-    w.rows = (int)rows;
+    // Workgroup i runs on XCD i % 8: heads stay with their XCD's cache where there
+    // are eight of them, and the sequences change places from tile to tile, so that
+    // one long sequence among short ones does not fall to some XCDs alone.
+    w.b = (int)((turn + (uint32_t)tile) % (uint32_t)c.B);
+    Sequence q;
+    if (!find_sequence(a, w.b, q)) return false;
+    const int64_t r0 = (int64_t)tile * tile_rows;
+    if (r0 >= q.rows) return false;
+    w.first = q.first;
+    w.p0 = q.p0;
+    w.rows = (int)q.rows;
     w.r0 = (int)r0;
-    const int r1 = w.rows - w.r0 < tile_rows ? w.rows : w.r0 + tile_rows;
-    const int hi = w.p0 + (r1 - 1) / a.G + 1;
-    int lo = 0;
-    if (a.window > 0) {
-        const int64_t from = (int64_t)w.p0 + w.r0 / a.G - a.window + 1;
-        if (from > 0) lo = (int)from;
-    }
-    const int64_t k0 = lo / kTile * kTile + (int64_t)w.split * a.chunk;
+    int lo, hi;
+    keys_seen(a, q, w.r0, w.rows - w.r0 < tile_rows ? w.rows : w.r0 + tile_rows, lo, hi);
+    const int64_t k0 = lo + (int64_t)w.part * a.chunk;
     w.k0 = (int)(k0 < hi ? k0 : hi);
-    w.k1 = w.split == a.splits - 1 || hi < k0 + a.chunk ? hi : w.k0 + a.chunk;
+    w.k1 = w.part == a.splits - 1 || hi < k0 + a.chunk ? hi : (int)k0 + a.chunk;
     return true;
 }
 
@@ -223,13 +253,10 @@ __device__ __forceinline__ float row_lse(float M, float l, bool seen) {
 //     lane's 16-byte load of a value row [d][16 g ..] is two steps' operand.
 // ---------------------------------------------------------------------------
 template <typename E, int NP, int PP, int D>
-__global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few(const AttnArgs a) {
+__device__ __forceinline__ void attend_few(const AttnArgs& a, const Work& w, int parts, float (*sm)[16],
+                                           float (*sl)[16], float (*so)[16][D + 4]) {
     constexpr int KC = D / 64, DT = D / 16;
-    __shared__ float sm[4][16], sl[4][16];
-    __shared__ __align__(16) float so[4][16][D + 4];
     const CacheArgs& c = a.c;
-    Work w;
-    if (!find_work(a, 16, w)) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int g = lane >> 4, n = lane & 15, gk = n >> 2;
     const bool valid = w.r0 + n < w.rows;
@@ -354,6 +381,7 @@ __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few
 
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
+    __syncthreads();        // the work before has been read from LDS
     if (g == 0) {
         sm[wave][n] = m;
         sl[wave][n] = l;
@@ -385,7 +413,7 @@ __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few
     const int tok2 = r2 / a.G, head2 = w.h * a.G + r2 - tok2 * a.G;
     const int64_t row = (int64_t)(w.first + tok2) * a.Hq + head2;
     const bool seen = row_sees(w.p0 + tok2, a.window, w.k0, w.k1);
-    if (a.splits == 1) {
+    if (parts == 1) {
         const float inv = row_inverse(sum, seen);
         E* out = static_cast<E*>(a.out.p) + ((int64_t)(w.first + tok2) * a.out.st + head2 * a.out.sh) + d0;
 #pragma unroll
@@ -394,10 +422,135 @@ __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few
         for (int d = 0; d < D / 16; d += 4) store4(out + d, acc + d);
         if (a.lse && d0 == 0) a.lse[row] = row_lse(M, sum, seen);
     } else {
-        const int64_t part = row * a.splits + w.split;
+        const int64_t part = row * a.splits + w.part;
 #pragma unroll
         for (int d = 0; d < D / 16; d += 4) store4(a.part_o + part * D + d0 + d, acc + d);
         if (d0 == 0) a.part_ml[part] = make_float2(M, sum == 0.f && seen ? -1.f : sum);
+    }
+    if (a.splits > 1 && w.part == 0 && d0 == 0) a.parts[row] = parts;
+}
+
+// v of lane l, the same in every lane
+__device__ __forceinline__ int lane_value(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
+
+// Sum (or largest, of values >= 0) of lanes 0 .. l, in lane l: within rows of 16
+// lanes, then across them.
+template <typename Op>
+__device__ __forceinline__ int wave_scan(int v, Op op) {
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));   // row_shr:1
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));   // row_shr:2
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));   // row_shr:4
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));   // row_shr:8
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));   // row_bcast:15
+    return op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));    // row_bcast:31
+}
+
+// The work of all sequences and heads in a row, cut into equal shares of the
+// grid's workgroups (as many as the chip holds at once): lengths are known on the
+// device alone, and a grid for the longest would be nearly all empty for ragged
+// ones (at 32 sequences of 1 .. 32768 keys: 86 us so, of which the empty workgroups
+// of finer ranges took more than those gave). In steps of 64 keys, a sequence and
+// head costs its steps, but at least kLeast: what beginning and ending one takes.
+// Those of at most kLeast steps, or all where nothing joins parts, go whole to the
+// workgroup in whose share they begin.
+constexpr int kLeast = 8;
+
+template <typename E, int NP, int PP, int D>
+__global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few(const AttnArgs a) {
+    __shared__ float sm[4][16], sl[4][16];
+    __shared__ __align__(16) float so[4][16][D + 4];
+    const int lane = threadIdx.x & 63;
+    const int B = a.c.B, Hkv = a.c.Hkv;
+    // 64 sequences from b0 on, one a lane: where they are, their steps (0: no rows)
+    // and the cost of them up to the lane's. (The host has seen to it that the cost
+    // of all fits 31 bits.)
+    struct Lane {
+        Sequence q;
+        int lo, hi, steps, cost;
+    };
+    auto padded = [&](int steps) { return steps > kLeast ? steps : kLeast; };
+    auto look = [&](int b0) {
+        Lane x;
+        x.steps = 0;
+        x.lo = x.hi = 0;
+        if (b0 + lane < B && find_sequence(a, b0 + lane, x.q)) {
+            keys_seen(a, x.q, 0, (int)x.q.rows, x.lo, x.hi);
+            x.steps = x.hi - x.lo > kTile ? (x.hi - x.lo + kTile - 1) / kTile : 1;
+        }
+        x.cost = wave_scan(x.steps > 0 ? padded(x.steps) * Hkv : 0, [](int p, int q) { return p + q; });
+        return x;
+    };
+    Lane x = look(0);
+    auto longest_of = [&](const Lane& y) {
+        return lane_value(wave_scan(y.steps, [](int p, int q) { return p > q ? p : q; }), 63);
+    };
+    int total = lane_value(x.cost, 63), longest = longest_of(x);
+    for (int b0 = 64; b0 < B; b0 += 64) {
+        const Lane y = look(b0);
+        const int l = longest_of(y);
+        total += lane_value(y.cost, 63);
+        longest = l > longest ? l : longest;
+    }
+    int share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+    if (share < kLeast) share = kLeast;
+    // no more parts than the workspace has room for
+    if (a.splits > 1 && share < longest / (a.splits - 1) + 1) share = longest / (a.splits - 1) + 1;
+    if ((int64_t)blockIdx.x * share >= total) return;
+    const int c0 = (int)blockIdx.x * share, c1 = total - c0 > share ? c0 + share : total;
+
+    // the sequence in whose cost c0 lies
+    int start = 0, b0 = 0;                  // start: cost before the 64, then before sequence and head
+    while (start + lane_value(x.cost, 63) <= c0) {
+        start += lane_value(x.cost, 63);
+        b0 += 64;
+        x = look(b0);
+    }
+    int at = __ffsll((unsigned long long)__ballot(start + x.cost > c0)) - 1;
+    int steps = lane_value(x.steps, at);
+    start += lane_value(x.cost, at) - padded(steps) * Hkv;
+    int h = (c0 - start) / padded(steps);
+    start += h * padded(steps);
+    while (start < c1) {
+        int from = 0, to = steps, part = 0, parts = 1;
+        if (a.splits == 1 || steps <= kLeast) {
+            if (start < c0) to = 0;         // another workgroup's
+        } else {
+            if (start < c0) {
+                from = c0 - start;
+                part = (c0 - start + share - 1) / share;
+                parts = part + 1;           // more than one: that is all the others have to know
+            }
+            if (c1 - start < steps) {
+                to = c1 - start;
+                parts = part + 2 + (steps - 1 - to) / share;
+            }
+        }
+        if (from < to) {
+            const int lo = lane_value(x.lo, at);
+            Work w;
+            w.first = lane_value(x.q.first, at);
+            w.p0 = lane_value(x.q.p0, at);
+            w.rows = lane_value((int)x.q.rows, at);
+            w.r0 = 0;
+            w.k0 = lo + from * kTile;
+            w.k1 = to == steps ? lane_value(x.hi, at) : lo + to * kTile;
+            w.b = b0 + at;
+            w.h = h;
+            w.part = part;
+            attend_few<E, NP, PP, D>(a, w, parts, sm, sl, so);
+        }
+        start += padded(steps);
+        if (++h < Hkv) continue;
+        h = 0;
+        do {
+            if (b0 + ++at >= B) return;
+            if (at == 64) {
+                at = 0;
+                b0 += 64;
+                x = look(b0);
+            }
+            steps = lane_value(x.steps, at);
+        } while (steps == 0);
     }
 }
 
@@ -739,7 +892,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     const int64_t row = (int64_t)(w.first + tok) * a.Hq + head;
     const bool seen = row_sees(pos, a.window, w.k0, w.k1);
     const float inv = a.splits == 1 ? row_inverse(l, seen) : 1.f;
-    const int64_t part = row * a.splits + w.split;
+    const int64_t part = row * a.splits + w.part;
     E* out = static_cast<E*>(a.out.p) + ((int64_t)(w.first + tok) * a.out.st + head * a.out.sh);
 #pragma unroll
     for (int i = 0; i < DT; ++i)
@@ -751,8 +904,12 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
             else store4(a.part_o + part * D + d, v);
         }
     if (half != 0) return;
-    if (a.splits > 1) a.part_ml[part] = make_float2(m, l == 0.f && seen ? -1.f : l);
-    else if (a.lse) a.lse[row] = row_lse(m, l, seen);
+    if (a.splits > 1) {
+        a.part_ml[part] = make_float2(m, l == 0.f && seen ? -1.f : l);
+        if (w.part == 0) a.parts[row] = a.splits;
+    } else if (a.lse) {
+        a.lse[row] = row_lse(m, l, seen);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -778,13 +935,15 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a) {
         const int first = a.c.cu[lo], last = a.c.cu[hi];
         if (first < 0 || last > a.c.T || t < first || t >= last || t - first >= a.c.max_new) return;
     }
+    const int parts = a.parts[row];
+    if (parts == 1) return;     // written at once
     const float2* ml = a.part_ml + (int64_t)row * a.splits;
     float M = neg_inf();
-    for (int s = lane; s < a.splits; s += 64) M = fmaxf(M, ml[s].x);
+    for (int s = lane; s < parts; s += 64) M = fmaxf(M, ml[s].x);
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor(M, o, 64));
     float sum = 0.f, marks = 0.f;
-    for (int s = lane; s < a.splits; s += 64) {
+    for (int s = lane; s < parts; s += 64) {
         const float2 p = ml[s];
         const float f = part_factor(p.x, p.y, M);
         if (f != 0.f) sum += f * p.y;
@@ -795,14 +954,14 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a) {
     const int cg = threadIdx.x % CG, sg = threadIdx.x / CG;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     const float4* o = reinterpret_cast<const float4*>(a.part_o + (int64_t)row * a.splits * D) + cg;
-    for (int s = sg; s < a.splits; s += 4 * SG) {
+    for (int s = sg; s < parts; s += 4 * SG) {
         float f[4];
         float4 v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int si = s + i * SG;
             f[i] = 0.f;
-            if (si < a.splits) {
+            if (si < parts) {
                 const float2 p = ml[si];
                 f[i] = part_factor(p.x, p.y, M);
             }
@@ -885,8 +1044,10 @@ hipError_t launch_cache_attention(const CacheArgs& c, const AttnPlan& plan, cons
     a.negate = scale < 0.f;
     a.lse = lse;
     if (plan.splits > 1) {
-        a.part_ml = static_cast<float2*>(ws);
-        a.part_o = static_cast<float*>(ws) + (size_t)c.T * Hq * plan.splits * 2;
+        const size_t rows = (size_t)c.T * Hq;
+        a.part_o = static_cast<float*>(ws);
+        a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * plan.splits * c.D);
+        a.parts = reinterpret_cast<int*>(a.part_ml + rows * plan.splits);
     }
     return c.dt == Dt::BF16 ? launch_dim<uint16_t, 1>(a, plan, s) : launch_dim<float, 3>(a, plan, s);
 }
