@@ -452,7 +452,9 @@ __device__ __forceinline__ int wave_scan(int v, Op op) {
 // of finer ranges took more than those gave). In steps of 64 keys, a sequence and
 // head costs its steps, but at least kLeast: what beginning and ending one takes.
 // Those of at most kLeast steps, or all where nothing joins parts, go whole to the
-// workgroup in whose share they begin.
+// workgroup in whose share they begin. Where there are workgroups enough, every
+// sequence and head begins a share of its own (cost rounded up to shares), so that
+// no workgroup has the end of one and the beginning of the next one after another.
 constexpr int kLeast = 8;
 
 template <typename E, int NP, int PP, int D>
@@ -468,22 +470,29 @@ __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few
         Sequence q;
         int lo, hi, steps, cost;
     };
-    auto padded = [&](int steps) { return steps > kLeast ? steps : kLeast; };
-    auto look = [&](int b0) {
-        Lane x;
-        x.steps = 0;
-        x.lo = x.hi = 0;
-        if (b0 + lane < B && find_sequence(a, b0 + lane, x.q)) {
-            keys_seen(a, x.q, 0, (int)x.q.rows, x.lo, x.hi);
-            x.steps = x.hi - x.lo > kTile ? (x.hi - x.lo + kTile - 1) / kTile : 1;
-        }
-        x.cost = wave_scan(x.steps > 0 ? padded(x.steps) * Hkv : 0, [](int p, int q) { return p + q; });
-        return x;
+    int round_to = 0;           // 0: costs as they are, else rounded up to multiples of it
+    auto padded = [&](int steps) {
+        if (round_to > 0) return (steps + round_to - 1) / round_to * round_to;
+        return steps > kLeast ? steps : kLeast;
     };
-    Lane x = look(0);
+    auto sum_costs = [&](Lane& y) {
+        y.cost = wave_scan(y.steps > 0 ? padded(y.steps) * Hkv : 0, [](int p, int q) { return p + q; });
+    };
+    auto look = [&](int b0) {
+        Lane y;
+        y.steps = 0;
+        y.lo = y.hi = 0;
+        if (b0 + lane < B && find_sequence(a, b0 + lane, y.q)) {
+            keys_seen(a, y.q, 0, (int)y.q.rows, y.lo, y.hi);
+            y.steps = y.hi - y.lo > kTile ? (y.hi - y.lo + kTile - 1) / kTile : 1;
+        }
+        sum_costs(y);
+        return y;
+    };
     auto longest_of = [&](const Lane& y) {
         return lane_value(wave_scan(y.steps, [](int p, int q) { return p > q ? p : q; }), 63);
     };
+    Lane x = look(0);
     int total = lane_value(x.cost, 63), longest = longest_of(x);
     for (int b0 = 64; b0 < B; b0 += 64) {
         const Lane y = look(b0);
@@ -495,6 +504,18 @@ __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few
     if (share < kLeast) share = kLeast;
     // no more parts than the workspace has room for
     if (a.splits > 1 && share < longest / (a.splits - 1) + 1) share = longest / (a.splits - 1) + 1;
+    if (B <= 64 && B * Hkv <= (int)gridDim.x && total < 1 << 29) {
+        round_to = share;
+        const int unrounded = x.cost;
+        sum_costs(x);
+        const int rounded = lane_value(x.cost, 63);
+        if (rounded / share > (int)gridDim.x) {
+            round_to = 0;
+            x.cost = unrounded;
+        } else {
+            total = rounded;
+        }
+    }
     if ((int64_t)blockIdx.x * share >= total) return;
     const int c0 = (int)blockIdx.x * share, c1 = total - c0 > share ? c0 + share : total;
 
@@ -913,18 +934,21 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
 }
 
 // ---------------------------------------------------------------------------
-// Joins the splits of a row: a workgroup per row; a thread takes four channels
-// of every SG-th split (four loads in flight), the SG sums meet in LDS in a
-// fixed order. A sum of -1 marks a split whose keys were seen but all scored
-// -inf. Tokens of no sequence, or beyond its first max_new, have no parts and
+// Joins the parts of a row: a workgroup per row; a thread takes four channels of
+// every SG-th part (four loads in flight), the SG sums meet in LDS in a fixed
+// order. A sum of -1 marks a part whose keys were seen but all scored -inf. Tokens of no sequence, or beyond its first max_new, have no parts and
 // are left alone.
 // ---------------------------------------------------------------------------
 template <typename E, int D>
 __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a) {
-    constexpr int CG = D / 4, SG = 256 / CG;
+    constexpr int CG = D / 4, SG = 256 / CG, IN = 4;
     __shared__ float4 so[SG][CG];
     const int lane = threadIdx.x & 63;
     const int row = blockIdx.x, t = row / a.Hq;
+    // loaded before it is known whether the row has parts
+    const float2* ml = a.part_ml + (int64_t)row * a.splits;
+    const int parts = a.parts[row];
+    const float2 mine = lane < a.splits ? ml[lane] : make_float2(0.f, 0.f);
     if (a.c.cu) {
         int lo = 0, hi = a.c.B;             // cu[lo] <= t < cu[hi], where t is in a sequence
         while (hi - lo > 1) {
@@ -935,46 +959,43 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a) {
         const int first = a.c.cu[lo], last = a.c.cu[hi];
         if (first < 0 || last > a.c.T || t < first || t >= last || t - first >= a.c.max_new) return;
     }
-    const int parts = a.parts[row];
     if (parts == 1) return;     // written at once
-    const float2* ml = a.part_ml + (int64_t)row * a.splits;
-    float M = neg_inf();
-    for (int s = lane; s < parts; s += 64) M = fmaxf(M, ml[s].x);
+    const int cg = threadIdx.x % CG, sg = threadIdx.x / CG;
+    const float4* o = reinterpret_cast<const float4*>(a.part_o + (int64_t)row * a.splits * D) + cg;
+    float4 v[IN];
+    auto load = [&](int s) {
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor(M, o, 64));
+        for (int i = 0; i < IN; ++i)
+            if (s + i * SG < parts) v[i] = o[(int64_t)(s + i * SG) * CG];
+    };
+    load(sg);                   // in flight during the sums over the parts
+
+    float M = lane < parts ? mine.x : neg_inf();
+    for (int s = lane + 64; s < parts; s += 64) M = fmaxf(M, ml[s].x);
+#pragma unroll
+    for (int w = 32; w >= 1; w >>= 1) M = fmaxf(M, __shfl_xor(M, w, 64));
     float sum = 0.f, marks = 0.f;
     for (int s = lane; s < parts; s += 64) {
-        const float2 p = ml[s];
+        const float2 p = s == lane ? mine : ml[s];
         const float f = part_factor(p.x, p.y, M);
         if (f != 0.f) sum += f * p.y;
         else if (p.y < 0.f) marks = 1.f;
     }
     sum = wave_sum(sum);
     marks = wave_sum(marks);
-    const int cg = threadIdx.x % CG, sg = threadIdx.x / CG;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4* o = reinterpret_cast<const float4*>(a.part_o + (int64_t)row * a.splits * D) + cg;
-    for (int s = sg; s < parts; s += 4 * SG) {
-        float f[4];
-        float4 v[4];
+    for (int s = sg; s < parts; s += IN * SG) {
+        if (s != sg) load(s);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int si = s + i * SG;
-            f[i] = 0.f;
-            if (si < parts) {
-                const float2 p = ml[si];
-                f[i] = part_factor(p.x, p.y, M);
-            }
-            // a split that counts nothing may never have been written
-            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (f[i] != 0.f) v[i] = o[(int64_t)si * CG];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            acc.x += f[i] * v[i].x;
-            acc.y += f[i] * v[i].y;
-            acc.z += f[i] * v[i].z;
-            acc.w += f[i] * v[i].w;
+        for (int i = 0; i < IN; ++i) {
+            if (s + i * SG >= parts) break;
+            const float2 p = ml[s + i * SG];
+            const float f = part_factor(p.x, p.y, M);
+            if (f == 0.f) continue;         // what counts nothing may hold anything
+            acc.x += f * v[i].x;
+            acc.y += f * v[i].y;
+            acc.z += f * v[i].z;
+            acc.w += f * v[i].w;
         }
     }
     so[sg][cg] = acc;
@@ -982,18 +1003,18 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a) {
     const int h = row - t * a.Hq;
     const float inv = row_inverse(sum, marks != 0.f);
     if (threadIdx.x < CG) {
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        float r[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < SG; ++i) {
             const float4 p = so[i][threadIdx.x];
-            v[0] += p.x;
-            v[1] += p.y;
-            v[2] += p.z;
-            v[3] += p.w;
+            r[0] += p.x;
+            r[1] += p.y;
+            r[2] += p.z;
+            r[3] += p.w;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] *= inv;
-        store4(static_cast<E*>(a.out.p) + ((int64_t)t * a.out.st + h * a.out.sh) + 4 * threadIdx.x, v);
+        for (int i = 0; i < 4; ++i) r[i] *= inv;
+        store4(static_cast<E*>(a.out.p) + ((int64_t)t * a.out.st + h * a.out.sh) + 4 * threadIdx.x, r);
     }
     if (a.lse && threadIdx.x == 0) a.lse[row] = row_lse(M, sum, marks != 0.f);
 }
