@@ -68,6 +68,7 @@ hipError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v,
 struct AttnPlan {
     bool few;
     int waves;                      // of the row-tile kernel's workgroups (32 rows each)
+    int pieces;                     // bf16 pieces of the weights of a bf16 q there
     int rows, splits;
     int64_t row_tiles, chunk, blocks;
     size_t ws_bytes;                // 0 with one split
@@ -78,6 +79,7 @@ inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
     const int64_t G = Hq / c.Hkv, most = (int64_t)c.max_new * G;
     p.few = most <= 16;
     p.waves = c.D > 128 || c.dt == Dt::F32 || most <= 128 ? 4 : 8;
+    p.pieces = most <= 128 ? 2 : 1;
     p.rows = p.few ? 16 : 32 * p.waves;
     p.row_tiles = (most + p.rows - 1) / p.rows;
     // keys that one row tile sees: all, or the window of its tokens

@@ -7,7 +7,10 @@
 // cores (fp32 accumulation) loses nothing; the page's scale multiplies the
 // fp32 score, and the value's scale the weight p before it is rounded to bf16
 // (p sv, so that a page of small values keeps its relative precision). An fp32
-// q is taken as three bf16 pieces (24 bits), and so are the weights.
+// q is taken as three bf16 pieces (24 bits), and so are the weights. For a bf16 q
+// the weights are two pieces where few rows leave the matrix cores idle, and one
+// (2^-9 of each weight, as much as the result's own rounding) for long chunks,
+// where a second would cost a third more of the time's main part.
 //
 // Both kernels compute S^T = K Q^T and O^T = V^T P^T, which keeps a query row
 // in one matrix column: the lane that holds scores of a row holds that row's
@@ -603,7 +606,7 @@ __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few
 // 16 bytes: a read's sixteen consecutive rows then start in other banks (68 and
 // 36 words apart), and every address of a step is one lane's base and a constant.
 // ---------------------------------------------------------------------------
-template <typename E, int NP, int D, int NW>
+template <typename E, int NP, int PP, int D, int NW>
 __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) void k_attend_rows(const AttnArgs a) {
     constexpr int NT = 64 * NW, KS = D / 16, DT = D / 32;
     constexpr int CH = (4 * D + NT - 1) / NT;           // 16-byte pieces a thread loads of keys, and of values
@@ -734,7 +737,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
         for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
     float m = neg_inf(), l = 0.f;
 
-    bf16x8 pf[2][2][NP];
+    bf16x8 pf[2][2][PP];
     f32x16 s[2];
     // Phase M of the step at t0: O += P V of the tile before (in buffer `buf` ^ 1;
     // not in the first step), S = K Q of this one and the staging (not in what
@@ -774,7 +777,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
                 const int i = g * GS + j;
                 if (i < NV) {
 #pragma unroll
-                    for (int p = 0; p < NP; ++p)
+                    for (int p = 0; p < PP; ++p)
                         o[i % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
                             f[g & 1][j], pf[i / (2 * DT)][i / DT % 2][p], o[i % DT], 0, 0, 0);
                 } else {
@@ -796,12 +799,6 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
                         load_values(i, t0 + kTile);
                     }
                 }
-            // one product, then a share of the arithmetic, four times
-#pragma unroll
-            for (int j = 0; j < GS; ++j) {
-                __builtin_amdgcn_sched_group_barrier(0x8, NP, 0);
-                __builtin_amdgcn_sched_group_barrier(0x2, 7, 0);
-            }
             __builtin_amdgcn_sched_barrier(0);
         }
         if (with_keys.value) {
@@ -878,7 +875,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
                     pv[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[tt][8 * u + e], f[tt].x, shift));
                     sum += pv[e];
                 }
-                pieces<NP>(pv, pf[tt][u]);
+                pieces<PP>(pv, pf[tt][u]);
             }
             l += sum * f[tt].z;
         }
@@ -888,7 +885,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int p = 0; p < NP; ++p)
+                    for (int p = 0; p < PP; ++p)
                         if (f[tt].w > 0.f) pf[tt][u][p] = __builtin_bit_cast(bf16x8, make_uint4(0, 0, 0, 0));
         }
     };
@@ -1025,11 +1022,12 @@ hipError_t launch(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
     if (plan.few) {
         k_attend_few<E, NP, NP == 1 ? 2 : 3, D><<<grid, 256, 0, s>>>(a);
     } else {
-        if constexpr (D <= 128 && NP == 1) {
-            if (plan.waves == 8) k_attend_rows<E, NP, D, 8><<<grid, 512, 0, s>>>(a);
-            else k_attend_rows<E, NP, D, 4><<<grid, 256, 0, s>>>(a);
+        if constexpr (NP == 3) {
+            k_attend_rows<E, 3, 3, D, 4><<<grid, 256, 0, s>>>(a);
         } else {
-            k_attend_rows<E, NP, D, 4><<<grid, 256, 0, s>>>(a);
+            if (plan.pieces == 2) k_attend_rows<E, 1, 2, D, 4><<<grid, 256, 0, s>>>(a);
+            else if constexpr (D <= 128) k_attend_rows<E, 1, 1, D, 8><<<grid, 512, 0, s>>>(a);
+            else k_attend_rows<E, 1, 1, D, 4><<<grid, 256, 0, s>>>(a);
         }
     }
     hipError_t e = hipGetLastError();
