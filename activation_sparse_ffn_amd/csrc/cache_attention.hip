@@ -49,6 +49,9 @@ struct AttnArgs {
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_huge_valf(); }
 
+// v of lane l, the same in every lane
+__device__ __forceinline__ int lane_value(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
+
 // The new tokens of a sequence. Positions fit 31 bits (the host bounds the
 // table's capacity and the call's tokens).
 struct Sequence {
@@ -103,17 +106,37 @@ struct Work {
 __device__ __forceinline__ bool find_work(const AttnArgs& a, int tile_rows, Work& w) {
     const CacheArgs& c = a.c;
     uint32_t id = blockIdx.x;
+    // Workgroup i runs on XCD i % 8: heads stay with their XCD's cache where there
+    // are eight of them.
     w.h = (int)(id % (uint32_t)c.Hkv);
     id /= (uint32_t)c.Hkv;
-    const uint32_t turn = id % (uint32_t)c.B;
-    id /= (uint32_t)c.B;
-    w.part = (int)(id % (uint32_t)a.splits);
-    id /= (uint32_t)a.splits;
-    const int tile = a.row_tiles - 1 - (int)id;     // the longest rows first
-    // Workgroup i runs on XCD i % 8: heads stay with their XCD's cache where there
-    // are eight of them, and the sequences change places from tile to tile, so that
-    // one long sequence among short ones does not fall to some XCDs alone.
-    w.b = (int)((turn + (uint32_t)tile) % (uint32_t)c.B);
+    int tile;
+    if (c.B <= 64) {
+        // the longest sequences first, and of each the longest rows: what begins
+        // last is short. (With the sequences taking turns a chunk of 1500 tokens
+        // over 6001 keys among five shorter ones took 303 us.)
+        w.part = (int)(id % (uint32_t)a.splits);
+        id /= (uint32_t)a.splits;
+        tile = a.row_tiles - 1 - (int)(id % (uint32_t)a.row_tiles);
+        const int place = (int)(id / (uint32_t)a.row_tiles);
+        const int lane = threadIdx.x & 63;
+        const int length = lane < c.B ? c.lens[lane] : 0;
+        int before = 0;
+        for (int j = 0; j < c.B; ++j) {
+            const int other = lane_value(length, j);
+            before += other > length || (other == length && j < lane);
+        }
+        w.b = __ffsll((unsigned long long)__ballot(lane < c.B && before == place)) - 1;
+    } else {
+        const uint32_t turn = id % (uint32_t)c.B;
+        id /= (uint32_t)c.B;
+        w.part = (int)(id % (uint32_t)a.splits);
+        id /= (uint32_t)a.splits;
+        tile = a.row_tiles - 1 - (int)id;
+        // the sequences change places from tile to tile, so that a long one among
+        // short ones does not fall to some XCDs alone
+        w.b = (int)((turn + (uint32_t)tile) % (uint32_t)c.B);
+    }
     Sequence q;
     if (!find_sequence(a, w.b, q)) return false;
     const int64_t r0 = (int64_t)tile * tile_rows;
@@ -432,9 +455,6 @@ __device__ __forceinline__ void attend_few(const AttnArgs& a, const Work& w, int
     }
     if (a.splits > 1 && w.part == 0 && d0 == 0) a.parts[row] = parts;
 }
-
-// v of lane l, the same in every lane
-__device__ __forceinline__ int lane_value(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
 
 // Sum (or largest, of values >= 0) of lanes 0 .. l, in lane l: within rows of 16
 // lanes, then across them.
