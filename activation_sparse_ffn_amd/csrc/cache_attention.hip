@@ -226,6 +226,16 @@ __device__ __forceinline__ void pieces(const float* x, bf16x8* out) {
     }
 }
 
+// x by a power of two (exact, unless it leaves bf16's range), 0 or what is not finite.
+__device__ __forceinline__ bf16x8 times(bf16x8 x, float by) {
+    const uint4 w = __builtin_bit_cast(uint4, x);
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    uint32_t out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[i] = round2(bf16_lo(in[i]) * by, bf16_hi(in[i]) * by);
+    return __builtin_bit_cast(bf16x8, make_uint4(out[0], out[1], out[2], out[3]));
+}
+
 template <typename E, int NP>
 __device__ __forceinline__ void load_q(const E* p, bool valid, bool negate, bf16x8* out) {
     float x[8];
@@ -633,8 +643,11 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     constexpr int KP = 2 * D + 16, VP = 2 * kTile + 16; // row pitches in bytes
     constexpr int KB = kTile * KP, BUF = KB + D * VP;   // bytes of the keys, of one buffer
     __shared__ __align__(16) char lds[2 * BUF];
-    // of each 16 keys: the key scale (with the softmax's), log2 of the value
-    // scale, its reciprocal, and whether it is 0 (or too small for a logarithm)
+    // of each 16 keys: the key scale (with the softmax's), and of the value scale
+    // the logarithm (base 2) and the reciprocal of one factor, and the other factor.
+    // The first goes into the exponent, so it may not take weights that count to
+    // where fp32 ends: scales far from 1 are a mantissa and a power of two there,
+    // all others themselves and 1.
     __shared__ float4 scales[2][4];
     const CacheArgs& c = a.c;
     Work w;
@@ -715,9 +728,13 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     auto stage_scales = [&](int buf) {
         if (wave == 0 && tid < 4) {
             const float ks = known ? ks_in * a.scale2 : __builtin_nanf(""), vs = known ? vs_in : __builtin_nanf("");
-            const bool none = fabsf(vs) < 1.1754944e-38f;
-            scales[buf][tid] = make_float4(ks, none ? 0.f : __builtin_amdgcn_logf(vs),
-                                           none ? 1.f : __builtin_amdgcn_rcpf(vs), none ? 1.f : 0.f);
+            float first = vs, rest = 1.f;
+            if (vs < 0x1p-64f || vs > 0x1p100f) {
+                const bool finite = vs > 0.f && vs < __builtin_huge_valf();
+                first = finite ? 2.f * __builtin_amdgcn_frexp_mantf(vs) : 1.f;
+                rest = finite ? __builtin_amdgcn_ldexpf(1.f, __builtin_amdgcn_frexp_expf(vs) - 1) : vs;
+            }
+            scales[buf][tid] = make_float4(ks, __builtin_amdgcn_logf(first), __builtin_amdgcn_rcpf(first), rest);
         }
     };
     // LDS written by this wave is visible after it; loads stay in flight
@@ -845,8 +862,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     // goes through it like the others (all keys are hidden): few tiles of a row
     // tile are such, and every wave meets every barrier.
     auto phase_v = [&](int buf, int t0) {
-        // the value scale vs goes into the exponent, p vs = 2^(x + log2 vs),
-        // and comes out of the sum of each 16 keys again
+        // the value scale (its first factor) goes into the exponent, p vs =
+        // 2^(x + log2 vs), and comes out of the sum of each 16 keys again
         float4 f[2];
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) f[tt] = scales[buf][2 * tt + half];
@@ -862,7 +879,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
                     s[tt][j] = key > up || key <= dn ? neg_inf() : s[tt][j] * f[tt].x;
                 }
                 f[tt].x = 1.f;
-                if (32 * tt > up || 32 * tt + 15 <= dn) f[tt] = make_float4(1.f, 0.f, 0.f, 0.f);
+                if (32 * tt > up || 32 * tt + 15 <= dn) f[tt] = make_float4(1.f, 0.f, 0.f, 1.f);
             }
         }
         float top[2];
@@ -899,14 +916,13 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
             }
             l += sum * f[tt].z;
         }
-        if (__any(f[0].w + f[1].w > 0.f)) {
+        if (__any(f[0].w != 1.f || f[1].w != 1.f)) {
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int p = 0; p < PP; ++p)
-                        if (f[tt].w > 0.f) pf[tt][u][p] = __builtin_bit_cast(bf16x8, make_uint4(0, 0, 0, 0));
+                    for (int p = 0; p < PP; ++p) pf[tt][u][p] = times(pf[tt][u][p], f[tt].w);
         }
     };
     if (w.k0 < w.k1) {
@@ -953,8 +969,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
 // ---------------------------------------------------------------------------
 // Joins the parts of a row: a workgroup per row; a thread takes four channels of
 // every SG-th part (four loads in flight), the SG sums meet in LDS in a fixed
-// order. A sum of -1 marks a part whose keys were seen but all scored -inf. Tokens of no sequence, or beyond its first max_new, have no parts and
-// are left alone.
+// order. A sum of -1 marks a part whose keys were seen but all scored -inf. Tokens
+// of no sequence, or beyond its first max_new, have no parts and are left alone.
 // ---------------------------------------------------------------------------
 template <typename E, int D>
 __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a) {

@@ -274,6 +274,30 @@ def test_zero_and_tiny_scales():
     compare(o, lse, ao.attend(q.double().cpu().numpy(), k, v, 99, 0.125), BF)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("scale", [2e-38, 1e-36, 1e-30, 1e-19, 1e28, 1e36])
+@pytest.mark.parametrize("new,H", [([1, 3], 4), ([20, 33], 4), ([70, 90], 4)])
+def test_value_scales_far_from_one(new, H, scale, dtype):
+    """Every second page's values are scaled far down (or up): the statistics, which
+    do not know the values, stay what they are, and so does every output that is
+    finite in fp32 before it is divided."""
+    s = Setup([300, 210], 2, 64, 16, 4)
+    s.v_scale[::2] = scale
+    q = queries(sum(new), H, 64, dtype, 5)
+    o, lse = s.sffn.cache_attention(s.cache(), s.batch(new), q, return_lse=True)
+    torch.cuda.synchronize()
+    refs, at = [], 0
+    for b, m in enumerate(new):
+        k, v = s.tokens(b)
+        refs.append(ao.attend(q[at:at + m].double().cpu().numpy(), k, v, s.kv[b] - m, 0.125))
+        at += m
+    ref = [np.concatenate(x) for x in zip(*refs)]
+    if scale > 1e35:
+        assert (np.abs(lse.double().cpu().numpy() - ref[1]) <= 2.0 ** -17 + 2.0 ** -19 * ref[3]).all()
+    else:
+        compare(o, lse, ref, dtype)
+
+
 def test_offsets_beyond_32_bits():
     """Pages behind 4 GiB of keys and of values."""
     import activation_sparse_ffn_amd as sffn
