@@ -192,17 +192,20 @@ __device__ __forceinline__ int before_seen(int p, int t0, int window) {
     return d < -1 ? -1 : (int)d;
 }
 
-// Eight int8 as bf16 (exact).
-__device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
-    uint32_t w[4];
+// Four int8 as bf16 (exact).
+__device__ __forceinline__ uint2 widen4(uint32_t from) {
+    uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t from = i < 2 ? lo : hi;
-        const float x = (float)(int8_t)(from >> (16 * (i & 1)));
-        const float y = (float)(int8_t)(from >> (16 * (i & 1) + 8));
+    for (int i = 0; i < 2; ++i) {
+        const float x = (float)(int8_t)(from >> (16 * i));
+        const float y = (float)(int8_t)(from >> (16 * i + 8));
         w[i] = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
     }
-    return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+    return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
+    const uint2 a = widen4(lo), b = widen4(hi);
+    return __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, b.x, b.y));
 }
 
 // Eight fp32 as NP bf16 pieces: their sum is x to 8 NP bits.
@@ -620,9 +623,16 @@ __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few
 // that one wave of a SIMD keeps the matrix cores busy while the other computes
 // weights; barriers between phases hold them there. Counting phases, K(t) is
 // read in 2t and 2t + 1, V(t) in 2t + 2 and 2t + 3, the scales of t in 2t + 1 and
-// 2t + 2; the first four waves write their part of K(t + 1), V(t) and the scales
-// of t in phase 2t, the others theirs in 2t + 1: always after the last read of
-// what the (double) buffer held and before its first use.
+// 2t + 2; the first four waves write their part of K(t + 1) and V(t) in phase 2t,
+// the others theirs in 2t + 1, and one wave the scales of t in its phase V(t - 1),
+// 2t (2t - 1 where there are four waves): always after the last read of what the
+// (double) buffer held and before its first use.
+//
+// Bound by the matrix cores and by power: a step of eight waves takes 3620 cycles
+// of which the matrix cores are busy for 2050, and what shortens it lowers the
+// clock (1.8 to 2.1 GHz; with a cache of zeros, which costs less power, the same
+// cycles take 1.6 ms instead of 1.83). A chunk of 4096 tokens over 32768 keys, 32
+// heads of 128: 1.83 ms, 1.13 PF, 82% of what a product of 16384^3 reaches.
 //
 // What a wave loads lies in one page, so page entries and addresses are scalar.
 //
@@ -691,7 +701,10 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     auto value_pages = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) entry_v[i] = page_entry(c, table, t0 + 16 * ((wave + i * NW) * 64 / D & 3));
-        if (wave == 0 && tid < 4) entry_s = page_entry(c, c.table + (int64_t)w.b * c.table_stride, t0 + 16 * tid);
+    };
+    const bool scaler = wave == (NW == 8 ? 4 : 0) && lane < 4;
+    auto scale_pages = [&](int t0) {
+        if (scaler) entry_s = page_entry(c, c.table + (int64_t)w.b * c.table_stride, t0 + 16 * lane);
     };
     auto load_keys = [&](int i, int t0) {
         if (active(i))
@@ -704,11 +717,11 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
                                                     (t0 & (c.P - 1)) + off_v[i]);
     };
     auto load_scales = [&](int t0) {
-        if (wave == 0 && tid < 4) {
+        if (scaler) {
             const size_t srow = (size_t)page_in(c, entry_s) * c.Hkv + w.h;
             ks_in = c.k_scale[srow];
             vs_in = c.v_scale[srow];
-            known = known_page(c, entry_s, t0 + 16 * tid);
+            known = known_page(c, entry_s, t0 + 16 * lane);
         }
     };
     auto stage_keys = [&](int i, int buf) {
@@ -718,15 +731,8 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
             *reinterpret_cast<bf16x8*>(to + 16) = widen(kr[i].z, kr[i].w);
         }
     };
-    auto stage_values = [&](int i, int buf) {
-        if (active(i)) {
-            char* to = lds + buf * BUF + to_v[i];
-            *reinterpret_cast<bf16x8*>(to) = widen(vr[i].x, vr[i].y);
-            *reinterpret_cast<bf16x8*>(to + 16) = widen(vr[i].z, vr[i].w);
-        }
-    };
     auto stage_scales = [&](int buf) {
-        if (wave == 0 && tid < 4) {
+        if (scaler) {
             const float ks = known ? ks_in * a.scale2 : __builtin_nanf(""), vs = known ? vs_in : __builtin_nanf("");
             float first = vs, rest = 1.f;
             if (vs < 0x1p-64f || vs > 0x1p100f) {
@@ -734,7 +740,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
                 first = finite ? 2.f * __builtin_amdgcn_frexp_mantf(vs) : 1.f;
                 rest = finite ? __builtin_amdgcn_ldexpf(1.f, __builtin_amdgcn_frexp_expf(vs) - 1) : vs;
             }
-            scales[buf][tid] = make_float4(ks, __builtin_amdgcn_logf(first), __builtin_amdgcn_rcpf(first), rest);
+            scales[buf][lane] = make_float4(ks, __builtin_amdgcn_logf(first), __builtin_amdgcn_rcpf(first), rest);
         }
     };
     // LDS written by this wave is visible after it; loads stay in flight
@@ -745,9 +751,41 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     };
 
     const bool late = NW == 8 && wave >= 4;
+    // One of the 8 CH words (four entries) of a thread's share of the keys of the
+    // step after the one at t0 and of that step's values: to bf16, every second one
+    // into LDS with the one before it, the last of a piece followed by the load of
+    // the piece's next.
+    uint4 wide;
+    auto stage_word = [&](int i, int buf, int t0) {
+        const int piece = i / 4 % CH, part = i & 3;
+        if (!active(piece)) return;
+        const bool is_key = i < 4 * CH;
+        const uint4& from = is_key ? kr[piece] : vr[piece];
+        const uint2 v = widen4(part == 0 ? from.x : part == 1 ? from.y : part == 2 ? from.z : from.w);
+        if (part & 1) {
+            wide.z = v.x;
+            wide.w = v.y;
+            char* to = lds + (is_key ? (buf ^ 1) * BUF + to_k[piece] : buf * BUF + to_v[piece]);
+            *reinterpret_cast<uint4*>(to + 16 * (part >> 1)) = wide;
+        } else {
+            wide.x = v.x;
+            wide.y = v.y;
+        }
+        if (part == 3) {
+            if (is_key) load_keys(piece, t0 + 2 * kTile);
+            else load_values(piece, t0 + kTile);
+        }
+    };
+    // the scales of the step after the one at t0
+    auto next_scales = [&](int buf, int t0) {
+        stage_scales(buf);
+        load_scales(t0 + 2 * kTile);
+        scale_pages(t0 + 3 * kTile);
+    };
     if (w.k0 < w.k1) {
         key_pages(w.k0);
         value_pages(w.k0);
+        scale_pages(w.k0);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
             load_keys(i, w.k0);
@@ -756,6 +794,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
         load_scales(w.k0);
         key_pages(w.k0 + kTile);
         value_pages(w.k0 + kTile);
+        scale_pages(w.k0 + kTile);
     }
     bf16x8 qf[KS][NP];
     {
@@ -779,9 +818,13 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     // Phase M of the step at t0: O += P V of the tile before (in buffer `buf` ^ 1;
     // not in the first step), S = K Q of this one and the staging (not in what
     // follows the last step). The products go in groups of four (128 cycles):
-    // before each the operands of the next group are read from LDS, and into some
-    // of them goes a piece of the staging, whose arithmetic fits the issue slots
-    // that the products leave free. The phase has priority over the softmax of the
+    // before each the operands of the next group are read from LDS, and each takes
+    // its part of the staging, a word at a time: six instructions that fit the issue
+    // slots the products leave free (a piece of four words in one group held them
+    // up: phase M took 1840 cycles instead of 1500, the chunk 1845 us instead of
+    // 1830; moved into phase V the staging took longer still, 1885 to 2090). The
+    // scales are phase V's: a chain of loads, logarithm and store that in phase M
+    // delayed every wave by 250 cycles (1920 us instead of 1845). The phase has priority over the softmax of the
     // SIMD's other wave: a product that starts late is lost, a weight is not.
     auto phase_m = [&](auto with_values, auto with_keys, int buf, int t0) {
         constexpr int NV = with_values.value ? 4 * DT : 0, NK = with_keys.value ? 2 * KS : 0, N = NV + NK;
@@ -826,21 +869,11 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
             }
             if (with_keys.value)
 #pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    if (g == (2 * i + 1) * NG / (2 * CH + 1)) {
-                        stage_keys(i, buf ^ 1);
-                        load_keys(i, t0 + 2 * kTile);
-                    }
-                    if (g == (2 * i + 2) * NG / (2 * CH + 1)) {
-                        stage_values(i, buf);
-                        load_values(i, t0 + kTile);
-                    }
-                }
+                for (int i = 0; i < 8 * CH; ++i)
+                    if (g == i * NG / (8 * CH)) stage_word(i, buf, t0);
             __builtin_amdgcn_sched_barrier(0);
         }
         if (with_keys.value) {
-            stage_scales(buf);
-            load_scales(t0 + kTile);
             key_pages(t0 + 3 * kTile);
             value_pages(t0 + 2 * kTile);
         }
@@ -855,13 +888,18 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
             load_keys(i, w.k0 + kTile);
         }
         key_pages(w.k0 + 2 * kTile);
+        if (NW == 4) next_scales(0, w.k0 - kTile);
         phase_end();
-        if (late) phase_end();
+        if (late) {
+            next_scales(0, w.k0 - kTile);
+            phase_end();
+        }
     }
     // Phase V of the step at t0. A wave whose rows see none of the tile's keys
     // goes through it like the others (all keys are hidden): few tiles of a row
     // tile are such, and every wave meets every barrier.
     auto phase_v = [&](int buf, int t0) {
+        next_scales(buf ^ 1, t0);
         // the value scale (its first factor) goes into the exponent, p vs =
         // 2^(x + log2 vs), and comes out of the sum of each 16 keys again
         float4 f[2];
