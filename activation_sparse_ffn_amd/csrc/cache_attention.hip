@@ -817,18 +817,22 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     f32x16 s[2];
     // Phase M of the step at t0: O += P V of the tile before (in buffer `buf` ^ 1;
     // not in the first step), S = K Q of this one and the staging (not in what
-    // follows the last step). The products go in groups of four (128 cycles):
-    // before each the operands of the next group are read from LDS, and each takes
-    // its part of the staging, a word at a time: six instructions that fit the issue
-    // slots the products leave free (a piece of four words in one group held them
-    // up: phase M took 1840 cycles instead of 1500, the chunk 1845 us instead of
-    // 1830; moved into phase V the staging took longer still, 1885 to 2090). The
-    // scales are phase V's: a chain of loads, logarithm and store that in phase M
-    // delayed every wave by 250 cycles (1920 us instead of 1845). The phase has priority over the softmax of the
-    // SIMD's other wave: a product that starts late is lost, a weight is not.
+    // follows the last step). The products go in groups of two (64 cycles): before
+    // each the operands of the next group are read from LDS, and each takes its part
+    // of the staging, a word at a time: six instructions, which fit the issue slots
+    // that the products leave free. (Pieces of four words held the products up:
+    // phase M took 1840 cycles instead of 1500, the chunk above 1845 us instead of
+    // 1830; in phase V the staging took longer still, 1885 to 2090 us. Groups of four
+    // take 1% more.) The phase has priority over the softmax of the SIMD's other
+    // wave: a product that starts late is lost, a weight is not (without: 4% more).
+    //
+    // The scales are phase V's work: their chain of loads, logarithm and store
+    // delayed every wave by 250 cycles in phase M (1920 us instead of 1845). Where a
+    // SIMD has one wave they come last there, behind the arithmetic that needs no
+    // load (heads of 256, 4096 tokens over 8192 keys: 922 us instead of 1076).
     auto phase_m = [&](auto with_values, auto with_keys, int buf, int t0) {
         constexpr int NV = with_values.value ? 4 * DT : 0, NK = with_keys.value ? 2 * KS : 0, N = NV + NK;
-        constexpr int GS = 4, NG = N / GS;
+        constexpr int GS = 2, NG = N / GS;
         const char* vb = lds + (buf ^ 1) * BUF + KB + col * VP + 32 * half;
         const char* kb = lds + buf * BUF + col * KP + 16 * half;
         auto read = [&](int i) {
@@ -899,7 +903,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     // goes through it like the others (all keys are hidden): few tiles of a row
     // tile are such, and every wave meets every barrier.
     auto phase_v = [&](int buf, int t0) {
-        next_scales(buf ^ 1, t0);
+        if (NW == 8) next_scales(buf ^ 1, t0);
         // the value scale (its first factor) goes into the exponent, p vs =
         // 2^(x + log2 vs), and comes out of the sum of each 16 keys again
         float4 f[2];
@@ -962,6 +966,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
 #pragma unroll
                     for (int p = 0; p < PP; ++p) pf[tt][u][p] = times(pf[tt][u][p], f[tt].w);
         }
+        if (NW == 4) next_scales(buf ^ 1, t0);
     };
     if (w.k0 < w.k1) {
         phase_m(no, yes, 0, w.k0);
