@@ -29,6 +29,7 @@ __all__ = ["rope_table", "qk_norm_rope", "qk_norm_rope_backward", "KVCache", "Ca
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = (None, "linear", "ntk", "by_parts")
 _DTYPES = {torch.bfloat16: SFFN_BF16, torch.float32: SFFN_F32}
+_empty_strided = torch.empty_strided
 
 
 class _Heads(ctypes.Structure):
@@ -86,11 +87,12 @@ def declare(lib):
 # ---------------------------------------------------------------------------
 
 def _heads(t: Optional[torch.Tensor], name: str, shape=None, dtype=None, device=None):
-    """A [T, heads, head_dim] view on the GPU as the library takes it."""
-    if shape is None or type(t) is not torch.Tensor or t.shape != shape or t.dtype is not dtype or t.device != device \
-            or dtype not in _DTYPES or not t.is_cuda:
+    """A [T, heads, head_dim] view on the GPU as the library takes it. With a shape,
+    dtype is one of _DTYPES and device a GPU."""
+    if shape is None or type(t) is not torch.Tensor or t.shape != shape or t.dtype is not dtype or t.device != device:
         _check_heads(t, name, shape, dtype, device)
-    T, H, D = t.shape
+        shape = t.shape
+    T, H, D = shape
     st, sh, sd = t.stride()
     if sd != 1 and D > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
@@ -112,10 +114,16 @@ def _check_heads(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be on {device or 'the GPU'} (got {t.device})")
 
 
-def _new_heads(t: torch.Tensor):
-    """A contiguous [T, heads, head_dim] tensor made here."""
-    _, H, D = t.shape
-    return _Heads(t.data_ptr(), H * D, D)
+def _new(shape, dtype, device):
+    """A new contiguous [T, heads, head_dim] tensor and what the library takes of it.
+    (empty_strided is the shortest of torch's ways to one.)"""
+    _, H, D = shape
+    t = _empty_strided(shape, (H * D, D, 1), dtype=dtype, device=device)
+    return t, _Heads(t.data_ptr(), H * D, D)
+
+
+def _vector(n, dtype, device):
+    return _empty_strided((n,), (1,), dtype=dtype, device=device)
 
 
 def _address(t: torch.Tensor, name: str, shape, dtype, device) -> int:
@@ -227,14 +235,12 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional
     cfg, pos, tab, wq, wk = _rope_call(q, k, positions, table, q_weight, k_weight, norm, eps, layout)
     hko = None
     if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        ho = _new_heads(q_out)
+        q_out, ho = _new(q.shape, dtype, dev)
     else:
         ho = _heads(q_out, "q_out", q.shape, dtype, dev)
     if k is not None:
         if k_out is None:
-            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-            hko = _new_heads(k_out)
+            k_out, hko = _new(k.shape, dtype, dev)
         else:
             hko = _heads(k_out, "k_out", k.shape, dtype, dev)
     _check(lib, lib.qk_norm_rope(cfg, hq, hk, pos, tab, wq, wk, q.shape[0], ho, hko, _stream(dev)))
@@ -262,19 +268,18 @@ def qk_norm_rope_backward(q: Optional[torch.Tensor], k: Optional[torch.Tensor], 
         hq = _heads(q, "q", g_q.shape, dtype, dev)
         if g_k is not None:
             hk = _heads(k, "k", g_k.shape, dtype, dev)
-    gq = torch.empty_like(g_q, memory_format=torch.contiguous_format)
+    gq, hoq = _new(g_q.shape, dtype, dev)
     if g_k is not None:
-        gk = torch.empty_like(g_k, memory_format=torch.contiguous_format)
-        hok = _new_heads(gk)
+        gk, hok = _new(g_k.shape, dtype, dev)
     if wq is not None:
-        gwq = g_q.new_empty(D, dtype=torch.float32)
+        gwq = _vector(D, torch.float32, dev)
     if wk is not None:
-        gwk = g_q.new_empty(D, dtype=torch.float32)
+        gwk = _vector(D, torch.float32, dev)
     if gwq is not None or gwk is not None:
         need = lib.qk_norm_rope_backward_workspace_size(cfg, T)
-        ws = g_q.new_empty(need, dtype=torch.uint8) if need else None
+        ws = _vector(need, torch.uint8, dev) if need else None
     _check(lib, lib.qk_norm_rope_backward(
-        cfg, hq, hk, hg, hgk, pos, tab, wq, wk, T, _new_heads(gq), hok, _ptr(gwq), _ptr(gwk), _ptr(ws), need,
+        cfg, hq, hk, hg, hgk, pos, tab, wq, wk, T, hoq, hok, _ptr(gwq), _ptr(gwk), _ptr(ws), need,
         _stream(dev)))
     return {"q": gq, "k": gk, "q_weight": gwq, "k_weight": gwk}
 
@@ -350,11 +355,14 @@ def kv_cache_append(cache: KVCache, batch: CacheBatch, k: torch.Tensor, v: torch
     makes the scale of its page and head NaN."""
     lib = load_library()
     _same_device(cache, batch)
-    T, dtype = k.shape[0], k.dtype
+    dtype, dev = k.dtype, cache.device
+    if dtype not in _DTYPES:
+        _check_heads(k, "k", None, None, dev)
+    T = k.shape[0]
     shape = (T, cache.kv_heads, cache.head_dim)
-    hk = _heads(k, "k", shape, dtype, cache.device)
-    hv = _heads(v, "v", shape, dtype, cache.device)
-    _check(lib, lib.kv_cache_append(cache._c, batch._c, hk, hv, _DTYPES[dtype], T, _stream(cache.device)))
+    hk = _heads(k, "k", shape, dtype, dev)
+    hv = _heads(v, "v", shape, dtype, dev)
+    _check(lib, lib.kv_cache_append(cache._c, batch._c, hk, hv, _DTYPES[dtype], T, _stream(dev)))
 
 
 def kv_cache_read(cache: KVCache, batch: CacheBatch, total: int, dtype: torch.dtype = torch.bfloat16,
@@ -365,11 +373,17 @@ def kv_cache_read(cache: KVCache, batch: CacheBatch, total: int, dtype: torch.dt
     _same_device(cache, batch)
     if dtype not in _DTYPES:
         raise ValueError(f"dtype must be bfloat16 or float32 (got {dtype})")
+    dev = cache.device
     shape = (total, cache.kv_heads, cache.head_dim)
-    k = cache.keys.new_empty(shape, dtype=dtype) if k is None else k
-    v = cache.keys.new_empty(shape, dtype=dtype) if v is None else v
-    hk, hv = _heads(k, "k", shape, dtype, cache.device), _heads(v, "v", shape, dtype, cache.device)
-    _check(lib, lib.kv_cache_read(cache._c, batch._c, hk, hv, _DTYPES[dtype], total, _stream(cache.device)))
+    if k is None:
+        k, hk = _new(shape, dtype, dev)
+    else:
+        hk = _heads(k, "k", shape, dtype, dev)
+    if v is None:
+        v, hv = _new(shape, dtype, dev)
+    else:
+        hv = _heads(v, "v", shape, dtype, dev)
+    _check(lib, lib.kv_cache_read(cache._c, batch._c, hk, hv, _DTYPES[dtype], total, _stream(dev)))
     return k, v
 
 
@@ -384,23 +398,24 @@ def cache_attention(cache: KVCache, batch: CacheBatch, q: torch.Tensor, scale: O
     no key gives zeros and -inf."""
     lib = load_library()
     _same_device(cache, batch)
-    hq = _heads(q, "q", None, None, cache.device)
-    T, heads, D = q.shape
+    dev = cache.device
+    hq = _heads(q, "q", None, None, dev)
+    shape, dtype = q.shape, q.dtype
+    T, heads, D = shape
     if D != cache.head_dim:
         raise ValueError(f"q has heads of {D}, the cache of {cache.head_dim}")
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        ho = _new_heads(out)
+        out, ho = _new(shape, dtype, dev)
     else:
-        ho = _heads(out, "out", q.shape, q.dtype, cache.device)
-    lse = q.new_empty((T, heads), dtype=torch.float32) if return_lse else None
-    dt = _DTYPES[q.dtype]
+        ho = _heads(out, "out", shape, dtype, dev)
+    lse = _empty_strided((T, heads), (heads, 1), dtype=torch.float32, device=dev) if return_lse else None
+    dt = _DTYPES[dtype]
     if workspace is None:
         need = lib.cache_attention_workspace_size(cache._c, batch._c, heads, dt, window, T)
-        workspace = q.new_empty(need, dtype=torch.uint8) if need else None
+        workspace = _vector(need, torch.uint8, dev) if need else None
     else:
-        _need_buffer(workspace, "workspace", None, torch.uint8, cache.device)
+        _need_buffer(workspace, "workspace", None, torch.uint8, dev)
         need = workspace.numel()
     _check(lib, lib.cache_attention(cache._c, batch._c, hq, heads, dt, T, D ** -0.5 if scale is None else scale,
-                                    window, ho, _ptr(lse), _ptr(workspace), need, _stream(cache.device)))
+                                    window, ho, _ptr(lse), _ptr(workspace), need, _stream(dev)))
     return (out, lse) if return_lse else out
