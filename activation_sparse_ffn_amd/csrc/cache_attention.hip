@@ -279,7 +279,11 @@ __device__ __forceinline__ float row_lse(float M, float l, bool seen) {
 // Few rows (at most 16: single tokens, drafts): memory-bound, each key and value
 // is read once. Four waves take the split's 64-key steps in turn, each with its
 // own running softmax, straight from memory into matrix operands; they meet in
-// LDS at the end.
+// LDS at the end. The values of a step and the keys of the next are in flight while
+// it computes: 16 KB a wave of heads of 128, 33 MB over the chip, which its memory
+// needs to stream. One token over 32768 keys of 8 heads of 128 (67 MB): 18.6 us, of
+// which 13 are the bytes at a copy's rate; 32 ragged sequences (237 MB): 55.6 us,
+// 4.3 TB/s.
 //
 // v_mfma_f32_16x16x32_bf16: lane l holds operand row (A) or column (B) l % 16,
 // k = 8 (l / 16) .. + 7, and of the result column l % 16, rows 4 (l / 16) ..
@@ -484,8 +488,8 @@ __device__ __forceinline__ int wave_scan(int v, Op op) {
 // The work of all sequences and heads in a row, cut into equal shares of the
 // grid's workgroups (as many as the chip holds at once): lengths are known on the
 // device alone, and a grid for the longest would be nearly all empty for ragged
-// ones (at 32 sequences of 1 .. 32768 keys: 86 us so, of which the empty workgroups
-// of finer ranges took more than those gave). In steps of 64 keys, a sequence and
+// ones (32 sequences of 1 .. 32768 keys took 86 us so, 55.6 in even shares; finer
+// ranges cost more in empty workgroups than they gave). In steps of 64 keys, a sequence and
 // head costs its steps, but at least kLeast: what beginning and ending one takes.
 // Those of at most kLeast steps, or all where nothing joins parts, go whole to the
 // workgroup in whose share they begin. Where there are workgroups enough, every
@@ -630,9 +634,9 @@ __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few
 //
 // Bound by the matrix cores and by power: a step of eight waves takes 3620 cycles
 // of which the matrix cores are busy for 2050, and what shortens it lowers the
-// clock (1.8 to 2.1 GHz; with a cache of zeros, which costs less power, the same
-// cycles take 1.6 ms instead of 1.83). A chunk of 4096 tokens over 32768 keys, 32
-// heads of 128: 1.83 ms, 1.13 PF, 82% of what a product of 16384^3 reaches.
+// clock (1.8 to 2.1 GHz; with a cache of zeros, which costs less power, a version
+// of 1.92 ms took 1.63). A chunk of 4096 tokens over 32768 keys, 32 heads of 128:
+// 1.82 ms, 1.13 PF, 82% of what a library's product of 16384^3 reaches.
 //
 // What a wave loads lies in one page, so page entries and addresses are scalar.
 //
@@ -1012,7 +1016,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
 // ---------------------------------------------------------------------------
 // Joins the parts of a row: a workgroup per row; a thread takes four channels of
 // every SG-th part (four loads in flight), the SG sums meet in LDS in a fixed
-// order. A sum of -1 marks a part whose keys were seen but all scored -inf. Tokens
+// order: 4.5 us for 32 rows of 64 parts, launch and a chain of two loads. A sum of -1 marks a part whose keys were seen but all scored -inf. Tokens
 // of no sequence, or beyond its first max_new, have no parts and are left alone.
 // ---------------------------------------------------------------------------
 template <typename E, int D>

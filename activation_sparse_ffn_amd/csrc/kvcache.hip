@@ -16,6 +16,11 @@
 // eight channels: four tokens of a channel are one word of the values' order
 // ([D][P]), which they reach through LDS in whole words. Held entries are touched
 // only where the scale grew.
+//
+// One token in each of 32 sequences (8 heads of 128): 5.6 us, launch and chain. A
+// chunk of 4095 tokens (17 MB in, 8.4 MB out, a copy's 5 us): 12.3 us, one round of
+// 1040 workgroups that all wait for the same links of the chain; with the values'
+// bytes stored one at a time 16.7. Reading that chunk back: 7.5 us, 3.4 TB/s.
 #include "attn_common.hpp"
 #include "attn_launch.hpp"
 
