@@ -60,19 +60,27 @@ hipError_t launch_cache_append(const CacheArgs& c, const Heads& k, const Heads& 
 hipError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v, hipStream_t s);
 
 // ---- attention over the cache -----------------------------------------------------
-// How one call is cut up. Few rows (every sequence's fit a tile of 16): `blocks`
-// workgroups share the work evenly and a row has up to `splits` parts. Otherwise:
-// row tiles of `rows` (token, head) rows for each sequence and key head, and
-// `splits` ranges of `chunk` keys (the last one open). With more than one split
-// partial results go to the workspace and a second kernel joins them.
+// How one call is cut up: row tiles of `rows` (token, head) rows for each sequence
+// and key head (few: one tile of 16 holds every sequence's). Shared: `blocks`
+// workgroups take equal shares of all of them, and a row has up to `splits` parts.
+// Otherwise: a workgroup for each tile and each of `splits` ranges of `chunk` keys
+// (the last one open). With more than one split partial results go to the workspace
+// and a second kernel joins them. (Shared: chunk is the least share's keys.)
 struct AttnPlan {
-    bool few;
+    bool few, shared;
     int waves;                      // of the row-tile kernel's workgroups (32 rows each)
     int pieces;                     // bf16 pieces of the weights of a bf16 q there
     int rows, splits;
     int64_t row_tiles, chunk, blocks;
     size_t ws_bytes;                // 0 with one split
 };
+
+// Calls of up to so many rows are shared out evenly, whatever their lengths, and
+// joined (a join of 32768 rows takes 35 us); larger ones have row tiles to fill the
+// chip without.
+constexpr int64_t kSharedRows = 32768;
+// and their parts take up to so much workspace
+constexpr int64_t kPartBytes = (int64_t)256 << 20;
 
 inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
     AttnPlan p{};
@@ -88,12 +96,19 @@ inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
         const int64_t seen = (int64_t)window + p.rows / G + 1 + 63;
         if (seen < span) span = seen;
     }
-    const int64_t whole = (int64_t)c.B * c.Hkv * p.row_tiles;
-    if (p.few) {
-        // no share is less than 8 steps of 64 keys (see k_attend_few); the chip
-        // holds one workgroup a compute unit of the largest kinds, else two
-        const int64_t steps = (span + 63) / 64, held = c.D > 128 || c.dt == Dt::F32 ? 1 : 2;
+    const int64_t whole = (int64_t)c.B * c.Hkv * p.row_tiles, rows = c.T * Hq;
+    const int64_t steps = (span + 63) / 64, all_steps = ((int64_t)c.max_pages * c.P + c.max_new) / 64 + 16;
+    p.shared = p.few || (rows <= kSharedRows && whole <= ((int64_t)1 << 31) / all_steps);
+    if (p.shared) {
+        // no share is less than 8 steps of 64 keys (see share_work); the chip holds one
+        // workgroup a compute unit of the largest kinds, else two
+        const int64_t held = c.D > 128 || c.dt == Dt::F32 || (p.waves == 8 && !p.few) ? 1 : 2;
+        p.chunk = 8 * 64;
         p.splits = steps <= 8 ? 1 : (int)(steps / 8 + 2);
+        if (!p.few) {
+            const int64_t room = (int64_t)kPartBytes / (rows * (c.D + 2) * 4 + 1);
+            if (p.splits > room) p.splits = (int)room;
+        }
         const int64_t most_blocks = whole * ((steps + 7) / 8);
         p.blocks = (int64_t)compute_units() * held;
         if (most_blocks < p.blocks) p.blocks = most_blocks;

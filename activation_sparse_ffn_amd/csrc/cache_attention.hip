@@ -153,6 +153,163 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int tile_rows, Work
     return true;
 }
 
+// Sum (or largest, of values >= 0) of lanes 0 .. l, in lane l: within rows of 16
+// lanes, then across them.
+template <typename Op>
+__device__ __forceinline__ int wave_scan(int v, Op op) {
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));   // row_shr:1
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));   // row_shr:2
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));   // row_shr:4
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));   // row_shr:8
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));   // row_bcast:15
+    return op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));    // row_bcast:31
+}
+
+// The work of all sequences, row tiles and heads in a row, cut into equal shares of
+// the grid's workgroups (as many as the chip holds at once): lengths are known on the
+// device alone, and a grid for the longest would be nearly all empty for ragged
+// ones (32 sequences of 1 .. 32768 keys, one token each, took 86 us so, 55.6 in even
+// shares; finer ranges cost more in empty workgroups than they gave). In steps of 64
+// keys, a unit (row tile and head) costs as many as the sequence's longest tile, but
+// at least kLeast: what beginning and ending one takes. Units of at most kLeast
+// steps, or all where nothing joins parts, go whole to the workgroup in whose share
+// they begin. Where there are workgroups enough, every unit begins a share of its own
+// (cost rounded up to shares), so that no workgroup has the end of one and the
+// beginning of the next one after another. `work(w, parts)` is called for each piece
+// of the workgroup's; a row whose part 0 it is has `parts` parts in all.
+constexpr int kLeast = 8;
+
+template <typename F>
+__device__ __forceinline__ void share_work(const AttnArgs& a, int tile_rows, F work) {
+    const int lane = threadIdx.x & 63;
+    const int B = a.c.B, Hkv = a.c.Hkv;
+    // 64 sequences from b0 on, one a lane: where they are, their units, a unit's steps
+    // and the cost of them up to the lane's. (The host has seen to it that the cost of
+    // all fits 31 bits.)
+    struct Lane {
+        Sequence q;
+        int units, steps, cost;
+    };
+    int round_to = 0;           // 0: costs as they are, else rounded up to multiples of it
+    auto padded = [&](int steps) {
+        if (round_to > 0) return (steps + round_to - 1) / round_to * round_to;
+        return steps > kLeast ? steps : kLeast;
+    };
+    auto add = [](int p, int q) { return p + q; };
+    auto sum_costs = [&](Lane& y) { y.cost = wave_scan(padded(y.steps) * y.units, add); };
+    auto look = [&](int b0) {
+        Lane y;
+        y.units = 0;
+        y.steps = 1;
+        if (b0 + lane < B && find_sequence(a, b0 + lane, y.q)) {
+            const int rows = (int)y.q.rows, tiles = (rows + tile_rows - 1) / tile_rows;
+            int lo, hi;
+            keys_seen(a, y.q, tiles == 1 ? 0 : (tiles - 1) * tile_rows, rows, lo, hi);
+            if (tiles > 1 && a.window > 0) {
+                // any tile's: the window and the tile's tokens, from a multiple of 64 on
+                const int64_t most = (int64_t)a.window + tile_rows / a.G + 2 + kTile;
+                lo = 0;
+                if (hi > most) hi = (int)most;
+            }
+            y.steps = hi - lo > kTile ? (hi - lo + kTile - 1) / kTile : 1;
+            y.units = tiles * Hkv;
+        }
+        sum_costs(y);
+        return y;
+    };
+    auto longest_of = [&](const Lane& y) {
+        return lane_value(wave_scan(y.units > 0 ? y.steps : 0, [](int p, int q) { return p > q ? p : q; }), 63);
+    };
+    Lane x = look(0);
+    int total = lane_value(x.cost, 63), longest = longest_of(x);
+    for (int b0 = 64; b0 < B; b0 += 64) {
+        const Lane y = look(b0);
+        const int l = longest_of(y);
+        total += lane_value(y.cost, 63);
+        longest = l > longest ? l : longest;
+    }
+    int share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+    if (share < kLeast) share = kLeast;
+    // no more parts than the workspace has room for
+    if (a.splits > 1 && share < longest / (a.splits - 1) + 1) share = longest / (a.splits - 1) + 1;
+    if (B <= 64 && lane_value(wave_scan(x.units, add), 63) <= (int)gridDim.x && total < 1 << 29) {
+        round_to = share;
+        const int unrounded = x.cost;
+        sum_costs(x);
+        const int rounded = lane_value(x.cost, 63);
+        if (rounded / share > (int)gridDim.x) {
+            round_to = 0;
+            x.cost = unrounded;
+        } else {
+            total = rounded;
+        }
+    }
+    if ((int64_t)blockIdx.x * share >= total) return;
+    const int c0 = (int)blockIdx.x * share, c1 = total - c0 > share ? c0 + share : total;
+
+    // the sequence in whose cost c0 lies
+    int start = 0, b0 = 0;                  // start: cost before the 64, then before the unit
+    while (start + lane_value(x.cost, 63) <= c0) {
+        start += lane_value(x.cost, 63);
+        b0 += 64;
+        x = look(b0);
+    }
+    int at = __ffsll((unsigned long long)__ballot(start + x.cost > c0)) - 1;
+    int steps = lane_value(x.steps, at), units = lane_value(x.units, at);
+    start += lane_value(x.cost, at) - padded(steps) * units;
+    int unit = (c0 - start) / padded(steps);
+    start += unit * padded(steps);
+    while (start < c1) {
+        int from = 0, to = steps, part = 0, parts = 1;
+        if (a.splits == 1 || steps <= kLeast) {
+            if (start < c0) to = 0;         // another workgroup's
+        } else {
+            if (start < c0) {
+                from = c0 - start;
+                part = (c0 - start + share - 1) / share;
+                parts = part + 1;           // more than one: that is all the others have to know
+            }
+            if (c1 - start < steps) {
+                to = c1 - start;
+                parts = part + 2 + (steps - 1 - to) / share;
+            }
+        }
+        if (from < to) {
+            Work w;
+            Sequence q;
+            w.first = q.first = lane_value(x.q.first, at);
+            w.p0 = q.p0 = lane_value(x.q.p0, at);
+            w.rows = lane_value((int)x.q.rows, at);
+            q.rows = w.rows;
+            const int tile = unit / Hkv;
+            w.h = unit - tile * Hkv;
+            w.r0 = tile * tile_rows;
+            w.b = b0 + at;
+            w.part = part;
+            int lo, hi;
+            keys_seen(a, q, w.r0, w.rows - w.r0 < tile_rows ? w.rows : w.r0 + tile_rows, lo, hi);
+            // a tile of fewer steps than the longest has none in the first ones
+            const int none = steps - (hi - lo > kTile ? (hi - lo + kTile - 1) / kTile : 1);
+            w.k0 = lo + (from > none ? from - none : 0) * kTile;
+            w.k1 = to == steps ? hi : lo + (to > none ? to - none : 0) * kTile;
+            work(w, parts);
+        }
+        start += padded(steps);
+        if (++unit < units) continue;
+        unit = 0;
+        do {
+            if (b0 + ++at >= B) return;
+            if (at == 64) {
+                at = 0;
+                b0 += 64;
+                x = look(b0);
+            }
+            units = lane_value(x.units, at);
+        } while (units == 0);
+        steps = lane_value(x.steps, at);
+    }
+}
+
 // The table's entry for the page of position `pos` (the last one behind the
 // table's end). It is loaded a step before it is used and checked only then, so
 // that nothing waits for it: known_page says whether it names a page of the
@@ -473,146 +630,11 @@ __device__ __forceinline__ void attend_few(const AttnArgs& a, const Work& w, int
     if (a.splits > 1 && w.part == 0 && d0 == 0) a.parts[row] = parts;
 }
 
-// Sum (or largest, of values >= 0) of lanes 0 .. l, in lane l: within rows of 16
-// lanes, then across them.
-template <typename Op>
-__device__ __forceinline__ int wave_scan(int v, Op op) {
-    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));   // row_shr:1
-    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));   // row_shr:2
-    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));   // row_shr:4
-    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));   // row_shr:8
-    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));   // row_bcast:15
-    return op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));    // row_bcast:31
-}
-
-// The work of all sequences and heads in a row, cut into equal shares of the
-// grid's workgroups (as many as the chip holds at once): lengths are known on the
-// device alone, and a grid for the longest would be nearly all empty for ragged
-// ones (32 sequences of 1 .. 32768 keys took 86 us so, 55.6 in even shares; finer
-// ranges cost more in empty workgroups than they gave). In steps of 64 keys, a sequence and
-// head costs its steps, but at least kLeast: what beginning and ending one takes.
-// Those of at most kLeast steps, or all where nothing joins parts, go whole to the
-// workgroup in whose share they begin. Where there are workgroups enough, every
-// sequence and head begins a share of its own (cost rounded up to shares), so that
-// no workgroup has the end of one and the beginning of the next one after another.
-constexpr int kLeast = 8;
-
 template <typename E, int NP, int PP, int D>
 __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few(const AttnArgs a) {
     __shared__ float sm[4][16], sl[4][16];
     __shared__ __align__(16) float so[4][16][D + 4];
-    const int lane = threadIdx.x & 63;
-    const int B = a.c.B, Hkv = a.c.Hkv;
-    // 64 sequences from b0 on, one a lane: where they are, their steps (0: no rows)
-    // and the cost of them up to the lane's. (The host has seen to it that the cost
-    // of all fits 31 bits.)
-    struct Lane {
-        Sequence q;
-        int lo, hi, steps, cost;
-    };
-    int round_to = 0;           // 0: costs as they are, else rounded up to multiples of it
-    auto padded = [&](int steps) {
-        if (round_to > 0) return (steps + round_to - 1) / round_to * round_to;
-        return steps > kLeast ? steps : kLeast;
-    };
-    auto sum_costs = [&](Lane& y) {
-        y.cost = wave_scan(y.steps > 0 ? padded(y.steps) * Hkv : 0, [](int p, int q) { return p + q; });
-    };
-    auto look = [&](int b0) {
-        Lane y;
-        y.steps = 0;
-        y.lo = y.hi = 0;
-        if (b0 + lane < B && find_sequence(a, b0 + lane, y.q)) {
-            keys_seen(a, y.q, 0, (int)y.q.rows, y.lo, y.hi);
-            y.steps = y.hi - y.lo > kTile ? (y.hi - y.lo + kTile - 1) / kTile : 1;
-        }
-        sum_costs(y);
-        return y;
-    };
-    auto longest_of = [&](const Lane& y) {
-        return lane_value(wave_scan(y.steps, [](int p, int q) { return p > q ? p : q; }), 63);
-    };
-    Lane x = look(0);
-    int total = lane_value(x.cost, 63), longest = longest_of(x);
-    for (int b0 = 64; b0 < B; b0 += 64) {
-        const Lane y = look(b0);
-        const int l = longest_of(y);
-        total += lane_value(y.cost, 63);
-        longest = l > longest ? l : longest;
-    }
-    int share = (total + (int)gridDim.x - 1) / (int)gridDim.x;
-    if (share < kLeast) share = kLeast;
-    // no more parts than the workspace has room for
-    if (a.splits > 1 && share < longest / (a.splits - 1) + 1) share = longest / (a.splits - 1) + 1;
-    if (B <= 64 && B * Hkv <= (int)gridDim.x && total < 1 << 29) {
-        round_to = share;
-        const int unrounded = x.cost;
-        sum_costs(x);
-        const int rounded = lane_value(x.cost, 63);
-        if (rounded / share > (int)gridDim.x) {
-            round_to = 0;
-            x.cost = unrounded;
-        } else {
-            total = rounded;
-        }
-    }
-    if ((int64_t)blockIdx.x * share >= total) return;
-    const int c0 = (int)blockIdx.x * share, c1 = total - c0 > share ? c0 + share : total;
-
-    // the sequence in whose cost c0 lies
-    int start = 0, b0 = 0;                  // start: cost before the 64, then before sequence and head
-    while (start + lane_value(x.cost, 63) <= c0) {
-        start += lane_value(x.cost, 63);
-        b0 += 64;
-        x = look(b0);
-    }
-    int at = __ffsll((unsigned long long)__ballot(start + x.cost > c0)) - 1;
-    int steps = lane_value(x.steps, at);
-    start += lane_value(x.cost, at) - padded(steps) * Hkv;
-    int h = (c0 - start) / padded(steps);
-    start += h * padded(steps);
-    while (start < c1) {
-        int from = 0, to = steps, part = 0, parts = 1;
-        if (a.splits == 1 || steps <= kLeast) {
-            if (start < c0) to = 0;         // another workgroup's
-        } else {
-            if (start < c0) {
-                from = c0 - start;
-                part = (c0 - start + share - 1) / share;
-                parts = part + 1;           // more than one: that is all the others have to know
-            }
-            if (c1 - start < steps) {
-                to = c1 - start;
-                parts = part + 2 + (steps - 1 - to) / share;
-            }
-        }
-        if (from < to) {
-            const int lo = lane_value(x.lo, at);
-            Work w;
-            w.first = lane_value(x.q.first, at);
-            w.p0 = lane_value(x.q.p0, at);
-            w.rows = lane_value((int)x.q.rows, at);
-            w.r0 = 0;
-            w.k0 = lo + from * kTile;
-            w.k1 = to == steps ? lane_value(x.hi, at) : lo + to * kTile;
-            w.b = b0 + at;
-            w.h = h;
-            w.part = part;
-            attend_few<E, NP, PP, D>(a, w, parts, sm, sl, so);
-        }
-        start += padded(steps);
-        if (++h < Hkv) continue;
-        h = 0;
-        do {
-            if (b0 + ++at >= B) return;
-            if (at == 64) {
-                at = 0;
-                b0 += 64;
-                x = look(b0);
-            }
-            steps = lane_value(x.steps, at);
-        } while (steps == 0);
-    }
+    share_work(a, 16, [&](const Work& w, int parts) { attend_few<E, NP, PP, D>(a, w, parts, sm, sl, so); });
 }
 
 // ---------------------------------------------------------------------------
@@ -651,21 +673,12 @@ __global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few
 // 36 words apart), and every address of a step is one lane's base and a constant.
 // ---------------------------------------------------------------------------
 template <typename E, int NP, int PP, int D, int NW>
-__global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) void k_attend_rows(const AttnArgs a) {
+__device__ __forceinline__ void attend_rows(const AttnArgs& a, const Work& w, int parts, char* lds, float4 (*scales)[4]) {
     constexpr int NT = 64 * NW, KS = D / 16, DT = D / 32;
     constexpr int CH = (4 * D + NT - 1) / NT;           // 16-byte pieces a thread loads of keys, and of values
     constexpr int KP = 2 * D + 16, VP = 2 * kTile + 16; // row pitches in bytes
     constexpr int KB = kTile * KP, BUF = KB + D * VP;   // bytes of the keys, of one buffer
-    __shared__ __align__(16) char lds[2 * BUF];
-    // of each 16 keys: the key scale (with the softmax's), and of the value scale
-    // the logarithm (base 2) and the reciprocal of one factor, and the other factor.
-    // The first goes into the exponent, so it may not take weights that count to
-    // where fp32 ends: scales far from 1 are a mantissa and a power of two there,
-    // all others themselves and 1.
-    __shared__ float4 scales[2][4];
     const CacheArgs& c = a.c;
-    Work w;
-    if (!find_work(a, 32 * NW, w)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
     const int r = w.r0 + 32 * wave + col;
@@ -738,6 +751,11 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     auto stage_scales = [&](int buf) {
         if (scaler) {
             const float ks = known ? ks_in * a.scale2 : __builtin_nanf(""), vs = known ? vs_in : __builtin_nanf("");
+            // of each 16 keys: the key scale (with the softmax's), and of the value
+            // scale the logarithm (base 2) and the reciprocal of one factor, and the
+            // other factor. The first goes into the exponent, so it may not take
+            // weights that count to where fp32 ends: scales far from 1 are a mantissa
+            // and a power of two there, all others themselves and 1.
             float first = vs, rest = 1.f;
             if (vs < 0x1p-64f || vs > 0x1p100f) {
                 const bool finite = vs > 0.f && vs < __builtin_huge_valf();
@@ -992,7 +1010,7 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
     if (!valid) return;
     const int64_t row = (int64_t)(w.first + tok) * a.Hq + head;
     const bool seen = row_sees(pos, a.window, w.k0, w.k1);
-    const float inv = a.splits == 1 ? row_inverse(l, seen) : 1.f;
+    const float inv = parts == 1 ? row_inverse(l, seen) : 1.f;
     const int64_t part = row * a.splits + w.part;
     E* out = static_cast<E*>(a.out.p) + ((int64_t)(w.first + tok) * a.out.st + head * a.out.sh);
 #pragma unroll
@@ -1001,15 +1019,29 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
         for (int q = 0; q < 4; ++q) {
             const int d = 32 * i + 8 * q + 4 * half;
             const float v[4] = {o[i][4 * q] * inv, o[i][4 * q + 1] * inv, o[i][4 * q + 2] * inv, o[i][4 * q + 3] * inv};
-            if (a.splits == 1) store4(out + d, v);
+            if (parts == 1) store4(out + d, v);
             else store4(a.part_o + part * D + d, v);
         }
     if (half != 0) return;
-    if (a.splits > 1) {
-        a.part_ml[part] = make_float2(m, l == 0.f && seen ? -1.f : l);
-        if (w.part == 0) a.parts[row] = a.splits;
-    } else if (a.lse) {
-        a.lse[row] = row_lse(m, l, seen);
+    if (parts > 1) a.part_ml[part] = make_float2(m, l == 0.f && seen ? -1.f : l);
+    else if (a.lse) a.lse[row] = row_lse(m, l, seen);
+    if (a.splits > 1 && w.part == 0) a.parts[row] = parts;
+}
+
+// SHARED: in equal shares (share_work), else a workgroup for each row tile, head and
+// range of keys (find_work).
+template <typename E, int NP, int PP, int D, int NW, bool SHARED>
+__global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) void k_attend_rows(const AttnArgs a) {
+    __shared__ __align__(16) char lds[2 * (kTile * (2 * D + 16) + D * (2 * kTile + 16))];
+    __shared__ float4 scales[2][4];
+    if constexpr (SHARED) {
+        share_work(a, 32 * NW, [&](const Work& w, int parts) {
+            __syncthreads();        // the work before has been read from LDS
+            attend_rows<E, NP, PP, D, NW>(a, w, parts, lds, scales);
+        });
+    } else {
+        Work w;
+        if (find_work(a, 32 * NW, w)) attend_rows<E, NP, PP, D, NW>(a, w, a.splits, lds, scales);
     }
 }
 
@@ -1099,19 +1131,24 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a) {
     if (a.lse && threadIdx.x == 0) a.lse[row] = row_lse(M, sum, marks != 0.f);
 }
 
+template <typename E, int NP, int PP, int D, int NW>
+void launch_rows(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
+    const dim3 grid((unsigned)plan.blocks);
+    if (plan.shared) k_attend_rows<E, NP, PP, D, NW, true><<<grid, 64 * NW, 0, s>>>(a);
+    else k_attend_rows<E, NP, PP, D, NW, false><<<grid, 64 * NW, 0, s>>>(a);
+}
+
 template <typename E, int NP, int D>
 hipError_t launch(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
     const dim3 grid((unsigned)plan.blocks);
     if (plan.few) {
         k_attend_few<E, NP, NP == 1 ? 2 : 3, D><<<grid, 256, 0, s>>>(a);
+    } else if constexpr (NP == 3) {
+        launch_rows<E, 3, 3, D, 4>(a, plan, s);
+    } else if (plan.pieces == 2) {
+        launch_rows<E, 1, 2, D, 4>(a, plan, s);
     } else {
-        if constexpr (NP == 3) {
-            k_attend_rows<E, 3, 3, D, 4><<<grid, 256, 0, s>>>(a);
-        } else {
-            if (plan.pieces == 2) k_attend_rows<E, 1, 2, D, 4><<<grid, 256, 0, s>>>(a);
-            else if constexpr (D <= 128) k_attend_rows<E, 1, 1, D, 8><<<grid, 512, 0, s>>>(a);
-            else k_attend_rows<E, 1, 1, D, 4><<<grid, 256, 0, s>>>(a);
-        }
+        launch_rows<E, 1, 1, D, D <= 128 ? 8 : 4>(a, plan, s);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || plan.splits == 1) return e;
