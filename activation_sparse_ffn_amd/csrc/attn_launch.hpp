@@ -60,6 +60,9 @@ hipError_t launch_cache_append(const CacheArgs& c, const Heads& k, const Heads& 
 hipError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v, hipStream_t s);
 
 // ---- attention over the cache -----------------------------------------------------
+// Workgroups of k_attend_few that a compute unit holds.
+constexpr int few_held(int D, bool f32, int tiles) { return D > 128 || f32 || (tiles == 2 && D == 128) ? 1 : 2; }
+
 // How one call is cut up: row tiles of `rows` (token, head) rows for each sequence
 // and key head (few: one tile of 16 holds every sequence's). Shared: `blocks`
 // workgroups take equal shares of all of them, and a row has up to `splits` parts.
@@ -67,7 +70,8 @@ hipError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v,
 // (the last one open). With more than one split partial results go to the workspace
 // and a second kernel joins them. (Shared: chunk is the least share's keys.)
 struct AttnPlan {
-    bool few, shared;
+    bool few, pair;                 // every sequence's rows fit a tile of 16, two of them
+    bool shared;
     int waves;                      // of the row-tile kernel's workgroups (32 rows each)
     int pieces;                     // bf16 pieces of the weights of a bf16 q there
     int rows, splits;
@@ -86,9 +90,10 @@ inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
     AttnPlan p{};
     const int64_t G = Hq / c.Hkv, most = (int64_t)c.max_new * G;
     p.few = most <= 16;
+    p.pair = !p.few && most <= 32 && c.D <= 128;
     p.waves = c.D > 128 || c.dt == Dt::F32 || most <= 128 ? 4 : 8;
     p.pieces = most <= 128 ? 2 : 1;
-    p.rows = p.few ? 16 : 32 * p.waves;
+    p.rows = p.few ? 16 : p.pair ? 32 : 32 * p.waves;
     p.row_tiles = (most + p.rows - 1) / p.rows;
     // keys that one row tile sees: all, or the window of its tokens
     int64_t span = c.max_kv > 0 ? c.max_kv : 1;
@@ -98,14 +103,15 @@ inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
     }
     const int64_t whole = (int64_t)c.B * c.Hkv * p.row_tiles, rows = c.T * Hq;
     const int64_t steps = (span + 63) / 64, all_steps = ((int64_t)c.max_pages * c.P + c.max_new) / 64 + 16;
-    p.shared = p.few || (rows <= kSharedRows && whole <= ((int64_t)1 << 31) / all_steps);
+    p.shared = p.few || p.pair || (rows <= kSharedRows && whole <= ((int64_t)1 << 31) / all_steps);
     if (p.shared) {
         // no share is less than 8 steps of 64 keys (see share_work); the chip holds one
         // workgroup a compute unit of the largest kinds, else two
-        const int64_t held = c.D > 128 || c.dt == Dt::F32 || (p.waves == 8 && !p.few) ? 1 : 2;
+        const int64_t held = p.few || p.pair ? few_held(c.D, c.dt == Dt::F32, p.pair ? 2 : 1)
+                                             : c.D > 128 || c.dt == Dt::F32 || p.waves == 8 ? 1 : 2;
         p.chunk = 8 * 64;
         p.splits = steps <= 8 ? 1 : (int)(steps / 8 + 2);
-        if (!p.few) {
+        if (!p.few && !p.pair) {
             const int64_t room = (int64_t)kPartBytes / (rows * (c.D + 2) * 4 + 1);
             if (p.splits > room) p.splits = (int)room;
         }

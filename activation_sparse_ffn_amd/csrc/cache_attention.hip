@@ -452,17 +452,14 @@ __device__ __forceinline__ float row_lse(float M, float l, bool seen) {
 //   O^T: step u takes keys 16 g + 8 u .. + 7: the weights are in place, and a
 //     lane's 16-byte load of a value row [d][16 g ..] is two steps' operand.
 // ---------------------------------------------------------------------------
-template <typename E, int NP, int PP, int D>
-__device__ __forceinline__ void attend_few(const AttnArgs& a, const Work& w, int parts, float (*sm)[16],
-                                           float (*sl)[16], float (*so)[16][D + 4]) {
+template <typename E, int NP, int PP, int D, int RT>
+__device__ __forceinline__ void attend_few(const AttnArgs& a, const Work& w, int parts, float (*sm)[16 * RT],
+                                           float (*sl)[16 * RT], float (*so)[16 * RT][D + 4]) {
     constexpr int KC = D / 64, DT = D / 16;
     const CacheArgs& c = a.c;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int g = lane >> 4, n = lane & 15, gk = n >> 2;
-    const bool valid = w.r0 + n < w.rows;
-    const int tok = valid ? (w.r0 + n) / a.G : 0;
-    const int head = w.h * a.G + (valid ? w.r0 + n - tok * a.G : 0);
-    const int pos = w.p0 + tok;
+    int pos[RT];            // of the lane's row in each tile of 16
 
     const uint32_t head_bytes = (uint32_t)c.P * D;      // of one page
     const uint32_t page_bytes = c.Hkv * head_bytes;
@@ -483,20 +480,28 @@ __device__ __forceinline__ void attend_few(const AttnArgs& a, const Work& w, int
     uint32_t entry_k = page_entry(c, table, t0 + 16 * gk), entry_v = page_entry(c, table, t0 + 16 * g);
     if (t0 < w.k1) load_keys(entry_k, t0);
 
-    bf16x8 qf[KC][2][NP];
-    {
+    bf16x8 qf[RT][KC][2][NP];
+    f32x4 o[RT][DT];
+    float m[RT], l[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const int row = w.r0 + 16 * r + n;
+        const bool valid = row < w.rows;
+        const int tok = valid ? row / a.G : 0;
+        const int head = w.h * a.G + (valid ? row - tok * a.G : 0);
         const E* q = static_cast<const E*>(a.q.p) + ((int64_t)(w.first + tok) * a.q.st + head * a.q.sh);
 #pragma unroll
         for (int cc = 0; cc < KC; ++cc)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) load_q<E, NP>(q + 64 * cc + 16 * g + 8 * u, valid, a.negate, qf[cc][u]);
-    }
-    f32x4 o[DT];
+            for (int u = 0; u < 2; ++u) load_q<E, NP>(q + 64 * cc + 16 * g + 8 * u, valid, a.negate, qf[r][cc][u]);
 #pragma unroll
-    for (int i = 0; i < DT; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float m = neg_inf(), l = 0.f;
+        for (int i = 0; i < DT; ++i) o[r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        pos[r] = w.p0 + tok;
+        m[r] = neg_inf();
+        l[r] = 0.f;
+    }
     const int p_first = w.p0 + w.r0 / a.G;
-    const int p_last = w.p0 + ((w.rows - w.r0 < 16 ? w.rows : w.r0 + 16) - 1) / a.G;
+    const int p_last = w.p0 + ((w.rows - w.r0 < 16 * RT ? w.rows : w.r0 + 16 * RT) - 1) / a.G;
 
     for (; t0 < w.k1; t0 += 4 * kTile) {
         // values and scales of this step, page ids of the next
@@ -511,62 +516,68 @@ __device__ __forceinline__ void attend_few(const AttnArgs& a, const Work& w, int
         entry_k = page_entry(c, table, tn + 16 * gk);
         entry_v = page_entry(c, table, tn + 16 * g);
 
-        f32x4 s[4];
+        f32x4 s[RT][4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int r = 0; r < RT; ++r) s[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int cc = 0; cc < KC; ++cc)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const bf16x8 kf = u ? widen(kr[t][cc].z, kr[t][cc].w) : widen(kr[t][cc].x, kr[t][cc].y);
 #pragma unroll
-                    for (int p = 0; p < NP; ++p)
-                        s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[cc][u][p], s[t], 0, 0, 0);
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int p = 0; p < NP; ++p)
+                            s[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[r][cc][u][p], s[r][t], 0, 0, 0);
                 }
         }
         if (tn < w.k1) load_keys(entry_k, tn);
 
         ks = known ? ks * a.scale2 : __builtin_nanf("");
         vs = known ? vs : __builtin_nanf("");
-        float x[16];
+        bf16x8 pf[RT][2][PP];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = s[e >> 2][e & 3] * ks;
-        // a key beyond the row's position or before its window has no weight,
-        // whatever is stored there: a select, and a scale of 0 where the row
-        // sees none of the lane's sixteen (they share a page)
-        if (t0 + kTile - 1 > p_first || t0 + kTile > w.k1 || (a.window > 0 && t0 <= p_last - a.window)) {
-            const int up = last_seen(pos, t0, w.k1) - 16 * g, dn = before_seen(pos, t0, a.window) - 16 * g;
+        for (int r = 0; r < RT; ++r) {
+            float x[16], pvs = vs;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (e > up || e <= dn) x[e] = neg_inf();
-            if (up < 0 || dn >= 15) vs = 0.f;
-        }
-        float top = x[0];
+            for (int e = 0; e < 16; ++e) x[e] = s[r][e >> 2][e & 3] * ks;
+            // a key beyond the row's position or before its window has no weight,
+            // whatever is stored there: a select, and a scale of 0 where the row
+            // sees none of the lane's sixteen (they share a page)
+            if (t0 + kTile - 1 > p_first || t0 + kTile > w.k1 || (a.window > 0 && t0 <= p_last - a.window)) {
+                const int up = last_seen(pos[r], t0, w.k1) - 16 * g, dn = before_seen(pos[r], t0, a.window) - 16 * g;
 #pragma unroll
-        for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = max_halves(top);
-        if (__any(top > m + kSlack)) {
-            const float to = fmaxf(m, top);
-            const float alpha = __builtin_amdgcn_exp2f(m - (to == neg_inf() ? 0.f : to));
-            m = to;
-            l *= alpha;
-#pragma unroll
-            for (int i = 0; i < DT; ++i) o[i] *= alpha;
-        }
-        const float ref = m == neg_inf() ? 0.f : m;
-        bf16x8 pf[2][PP];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            float pv[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float p = __builtin_amdgcn_exp2f(x[8 * u + e] - ref);
-                l += p;
-                pv[e] = p * vs;
+                for (int e = 0; e < 16; ++e)
+                    if (e > up || e <= dn) x[e] = neg_inf();
+                if (up < 0 || dn >= 15) pvs = 0.f;
             }
-            pieces<PP>(pv, pf[u]);
+            float top = x[0];
+#pragma unroll
+            for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
+            top = fmaxf(top, __shfl_xor(top, 16, 64));
+            top = max_halves(top);
+            if (__any(top > m[r] + kSlack)) {
+                const float to = fmaxf(m[r], top);
+                const float alpha = __builtin_amdgcn_exp2f(m[r] - (to == neg_inf() ? 0.f : to));
+                m[r] = to;
+                l[r] *= alpha;
+#pragma unroll
+                for (int i = 0; i < DT; ++i) o[r][i] *= alpha;
+            }
+            const float ref = m[r] == neg_inf() ? 0.f : m[r];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float pv[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float p = __builtin_amdgcn_exp2f(x[8 * u + e] - ref);
+                    l[r] += p;
+                    pv[e] = p * pvs;
+                }
+                pieces<PP>(pv, pf[r][u]);
+            }
         }
 #pragma unroll
         for (int i = 0; i < DT; ++i)
@@ -574,67 +585,75 @@ __device__ __forceinline__ void attend_few(const AttnArgs& a, const Work& w, int
             for (int u = 0; u < 2; ++u) {
                 const bf16x8 vf = u ? widen(vr[i].z, vr[i].w) : widen(vr[i].x, vr[i].y);
 #pragma unroll
-                for (int p = 0; p < PP; ++p)
-                    o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[u][p], o[i], 0, 0, 0);
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int p = 0; p < PP; ++p)
+                        o[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf[r][u][p], o[r][i], 0, 0, 0);
             }
     }
 
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
     __syncthreads();        // the work before has been read from LDS
-    if (g == 0) {
-        sm[wave][n] = m;
-        sl[wave][n] = l;
-    }
 #pragma unroll
-    for (int i = 0; i < DT; ++i) *reinterpret_cast<f32x4*>(&so[wave][n][16 * i + 4 * g]) = o[i];
+    for (int r = 0; r < RT; ++r) {
+        l[r] += __shfl_xor(l[r], 16, 64);
+        l[r] += __shfl_xor(l[r], 32, 64);
+        if (g == 0) {
+            sm[wave][16 * r + n] = m[r];
+            sl[wave][16 * r + n] = l[r];
+        }
+#pragma unroll
+        for (int i = 0; i < DT; ++i) *reinterpret_cast<f32x4*>(&so[wave][16 * r + n][16 * i + 4 * g]) = o[r][i];
+    }
     __syncthreads();
 
-    // thread: row n2, D / 16 consecutive channels
-    const int n2 = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * (D / 16);
-    const int r2 = w.r0 + n2;
-    if (r2 >= w.rows) return;
-    float M = neg_inf(), sum = 0.f, f[4];
+    // thread: row n2 of each tile of 16, D / 16 consecutive channels
+    const int d0 = (threadIdx.x & 15) * (D / 16);
+#pragma unroll 1
+    for (int n2 = threadIdx.x >> 4; n2 < 16 * RT; n2 += 16) {
+        const int r2 = w.r0 + n2;
+        if (r2 >= w.rows) return;
+        float M = neg_inf(), sum = 0.f, f[4];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) M = fmaxf(M, sm[v][n2]);
+        for (int v = 0; v < 4; ++v) M = fmaxf(M, sm[v][n2]);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-        f[v] = part_factor(sm[v][n2], sl[v][n2], M);
-        sum += f[v] * sl[v][n2];
+        for (int v = 0; v < 4; ++v) {
+            f[v] = part_factor(sm[v][n2], sl[v][n2], M);
+            sum += f[v] * sl[v][n2];
+        }
+        float acc[D / 16];
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) acc[d] = 0.f;
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            if (f[v] != 0.f)
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) acc[d] += f[v] * so[v][n2][d0 + d];
+        const int tok2 = r2 / a.G, head2 = w.h * a.G + r2 - tok2 * a.G;
+        const int64_t row = (int64_t)(w.first + tok2) * a.Hq + head2;
+        const bool seen = row_sees(w.p0 + tok2, a.window, w.k0, w.k1);
+        if (parts == 1) {
+            const float inv = row_inverse(sum, seen);
+            E* out = static_cast<E*>(a.out.p) + ((int64_t)(w.first + tok2) * a.out.st + head2 * a.out.sh) + d0;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) acc[d] *= inv;
+#pragma unroll
+            for (int d = 0; d < D / 16; d += 4) store4(out + d, acc + d);
+            if (a.lse && d0 == 0) a.lse[row] = row_lse(M, sum, seen);
+        } else {
+            const int64_t part = row * a.splits + w.part;
+#pragma unroll
+            for (int d = 0; d < D / 16; d += 4) store4(a.part_o + part * D + d0 + d, acc + d);
+            if (d0 == 0) a.part_ml[part] = make_float2(M, sum == 0.f && seen ? -1.f : sum);
+        }
+        if (a.splits > 1 && w.part == 0 && d0 == 0) a.parts[row] = parts;
     }
-    float acc[D / 16];
-#pragma unroll
-    for (int d = 0; d < D / 16; ++d) acc[d] = 0.f;
-#pragma unroll
-    for (int v = 0; v < 4; ++v)
-        if (f[v] != 0.f)
-#pragma unroll
-            for (int d = 0; d < D / 16; ++d) acc[d] += f[v] * so[v][n2][d0 + d];
-    const int tok2 = r2 / a.G, head2 = w.h * a.G + r2 - tok2 * a.G;
-    const int64_t row = (int64_t)(w.first + tok2) * a.Hq + head2;
-    const bool seen = row_sees(w.p0 + tok2, a.window, w.k0, w.k1);
-    if (parts == 1) {
-        const float inv = row_inverse(sum, seen);
-        E* out = static_cast<E*>(a.out.p) + ((int64_t)(w.first + tok2) * a.out.st + head2 * a.out.sh) + d0;
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d) acc[d] *= inv;
-#pragma unroll
-        for (int d = 0; d < D / 16; d += 4) store4(out + d, acc + d);
-        if (a.lse && d0 == 0) a.lse[row] = row_lse(M, sum, seen);
-    } else {
-        const int64_t part = row * a.splits + w.part;
-#pragma unroll
-        for (int d = 0; d < D / 16; d += 4) store4(a.part_o + part * D + d0 + d, acc + d);
-        if (d0 == 0) a.part_ml[part] = make_float2(M, sum == 0.f && seen ? -1.f : sum);
-    }
-    if (a.splits > 1 && w.part == 0 && d0 == 0) a.parts[row] = parts;
 }
 
-template <typename E, int NP, int PP, int D>
-__global__ __launch_bounds__(256, D == 256 || NP == 3 ? 1 : 2) void k_attend_few(const AttnArgs a) {
-    __shared__ float sm[4][16], sl[4][16];
-    __shared__ __align__(16) float so[4][16][D + 4];
-    share_work(a, 16, [&](const Work& w, int parts) { attend_few<E, NP, PP, D>(a, w, parts, sm, sl, so); });
+template <typename E, int NP, int PP, int D, int RT>
+__global__ __launch_bounds__(256, few_held(D, NP == 3, RT)) void k_attend_few(const AttnArgs a) {
+    __shared__ float sm[4][16 * RT], sl[4][16 * RT];
+    __shared__ __align__(16) float so[4][16 * RT][D + 4];
+    share_work(a, 16 * RT, [&](const Work& w, int parts) { attend_few<E, NP, PP, D, RT>(a, w, parts, sm, sl, so); });
 }
 
 // ---------------------------------------------------------------------------
@@ -1142,7 +1161,9 @@ template <typename E, int NP, int D>
 hipError_t launch(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
     const dim3 grid((unsigned)plan.blocks);
     if (plan.few) {
-        k_attend_few<E, NP, NP == 1 ? 2 : 3, D><<<grid, 256, 0, s>>>(a);
+        k_attend_few<E, NP, NP == 1 ? 2 : 3, D, 1><<<grid, 256, 0, s>>>(a);
+    } else if (plan.pair) {
+        if constexpr (D <= 128) k_attend_few<E, NP, NP == 1 ? 2 : 3, D, 2><<<grid, 256, 0, s>>>(a);
     } else if constexpr (NP == 3) {
         launch_rows<E, 3, 3, D, 4>(a, plan, s);
     } else if (plan.pieces == 2) {
