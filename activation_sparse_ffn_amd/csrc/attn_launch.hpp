@@ -60,8 +60,10 @@ hipError_t launch_cache_append(const CacheArgs& c, const Heads& k, const Heads& 
 hipError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v, hipStream_t s);
 
 // ---- attention over the cache -----------------------------------------------------
-// Workgroups of k_attend_few that a compute unit holds.
-constexpr int few_held(int D, bool f32, int tiles) { return D > 128 || f32 || (tiles == 2 && D == 128) ? 1 : 2; }
+// Workgroups of k_attend_few that a compute unit holds. (Two tiles of rows of heads
+// of 128 spill 32 bytes a lane so; 32 ragged sequences of 6 tokens of 4 heads take
+// 74 us, at one workgroup without spills 112: loads in flight are what counts.)
+constexpr int few_held(int D, bool f32, int tiles) { return D > 128 || f32 ? 1 : 2; }
 
 // How one call is cut up: row tiles of `rows` (token, head) rows for each sequence
 // and key head (few: one tile of 16 holds every sequence's). Shared: `blocks`
@@ -81,7 +83,9 @@ struct AttnPlan {
 
 // Calls of up to so many rows are shared out evenly, whatever their lengths, and
 // joined (a join of 32768 rows takes 35 us); larger ones have row tiles to fill the
-// chip without.
+// chip without. (32 sequences of 1 .. 32768 keys, one token of 32 heads to one of
+// keys: 61 us shared, 240 as a workgroup for each range of keys; 32 tokens of one
+// sequence, where every length is the same, 39 against 36.)
 constexpr int64_t kSharedRows = 32768;
 // and their parts take up to so much workspace
 constexpr int64_t kPartBytes = (int64_t)256 << 20;
@@ -90,6 +94,8 @@ inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
     AttnPlan p{};
     const int64_t G = Hq / c.Hkv, most = (int64_t)c.max_new * G;
     p.few = most <= 16;
+    // two tiles of 16 rows: 5 tokens of 4 heads over 32768 keys 24.6 us, by a row tile
+    // of 128 33 (heads of 256 have no registers for it)
     p.pair = !p.few && most <= 32 && c.D <= 128;
     p.waves = c.D > 128 || c.dt == Dt::F32 || most <= 128 ? 4 : 8;
     p.pieces = most <= 128 ? 2 : 1;

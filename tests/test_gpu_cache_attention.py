@@ -155,6 +155,36 @@ def test_long_context_split_over_workgroups(dtype):
     check([5003], [9], 4, 4, 128, 32, dtype, window=1500, seed=4)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 150])
+def test_ragged_work_in_shares(window, D, dtype):
+    """Drafts and chunks beside single tokens, cut across sequences, row tiles and
+    heads: one tile of 16, two, one of 128, several."""
+    check([2100, 33, 700], [5, 8, 3], 8, 2, D, 64, dtype, window=window, seed=1)
+    check([1900, 40, 900], [20, 1, 3], 8, 2, D, 16, dtype, window=window, seed=2)
+    check([1500, 40, 1200, 700], [300, 1, 64, 5], 6, 2, D, 32, dtype, window=window, seed=3)
+
+
+@pytest.mark.parametrize("max_kv", [1, 300, 1500, 50000])
+def test_shares_of_any_max_kv(max_kv):
+    check([1500, 40, 1200, 700], [100, 1, 64, 5], 8, 2, 64, 32, BF, max_kv=max_kv, seed=4)
+    check([1500] + [7 + i for i in range(70)], [6] + [3] * 70, 4, 1, 64, 16, BF, max_kv=max_kv, seed=5)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,window", [(64, 0), (128, 0), (64, 100), (256, 0)])
+def test_more_rows_than_are_shared(D, window, dtype):
+    """Above 32768 rows: a workgroup for each tile and range of keys."""
+    check([1100, 90], [490, 30], 64, 2, D, 64, dtype, window=window, seed=6)
+
+
+def test_many_short_sequences():
+    """Above 32768 rows, tiles of one sequence's few tokens, more than 64 sequences."""
+    rng = np.random.default_rng(7)
+    check(rng.integers(2, 90, 270).tolist(), [2] * 270, 64, 2, 64, 16, BF, seed=7)
+
+
 @pytest.mark.parametrize("max_kv", [1, 64, 500, 100000])
 def test_max_kv_never_changes_what_is_computed(max_kv):
     check([3000, 100], None, 4, 2, 64, 16, BF, seed=1, max_kv=max_kv)
