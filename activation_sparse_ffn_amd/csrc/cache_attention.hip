@@ -1066,17 +1066,23 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
 }
 
 // ---------------------------------------------------------------------------
-// Joins the parts of a row: a workgroup per row; a thread takes four channels of
-// every SG-th part (four loads in flight), the SG sums meet in LDS in a fixed
-// order: 4.5 us for 32 rows of 64 parts, launch and a chain of two loads. A sum of -1 marks a part whose keys were seen but all scored -inf. Tokens
-// of no sequence, or beyond its first max_new, have no parts and are left alone.
+// Joins the parts of a row: NT threads, each with four channels of every SG-th part
+// (four loads in flight); the SG sums meet in LDS or by lane exchanges, in a fixed
+// order. A workgroup takes one row: 4.5 us for 32 rows of 64 parts, launch and a chain
+// of two loads. From kWaveRows rows on, which have few parts each, a wave does: 32768
+// rows 15 us (as workgroups 45), 8192 9.4 (14.2); 1024 rows of up to 66 parts would
+// take 11.1 (8.7). A sum of -1 marks a part whose keys were seen but all scored -inf.
+// Tokens of no sequence, or beyond its first max_new, have no parts and are left
+// alone.
 // ---------------------------------------------------------------------------
-template <typename E, int D>
+constexpr int64_t kWaveRows = 4096;
+template <typename E, int D, int NT>
 __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a) {
-    constexpr int CG = D / 4, SG = 256 / CG, IN = 4;
-    __shared__ float4 so[SG][CG];
-    const int lane = threadIdx.x & 63;
-    const int row = blockIdx.x, t = row / a.Hq;
+    constexpr int CG = D / 4, SG = NT / CG, IN = 4;
+    const int lane = threadIdx.x & 63, tid = threadIdx.x % NT;
+    const int64_t row64 = (int64_t)blockIdx.x * (256 / NT) + threadIdx.x / NT;
+    if (row64 >= a.c.T * a.Hq) return;
+    const int row = (int)row64, t = row / a.Hq;
     // loaded before it is known whether the row has parts
     const float2* ml = a.part_ml + (int64_t)row * a.splits;
     const int parts = a.parts[row];
@@ -1092,7 +1098,7 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a) {
         if (first < 0 || last > a.c.T || t < first || t >= last || t - first >= a.c.max_new) return;
     }
     if (parts == 1) return;     // written at once
-    const int cg = threadIdx.x % CG, sg = threadIdx.x / CG;
+    const int cg = tid % CG, sg = tid / CG;
     const float4* o = reinterpret_cast<const float4*>(a.part_o + (int64_t)row * a.splits * D) + cg;
     float4 v[IN];
     auto load = [&](int s) {
@@ -1130,25 +1136,35 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a) {
             acc.w += f * v[i].w;
         }
     }
-    so[sg][cg] = acc;
-    __syncthreads();
+    float r[4] = {acc.x, acc.y, acc.z, acc.w};
+    if constexpr (NT == 64) {
+#pragma unroll
+        for (int w = 32; w >= CG; w >>= 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] += __shfl_xor(r[i], w, 64);
+    } else {
+        __shared__ float4 so[SG][CG];
+        so[sg][cg] = acc;
+        __syncthreads();
+        r[0] = r[1] = r[2] = r[3] = 0.f;
+        if (sg == 0)
+#pragma unroll
+            for (int i = 0; i < SG; ++i) {
+                const float4 p = so[i][cg];
+                r[0] += p.x;
+                r[1] += p.y;
+                r[2] += p.z;
+                r[3] += p.w;
+            }
+    }
     const int h = row - t * a.Hq;
     const float inv = row_inverse(sum, marks != 0.f);
-    if (threadIdx.x < CG) {
-        float r[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < SG; ++i) {
-            const float4 p = so[i][threadIdx.x];
-            r[0] += p.x;
-            r[1] += p.y;
-            r[2] += p.z;
-            r[3] += p.w;
-        }
+    if (sg == 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) r[i] *= inv;
-        store4(static_cast<E*>(a.out.p) + ((int64_t)t * a.out.st + h * a.out.sh) + 4 * threadIdx.x, r);
+        store4(static_cast<E*>(a.out.p) + ((int64_t)t * a.out.st + h * a.out.sh) + 4 * cg, r);
     }
-    if (a.lse && threadIdx.x == 0) a.lse[row] = row_lse(M, sum, marks != 0.f);
+    if (a.lse && tid == 0) a.lse[row] = row_lse(M, sum, marks != 0.f);
 }
 
 template <typename E, int NP, int PP, int D, int NW>
@@ -1174,7 +1190,9 @@ hipError_t launch(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || plan.splits == 1) return e;
-    k_attend_join<E, D><<<dim3((unsigned)(a.c.T * a.Hq)), 256, 0, s>>>(a);
+    const int64_t rows = a.c.T * a.Hq;
+    if (rows < kWaveRows) k_attend_join<E, D, 256><<<dim3((unsigned)rows), 256, 0, s>>>(a);
+    else k_attend_join<E, D, 64><<<dim3((unsigned)((rows + 3) / 4)), 256, 0, s>>>(a);
     return hipGetLastError();
 }
 
