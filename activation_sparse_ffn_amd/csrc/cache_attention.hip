@@ -693,7 +693,8 @@ __global__ __launch_bounds__(256, few_held(D, NP == 3, RT)) void k_attend_few(co
 // 36 words apart), and every address of a step is one lane's base and a constant.
 // ---------------------------------------------------------------------------
 template <typename E, int NP, int PP, int D, int NW>
-__device__ __forceinline__ void attend_rows(const AttnArgs& a, const Work& w, int parts, char* lds, float4 (*scales)[4]) {
+__device__ __forceinline__ void attend_rows(const AttnArgs& a, const Work& w, int parts, char* lds,
+                                            float4 (*scales)[4]) {
     constexpr int NT = 64 * NW, KS = D / 16, DT = D / 32;
     constexpr int CH = (4 * D + NT - 1) / NT;           // 16-byte pieces a thread loads of keys, and of values
     constexpr int KP = 2 * D + 16, VP = 2 * kTile + 16; // row pitches in bytes
