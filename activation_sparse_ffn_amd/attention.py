@@ -395,7 +395,9 @@ def cache_attention(cache: KVCache, batch: CacheBatch, q: torch.Tensor, scale: O
     keys, its own among them. scale: head_dim^-0.5 by default. heads is a
     multiple of the cache's kv_heads. Returns out [T, heads, head_dim], with
     return_lse also the log of each row's sum, fp32 [T, heads]. A row that sees
-    no key gives zeros and -inf."""
+    no key gives zeros and -inf. The softmax weights of a bf16 q are kept to 16
+    bits, or to 8 in a sequence whose new tokens times heads / kv_heads are more
+    than 128; those of an fp32 q to fp32."""
     lib = load_library()
     _same_device(cache, batch)
     dev = cache.device

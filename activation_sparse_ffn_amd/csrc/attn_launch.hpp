@@ -75,11 +75,15 @@ struct AttnPlan {
     bool few, pair;                 // every sequence's rows fit a tile of 16, two of them
     bool shared;
     int waves;                      // of the row-tile kernel's workgroups (32 rows each)
-    int pieces;                     // bf16 pieces of the weights of a bf16 q there
+    int pieces;                     // bf16 pieces of the weights of a bf16 q there, at least
     int rows, splits;
     int64_t row_tiles, chunk, blocks;
     size_t ws_bytes;                // 0 with one split
 };
+
+// Sequences of up to so many rows a key head keep the weights of a bf16 q to 16 bits,
+// in every kernel.
+constexpr int kPreciseRows = 128;
 
 // Calls of up to so many rows are shared out evenly, whatever their lengths, and
 // joined (a join of 32768 rows takes 15 us); larger ones have row tiles to fill the
@@ -98,7 +102,7 @@ inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
     // of 128 33 (heads of 256 have no registers for it)
     p.pair = !p.few && most <= 32 && c.D <= 128;
     p.waves = c.D > 128 || c.dt == Dt::F32 || most <= 128 ? 4 : 8;
-    p.pieces = most <= 128 ? 2 : 1;
+    p.pieces = most <= kPreciseRows ? 2 : 1;
     p.rows = p.few ? 16 : p.pair ? 32 : 32 * p.waves;
     p.row_tiles = (most + p.rows - 1) / p.rows;
     // keys that one row tile sees: all, or the window of its tokens

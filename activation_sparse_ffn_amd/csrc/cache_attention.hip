@@ -8,9 +8,12 @@
 // fp32 score, and the value's scale the weight p before it is rounded to bf16
 // (p sv, so that a page of small values keeps its relative precision). An fp32
 // q is taken as three bf16 pieces (24 bits), and so are the weights. For a bf16 q
-// the weights are two pieces where few rows leave the matrix cores idle, and one
-// (2^-9 of each weight, as much as the result's own rounding) for long chunks,
-// where a second would cost a third more of the time's main part.
+// the weights are two pieces (16 bits) where a sequence has up to kPreciseRows rows
+// a key head, and one (up to 2^-8 of each weight, as much as the result's own rounding)
+// above, where the second costs a third: 4096 tokens over 32768 keys 1.81 ms, with
+// two pieces 2.39; heads of 64 1.25 and 1.62; heads of 256 over 8192 keys 0.91 and
+// 1.18. A sequence's own tokens decide it, not the call's: what else is in the batch
+// does not change how exact a row is.
 //
 // Both kernels compute S^T = K Q^T and O^T = V^T P^T, which keeps a query row
 // in one matrix column: the lane that holds scores of a row holds that row's
@@ -1055,14 +1058,21 @@ template <typename E, int NP, int PP, int D, int NW, bool SHARED>
 __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) void k_attend_rows(const AttnArgs a) {
     __shared__ __align__(16) char lds[2 * (kTile * (2 * D + 16) + D * (2 * kTile + 16))];
     __shared__ float4 scales[2][4];
+    // PP 1: sequences of few rows beside ones of many keep their weights to two pieces
+    // (2048 tokens over 32768 keys beside 31 single tokens: 1.86 ms, with one 1.68)
+    auto attend = [&](const Work& w, int parts) {
+        if constexpr (PP == 1)
+            if (w.rows <= kPreciseRows) return attend_rows<E, NP, 2, D, NW>(a, w, parts, lds, scales);
+        attend_rows<E, NP, PP, D, NW>(a, w, parts, lds, scales);
+    };
     if constexpr (SHARED) {
         share_work(a, 32 * NW, [&](const Work& w, int parts) {
             __syncthreads();        // the work before has been read from LDS
-            attend_rows<E, NP, PP, D, NW>(a, w, parts, lds, scales);
+            attend(w, parts);
         });
     } else {
         Work w;
-        if (find_work(a, 32 * NW, w)) attend_rows<E, NP, PP, D, NW>(a, w, a.splits, lds, scales);
+        if (find_work(a, 32 * NW, w)) attend(w, a.splits);
     }
 }
 

@@ -155,8 +155,9 @@ size_t cache_attention_workspace_size(const sffn_kv_cache_t* cache, const sffn_k
  * values of head a / (n_q_heads / kv_heads):
  *   s_j = scale q . k_j,  out = sum_j softmax(s)_j v_j,  lse = log sum_j exp s_j
  * Scores, statistics and sums are fp32; the weights of the values are kept to
- * fp32 for an fp32 q and to 16 bits for a bf16 q, or 8 (bf16) where a sequence
- * and key head has more than 128 rows. A row that sees no key
+ * fp32 for an fp32 q. For a bf16 q they are kept to 16 bits in a sequence of up
+ * to 128 rows (new tokens times n_q_heads / kv_heads) and to 8 (bf16) in one of
+ * more, whatever the call's other sequences and max_new. A row that sees no key
  * gives zeros and lse -inf.
  *   q, out [T, n_q_heads, head_dim] views (dtype, 16-byte aligned rows); rows
  *          of tokens outside every sequence are left as they are
