@@ -91,7 +91,9 @@ constexpr int kPreciseRows = 128;
 // keys: 61 us shared, 240 as a workgroup for each range of keys; 32 tokens of one
 // sequence, where every length is the same, 39 against 36.)
 constexpr int64_t kSharedRows = 32768;
-// and their parts take up to so much workspace
+// The parts of rows take up to so much workspace in any call. Few sequences stay far
+// below it (32 of 32768 keys, 32 heads of 128: 34 MiB); many need few parts each,
+// since the shares are then longer than a sequence.
 constexpr int64_t kPartBytes = (int64_t)256 << 20;
 
 inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
@@ -112,6 +114,8 @@ inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
         if (seen < span) span = seen;
     }
     const int64_t whole = (int64_t)c.B * c.Hkv * p.row_tiles, rows = c.T * Hq;
+    // parts of every row that kPartBytes hold
+    const int64_t room = (kPartBytes / 4 / rows - 1) / (c.D + 2);
     const int64_t steps = (span + 63) / 64, all_steps = ((int64_t)c.max_pages * c.P + c.max_new) / 64 + 16;
     p.shared = p.few || p.pair || (rows <= kSharedRows && whole <= ((int64_t)1 << 31) / all_steps);
     if (p.shared) {
@@ -121,10 +125,7 @@ inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
                                              : c.D > 128 || c.dt == Dt::F32 || p.waves == 8 ? 1 : 2;
         p.chunk = 8 * 64;
         p.splits = steps <= 8 ? 1 : (int)(steps / 8 + 2);
-        if (!p.few && !p.pair) {
-            const int64_t room = (int64_t)kPartBytes / (rows * (c.D + 2) * 4 + 1);
-            if (p.splits > room) p.splits = (int)room;
-        }
+        if (p.splits > room) p.splits = room < 2 ? 1 : (int)room;
         const int64_t most_blocks = whole * ((steps + 7) / 8);
         p.blocks = (int64_t)compute_units() * held;
         if (most_blocks < p.blocks) p.blocks = most_blocks;
@@ -132,6 +133,7 @@ inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
         int64_t splits = whole > 0 ? (int64_t)compute_units() * 2 / whole : 1;
         const int64_t most_splits = (span + 511) / 512;
         if (splits > most_splits) splits = most_splits;
+        if (splits > room) splits = room;
         if (splits < 1) splits = 1;
         p.chunk = ((span + splits - 1) / splits + 63) / 64 * 64;
         p.splits = (int)((span + p.chunk - 1) / p.chunk);

@@ -145,7 +145,7 @@ sffn_status_t kv_cache_read(const sffn_kv_cache_t* cache, const sffn_kv_batch_t*
                             const sffn_heads_t* v, sffn_dtype_t dtype, int64_t T, void* hip_stream);
 
 /* Workspace bytes of cache_attention for T tokens of n_q_heads heads (0 when
- * an argument is invalid or none is needed). */
+ * an argument is invalid or none is needed; 256 MiB at most). */
 size_t cache_attention_workspace_size(const sffn_kv_cache_t* cache, const sffn_kv_batch_t* batch,
                                       int32_t n_q_heads, sffn_dtype_t dtype, int32_t window, int64_t T);
 

@@ -7,7 +7,7 @@ import torch
 
 from oracle import attention_oracle as ao
 from tests.conftest import gpu_available
-from tests.test_gpu_cache_attention import BF, Setup, queries
+from tests.test_gpu_cache_attention import BF, F32, Setup, compare, queries
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
@@ -82,3 +82,48 @@ def test_the_same_bits_every_time_for_chunks_and_single_tokens(H):
     for _ in range(4):
         again = s.sffn.cache_attention(cache, batch, q, return_lse=True)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+# ---------------------------------------------------------------------------
+# many sequences: rows have fewer parts than their keys would fill, or one
+# ---------------------------------------------------------------------------
+
+def some_rows(s, o, lse, q, new, which):
+    """Sequences `which` against the reference (the bounds of test_gpu_cache_attention)."""
+    at = np.concatenate([[0], np.cumsum(new)])
+    for b in which:
+        a, e = at[b], at[b + 1]
+        k, v = s.tokens(b)
+        ref = ao.attend(q[a:e].double().cpu().numpy(), k, v, s.kv[b] - new[b], s.D ** -0.5)
+        compare(o[a:e], lse[a:e], ref, q.dtype)
+
+
+@pytest.mark.parametrize("B,H,dtype,parts", [(1000, 16, BF, 16), (4200, 32, BF, 1), (4200, 32, F32, 1)])
+def test_one_long_sequence_among_many_short_ones(B, H, dtype, parts):
+    """1000 sequences of 16 rows of 256 channels leave room for 16 parts a row: the
+    longest sequence is cut into fewer than its 40 shares; 4200 of 32 heads leave none."""
+    rng = np.random.default_rng(21)
+    kv = rng.integers(1, 60, B)
+    kv[B // 3] = 20000
+    s = Setup(kv.tolist(), H // 16, 256, 128, 22)
+    q = queries(B, H, 256, dtype, 23)
+    cache, batch = s.cache(), s.batch(max_kv=20000)
+    lib = s.sffn.load_library()
+    need = lib.cache_attention_workspace_size(cache._c, batch._c, H, int(dtype is BF), 0, B)
+    assert need == (0 if parts == 1 else B * H * (parts * 258 + 1) * 4)
+    o, lse = s.sffn.cache_attention(cache, batch, q, return_lse=True)
+    torch.cuda.synchronize()
+    some_rows(s, o, lse, q, [1] * B, [0, 1, B // 3 - 1, B // 3, B // 3 + 1, B // 2, B - 2, B - 1])
+
+
+def test_drafts_of_many_sequences():
+    """Two tiles of 16 rows (8 tokens of 4 heads) in 400 sequences, 25600 rows."""
+    rng = np.random.default_rng(24)
+    kv = rng.integers(8, 100, 400)
+    kv[[5, 399]] = [9000, 4000]
+    s = Setup(kv.tolist(), 2, 128, 64, 25)
+    new = [8] * 400
+    q = queries(3200, 8, 128, BF, 26)
+    o, lse = s.sffn.cache_attention(s.cache(), s.batch(new), q, return_lse=True)
+    torch.cuda.synchronize()
+    some_rows(s, o, lse, q, new, [0, 4, 5, 6, 200, 398, 399])
