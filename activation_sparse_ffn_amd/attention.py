@@ -29,6 +29,7 @@ __all__ = ["rope_table", "qk_norm_rope", "qk_norm_rope_backward", "KVCache", "Ca
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = (None, "linear", "ntk", "by_parts")
 _DTYPES = {torch.bfloat16: SFFN_BF16, torch.float32: SFFN_F32}
+_INT32_MAX = 2 ** 31 - 1
 _empty_strided = torch.empty_strided
 
 
@@ -325,16 +326,21 @@ class CacheBatch:
     cu[b + 1] of the call are its last. Without cu every sequence has one.
 
     block_table [B, max_pages], kv_lens [B], cu [B + 1]: int32 on the GPU.
-    max_new: at least every sequence's count of new tokens. max_kv: about the
-    largest kv_lens (it splits the work and never changes what is computed).
+    max_new: at least every sequence's count of new tokens; left out it is one
+    without cu, and with cu as many as the call has (a call of few tokens for each
+    of many sequences is faster if told so). A sequence's tokens beyond it are not
+    stored, and their rows are NaN. max_kv: about the largest kv_lens (it splits
+    the work and never changes what is computed).
     """
 
     def __init__(self, block_table: torch.Tensor, kv_lens: torch.Tensor, max_kv: int,
-                 cu: Optional[torch.Tensor] = None, max_new: int = 1):
+                 cu: Optional[torch.Tensor] = None, max_new: Optional[int] = None):
         if block_table.dim() != 2 or not block_table.is_cuda:
             raise ValueError("block_table must be [B, max_pages] on the GPU")
         B, pages = block_table.shape
         dev = block_table.device
+        if max_new is None:
+            max_new = 1 if cu is None else _INT32_MAX       # no sequence has more than the call
         self._c = _Batch(_address(block_table, "block_table", None, torch.int32, dev), pages,
                          _address(kv_lens, "kv_lens", (B,), torch.int32, dev),
                          None if cu is None else _address(cu, "cu", (B + 1,), torch.int32, dev),
@@ -368,7 +374,8 @@ def kv_cache_append(cache: KVCache, batch: CacheBatch, k: torch.Tensor, v: torch
 def kv_cache_read(cache: KVCache, batch: CacheBatch, total: int, dtype: torch.dtype = torch.bfloat16,
                   k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None):
     """The batch's `total` tokens out of the cache: (k, v), each [total,
-    kv_heads, head_dim], as the values the entries stand for."""
+    kv_heads, head_dim], as the values the entries stand for. Rows of tokens in no
+    sequence are left as k and v hold them (undefined where those are not given)."""
     lib = load_library()
     _same_device(cache, batch)
     if dtype not in _DTYPES:
@@ -395,7 +402,8 @@ def cache_attention(cache: KVCache, batch: CacheBatch, q: torch.Tensor, scale: O
     keys, its own among them. scale: head_dim^-0.5 by default. heads is a
     multiple of the cache's kv_heads. Returns out [T, heads, head_dim], with
     return_lse also the log of each row's sum, fp32 [T, heads]. A row that sees
-    no key gives zeros and -inf. The softmax weights of a bf16 q are kept to 16
+    no key gives zeros and -inf; rows of tokens in no sequence are left as out
+    holds them (undefined where it is not given). The softmax weights of a bf16 q are kept to 16
     bits, or to 8 in a sequence whose new tokens times heads / kv_heads are more
     than 128; those of an fp32 q to fp32."""
     lib = load_library()

@@ -1,9 +1,22 @@
 // Device helpers that the attention-side kernels share.
 #pragma once
 
+#include "attn_launch.hpp"
 #include "common.hpp"
 
 namespace sffn {
+
+// Tokens [from, to) of the call that belong to sequence b and are not computed: those
+// beyond its first max_new, or all of a sequence whose offsets leave the call. Their
+// rows are made NaN. False if there are none.
+__device__ __forceinline__ bool lost_tokens(const CacheArgs& c, int b, int& from, int& to) {
+    if (!c.cu) return false;            // one token each
+    const int T = (int)c.T, first = c.cu[b], last = c.cu[b + 1];
+    const bool inside = first >= 0 && last <= T;
+    from = inside ? first + c.max_new : first > 0 ? first : 0;
+    to = last < T ? last : T;
+    return from < to;
+}
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));

@@ -94,6 +94,21 @@ __device__ __forceinline__ void keys_seen(const AttnArgs& a, const Sequence& q, 
     if (hi < lo) hi = lo;
 }
 
+// NaN in the rows that lost_tokens names, heads h0 .. h1 - 1, by the whole workgroup.
+template <typename E, int D>
+__device__ __forceinline__ void lose_rows(const AttnArgs& a, int b, int h0, int h1) {
+    int from, to;
+    if (!lost_tokens(a.c, b, from, to)) return;
+    const float nan = __builtin_nanf(""), none[4] = {nan, nan, nan, nan};
+    const int64_t n = (int64_t)(to - from) * (h1 - h0) * (D / 4);
+    for (int64_t i = threadIdx.x; i < n; i += blockDim.x) {
+        const int64_t r = i / (D / 4), t = from + r / (h1 - h0);
+        const int h = h0 + (int)(r % (h1 - h0)), d = 4 * (int)(i % (D / 4));
+        store4(static_cast<E*>(a.out.p) + (t * a.out.st + h * a.out.sh) + d, none);
+        if (a.lse && d == 0) a.lse[t * a.Hq + h] = nan;
+    }
+}
+
 // The rows and keys of one piece of work.
 struct Work {
     int first, p0;          // as in Sequence
@@ -105,8 +120,10 @@ struct Work {
 };
 
 // Work of a workgroup of k_attend_rows: a row tile and a range of a.chunk keys.
-// False when the tile has no rows.
-__device__ __forceinline__ bool find_work(const AttnArgs& a, int tile_rows, Work& w) {
+// False when the tile has no rows. `lost(b, h)` is called by one workgroup for each
+// sequence and key head.
+template <typename F>
+__device__ __forceinline__ bool find_work(const AttnArgs& a, int tile_rows, Work& w, F lost) {
     const CacheArgs& c = a.c;
     uint32_t id = blockIdx.x;
     // Workgroup i runs on XCD i % 8: heads stay with their XCD's cache where there
@@ -140,6 +157,7 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int tile_rows, Work
         // short ones does not fall to some XCDs alone
         w.b = (int)((turn + (uint32_t)tile) % (uint32_t)c.B);
     }
+    if (tile == 0 && w.part == 0) lost(w.b, w.h);
     Sequence q;
     if (!find_sequence(a, w.b, q)) return false;
     const int64_t r0 = (int64_t)tile * tile_rows;
@@ -180,11 +198,12 @@ __device__ __forceinline__ int wave_scan(int v, Op op) {
 // they begin. Where there are workgroups enough, every unit begins a share of its own
 // (cost rounded up to shares), so that no workgroup has the end of one and the
 // beginning of the next one after another. `work(w, parts)` is called for each piece
-// of the workgroup's; a row whose part 0 it is has `parts` parts in all.
+// of the workgroup's; a row whose part 0 it is has `parts` parts in all. `lost(b)` is
+// called by one workgroup for each sequence with tokens that are not computed.
 constexpr int kLeast = 8;
 
-template <typename F>
-__device__ __forceinline__ void share_work(const AttnArgs& a, int tile_rows, F work) {
+template <typename F, typename L>
+__device__ __forceinline__ void share_work(const AttnArgs& a, int tile_rows, F work, L lost) {
     const int lane = threadIdx.x & 63;
     const int B = a.c.B, Hkv = a.c.Hkv;
     // 64 sequences from b0 on, one a lane: where they are, their units, a unit's steps
@@ -224,10 +243,20 @@ __device__ __forceinline__ void share_work(const AttnArgs& a, int tile_rows, F w
     auto longest_of = [&](const Lane& y) {
         return lane_value(wave_scan(y.units > 0 ? y.steps : 0, [](int p, int q) { return p > q ? p : q; }), 63);
     };
+    auto look_for_lost = [&](int b0) {
+        int from, to;
+        uint64_t found = __ballot(b0 + lane < B && lost_tokens(a.c, b0 + lane, from, to));
+        for (; found != 0; found &= found - 1) {
+            const uint32_t b = b0 + __ffsll((unsigned long long)found) - 1;
+            if (b % gridDim.x == blockIdx.x) lost((int)b);
+        }
+    };
     Lane x = look(0);
+    look_for_lost(0);
     int total = lane_value(x.cost, 63), longest = longest_of(x);
     for (int b0 = 64; b0 < B; b0 += 64) {
         const Lane y = look(b0);
+        look_for_lost(b0);
         const int l = longest_of(y);
         total += lane_value(y.cost, 63);
         longest = l > longest ? l : longest;
@@ -657,7 +686,9 @@ template <typename E, int NP, int PP, int D, int RT>
 __global__ __launch_bounds__(256, few_held(D, NP == 3, RT)) void k_attend_few(const AttnArgs a) {
     __shared__ float sm[4][16 * RT], sl[4][16 * RT];
     __shared__ __align__(16) float so[4][16 * RT][D + 4];
-    share_work(a, 16 * RT, [&](const Work& w, int parts) { attend_few<E, NP, PP, D, RT>(a, w, parts, sm, sl, so); });
+    share_work(
+        a, 16 * RT, [&](const Work& w, int parts) { attend_few<E, NP, PP, D, RT>(a, w, parts, sm, sl, so); },
+        [&](int b) { lose_rows<E, D>(a, b, 0, a.Hq); });
 }
 
 // ---------------------------------------------------------------------------
@@ -1066,13 +1097,17 @@ __global__ __launch_bounds__(64 * NW, NW == 8 || D == 256 || NP == 3 ? 1 : 2) vo
         attend_rows<E, NP, PP, D, NW>(a, w, parts, lds, scales);
     };
     if constexpr (SHARED) {
-        share_work(a, 32 * NW, [&](const Work& w, int parts) {
-            __syncthreads();        // the work before has been read from LDS
-            attend(w, parts);
-        });
+        share_work(
+            a, 32 * NW,
+            [&](const Work& w, int parts) {
+                __syncthreads();        // the work before has been read from LDS
+                attend(w, parts);
+            },
+            [&](int b) { lose_rows<E, D>(a, b, 0, a.Hq); });
     } else {
         Work w;
-        if (find_work(a, 32 * NW, w)) attend(w, a.splits);
+        auto lost = [&](int b, int h) { lose_rows<E, D>(a, b, h * a.G, (h + 1) * a.G); };
+        if (find_work(a, 32 * NW, w, lost)) attend(w, a.splits);
     }
 }
 

@@ -36,12 +36,13 @@ struct PageJob {
     int64_t t0;         // first token of the call in this page
     int held, m;        // tokens before it in the page, new tokens in the page
     int64_t early;      // call tokens before position 0 (more tokens than kv_lens says), first page's job only
-    int h;
+    bool beside;        // first page's job, which has the sequence's lost tokens to itself
+    int b, h;
     bool values;
     bool known;         // the page is one of the pool (row is then valid)
 };
 
-// Fills the job of this workgroup; false if it has nothing to do.
+// Fills the job of this workgroup; false if it has no token.
 __device__ bool page_job(const CacheArgs& c, int per_seq, PageJob& j) {
     uint32_t id = blockIdx.x;
     j.values = id & 1;
@@ -49,18 +50,20 @@ __device__ bool page_job(const CacheArgs& c, int per_seq, PageJob& j) {
     j.h = (int)(id % (uint32_t)c.Hkv);
     id /= (uint32_t)c.Hkv;
     const int b = (int)(id / (uint32_t)per_seq), nth = (int)(id % (uint32_t)per_seq);
+    j.b = b;
+    j.beside = nth == 0;
     int64_t first = b, last = b + 1;
     if (c.cu) {
         first = c.cu[b];
         last = c.cu[b + 1];
     }
     if (first < 0 || last > c.T || last <= first) return false;
-    const int64_t L = c.lens[b] > 0 ? c.lens[b] : 0;
-    const int64_t start = L - (last - first);                    // position of token `first`
+    const int64_t start = (c.lens[b] > 0 ? c.lens[b] : 0) - (last - first);     // position of token `first`
+    const int64_t end = start + (last - first < c.max_new ? last - first : c.max_new);
     const int64_t from = start > 0 ? start : 0;
     const int64_t page = (from >> c.shift) + nth;
     const int64_t lo = page * c.P > from ? page * c.P : from;
-    const int64_t hi = (page + 1) * c.P < L ? (page + 1) * c.P : L;
+    const int64_t hi = (page + 1) * c.P < end ? (page + 1) * c.P : end;
     j.early = nth == 0 && start < 0 ? -start : 0;
     j.t0 = first + (lo - start);
     j.held = (int)(lo - page * c.P);
@@ -270,12 +273,19 @@ __global__ __launch_bounds__(kThreads) void k_cache_read(const CacheArgs c, cons
                                                          int per_seq) {
     extern __shared__ uint32_t tile[];      // values: the page's rows [D][P]
     PageJob j;
-    if (!page_job(c, per_seq, j)) return;
+    const bool any = page_job(c, per_seq, j);
     const Heads& out = j.values ? v : k;
-    E* y = static_cast<E*>(out.p) + (j.t0 * out.st + (int64_t)j.h * out.sh);
     const int chunks = c.D / 8;
     const float none[8] = {__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""),
                            __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf("")};
+    int from, to;
+    if (j.beside && lost_tokens(c, j.b, from, to)) {
+        E* z = static_cast<E*>(out.p) + (from * out.st + (int64_t)j.h * out.sh);
+        for (int64_t i = threadIdx.x; i < (int64_t)(to - from) * chunks; i += kThreads)
+            store8(z + i / chunks * out.st + 8 * (i % chunks), none);
+    }
+    if (!any) return;
+    E* y = static_cast<E*>(out.p) + (j.t0 * out.st + (int64_t)j.h * out.sh);
     for (int64_t i = threadIdx.x; i < j.early * chunks; i += kThreads)
         store8(y + (i / chunks - j.early) * out.st + 8 * (i % chunks), none);
     if (!j.known) {

@@ -116,7 +116,10 @@ typedef struct {
  *   block_table [n_seqs] rows of max_pages int32 (row stride table_stride);
  *               max_pages * page at most 2^30, T at most 2^28
  *   kv_lens [n_seqs] int32, cu [n_seqs + 1] int32 ascending from 0, or NULL
- *   max_new   >= every cu[b + 1] - cu[b]; tokens beyond it are not processed
+ *   max_new   >= every cu[b + 1] - cu[b] (T always is); it splits the work. Tokens
+ *             of a sequence beyond its first max_new are not stored by an append;
+ *             a read and attention make their rows NaN, as they do with all rows
+ *             of a sequence whose offsets leave the call
  *   max_kv    about the largest kv_lens[b]: splits the work, never the result */
 typedef struct {
     const int32_t* block_table;

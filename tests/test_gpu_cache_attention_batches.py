@@ -64,7 +64,6 @@ def test_a_generous_max_new_costs_no_precision(max_new):
     import activation_sparse_ffn_amd as sffn
     s = Setup([700, 90], 2, 128, 64, 15)
     q = queries(2, 8, 128, BF, 16)
-    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
     batch = sffn.CacheBatch(i32(s.table), i32(s.kv), 700, i32([0, 1, 2]), max_new)
     o = sffn.cache_attention(s.cache(), batch, q)
     torch.cuda.synchronize()
@@ -127,3 +126,128 @@ def test_drafts_of_many_sequences():
     o, lse = s.sffn.cache_attention(s.cache(), s.batch(new), q, return_lse=True)
     torch.cuda.synchronize()
     some_rows(s, o, lse, q, new, [0, 4, 5, 6, 200, 398, 399])
+
+
+# ---------------------------------------------------------------------------
+# bounds that are left out, too small, or passed by the offsets
+# ---------------------------------------------------------------------------
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+@pytest.mark.parametrize("new", [[5, 1, 3], [40, 200, 1]])
+def test_max_new_left_out(new):
+    """With cu and no max_new any count of new tokens is taken."""
+    import activation_sparse_ffn_amd as sffn
+    s = Setup([90, 700, 33], 2, 64, 16, 31)
+    cu = i32(np.concatenate([[0], np.cumsum(new)]))
+    q = queries(sum(new), 4, 64, BF, 32)
+    batch = sffn.CacheBatch(i32(s.table), i32(s.kv), 700, cu)
+    cache = s.cache()
+    out, lse = sffn.cache_attention(cache, batch, q, out=torch.full_like(q, 7.0), return_lse=True)
+    torch.cuda.synchronize()
+    some_rows(s, out, lse, q, new, range(3))
+    told = s.batch(new)
+    x = torch.randn(sum(new), 2, 64, dtype=BF, device="cuda")
+    sffn.kv_cache_append(cache, batch, x, x)
+    for a, b in zip(sffn.kv_cache_read(cache, batch, sum(new)), sffn.kv_cache_read(cache, told, sum(new))):
+        assert torch.equal(a, b) and (a.float() - x.float()).abs().max() < 0.05
+
+
+def test_max_new_without_cu_is_one():
+    import activation_sparse_ffn_amd as sffn
+    s = Setup([9, 70], 2, 64, 16, 33)
+    assert sffn.CacheBatch(i32(s.table), i32(s.kv), 70).max_new == 1
+
+
+@pytest.mark.parametrize("H,most,max_kv", [
+    (4, 1, 700), (4, 1, 90000),             # few rows, whole and in shares
+    (8, 7, 700), (8, 7, 90000),             # two tiles of 16 rows
+    (64, 3, 700), (64, 3, 90000),           # row tiles
+])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_tokens_beyond_max_new_are_nan(H, most, max_kv, dtype):
+    import activation_sparse_ffn_amd as sffn
+    new = [most, most + 9, 0, 2 * most]
+    s = Setup([1900, 700, 33, 40], 2, 64, 16, 34)
+    cu = i32(np.concatenate([[0], np.cumsum(new)]))
+    T = sum(new) + 2                        # the last two tokens are in no sequence
+    q = queries(T, H, 64, dtype, 35)
+    batch = sffn.CacheBatch(i32(s.table), i32(s.kv), max_kv, cu, most)
+    out, lse = sffn.cache_attention(s.cache(), batch, q, out=torch.full_like(q, 7.0), return_lse=True)
+    torch.cuda.synchronize()
+    at = 0
+    for b, n in enumerate(new):
+        m = min(n, most)
+        if m:
+            k, v = s.tokens(b)
+            ref = ao.attend(q[at:at + m].double().cpu().numpy(), k, v, s.kv[b] - n, 0.125)
+            compare(out[at:at + m], lse[at:at + m], ref, dtype)
+        assert out[at + m:at + n].isnan().all() and lse[at + m:at + n].isnan().all()
+        at += n
+    assert (out[at:] == 7).all()
+
+
+def test_tokens_beyond_max_new_above_the_shared_rows():
+    import activation_sparse_ffn_amd as sffn
+    new = [400, 300, 1]
+    s = Setup([900, 310, 33], 2, 64, 64, 36)
+    cu = i32(np.concatenate([[0], np.cumsum(new)]))
+    q = queries(701, 64, 64, BF, 37)
+    out, lse = sffn.cache_attention(s.cache(), sffn.CacheBatch(i32(s.table), i32(s.kv), 900, cu, 290), q,
+                                    out=torch.full_like(q, 7.0), return_lse=True)
+    torch.cuda.synchronize()
+    good = sffn.cache_attention(s.cache(), s.batch(new), q)
+    bad = torch.zeros(701, dtype=torch.bool, device="cuda")
+    bad[290:400] = bad[690:700] = True
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    assert not out[~bad].isnan().any() and (out[~bad].float() - good[~bad].float()).abs().max() < 0.05
+
+
+def test_sequences_that_run_out_of_the_call_are_nan():
+    """cu beyond the call's tokens: the sequence's rows show it, in attention and in a
+    read, and nothing is stored."""
+    import activation_sparse_ffn_amd as sffn
+    s = Setup([90, 70], 2, 64, 16, 38)
+    for H in (4, 64):
+        q = queries(7, H, 64, BF, 39)
+        batch = sffn.CacheBatch(i32(s.table), i32(s.kv), 90, i32([0, 3, 9]), 6)
+        out, lse = sffn.cache_attention(s.cache(), batch, q, out=torch.full_like(q, 7.0), return_lse=True)
+        assert not out[:3].isnan().any() and out[3:].isnan().all() and lse[3:].isnan().all()
+    cache = s.cache()
+    before = [getattr(cache, n)[torch.from_numpy(s.table[1, :5])].clone() for n in ("keys", "values")]
+    x = torch.randn(7, 2, 64, dtype=BF, device="cuda")
+    sffn.kv_cache_append(cache, batch, x, x)
+    for a, n in zip(before, ("keys", "values")):
+        assert torch.equal(a, getattr(cache, n)[torch.from_numpy(s.table[1, :5])])
+    k = torch.full((7, 2, 64), 7.0, dtype=BF, device="cuda")
+    _, v = sffn.kv_cache_read(cache, batch, 7, k=k)
+    assert not k[:3].isnan().any() and k[3:].isnan().all() and v[3:].isnan().all()
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("most", [1, 5, 17])
+def test_append_and_read_take_max_new_tokens_and_no_more(page, most):
+    import activation_sparse_ffn_amd as sffn
+    kv, new = [100, 40], [30, 3]
+    s = Setup(kv, 2, 64, page, 40)
+    cu = i32([0, 30, 33])
+    x = torch.randn(33, 2, 64, dtype=BF, device="cuda")
+    few, all_ = s.cache(), s.cache()
+    small = sffn.CacheBatch(i32(s.table), i32(kv), 100, cu, most)
+    sffn.kv_cache_append(few, small, x, x)
+    # the same first tokens as a call of their own
+    m = [min(n, most) for n in new]
+    part = sffn.CacheBatch(i32(s.table), i32([k - n + i for k, n, i in zip(kv, new, m)]), 100,
+                           i32(np.concatenate([[0], np.cumsum(m)])), most)
+    sffn.kv_cache_append(all_, part, torch.cat([x[:m[0]], x[30:30 + m[1]]]), torch.cat([x[:m[0]], x[30:30 + m[1]]]))
+    for n in ("keys", "values", "k_scale", "v_scale"):
+        a, b = getattr(few, n), getattr(all_, n)
+        assert torch.equal(a.nan_to_num(-1) if a.is_floating_point() else a, b.nan_to_num(-1) if b.is_floating_point() else b), n
+    out = torch.full((33, 2, 64), 7.0, dtype=BF, device="cuda")
+    k, v = sffn.kv_cache_read(few, small, 33, k=out)
+    full = sffn.kv_cache_read(few, s.batch(new), 33)
+    for got, ref in zip((k, v), full):
+        for a, n, i in ((0, 30, m[0]), (30, 3, m[1])):
+            assert torch.equal(got[a:a + i], ref[a:a + i]) and got[a + i:a + n].isnan().all()
