@@ -10,6 +10,19 @@
 
 namespace sffn {
 
+// HIP takes fewer than 2^32 threads in a grid. Larger ones (of workgroups of up to
+// 512) are launched in pieces: launch(first, blocks) for each.
+constexpr int64_t kMostBlocks = (int64_t)1 << 22;
+template <typename F>
+inline hipError_t launch_in_pieces(int64_t blocks, F launch) {
+    for (int64_t first = 0; first < blocks; first += kMostBlocks) {
+        launch((uint32_t)first, (unsigned)(blocks - first < kMostBlocks ? blocks - first : kMostBlocks));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 // A [T, heads, head_dim] view (strides in elements).
 struct Heads {
     void* p;

@@ -42,6 +42,7 @@ struct AttnArgs {
     Heads q, out;
     int Hq, G, window, splits;
     int chunk, row_tiles;
+    uint32_t first_block;   // of this launch, where a call's workgroups take several
     float scale2;           // |scale| log2 e; a negative scale turns q round
     bool negate;
     float* lse;             // [T, Hq] or null
@@ -125,7 +126,7 @@ struct Work {
 template <typename F>
 __device__ __forceinline__ bool find_work(const AttnArgs& a, int tile_rows, Work& w, F lost) {
     const CacheArgs& c = a.c;
-    uint32_t id = blockIdx.x;
+    uint32_t id = a.first_block + blockIdx.x;
     // Workgroup i runs on XCD i % 8: heads stay with their XCD's cache where there
     // are eight of them.
     w.h = (int)(id % (uint32_t)c.Hkv);
@@ -1214,29 +1215,36 @@ __global__ __launch_bounds__(256) void k_attend_join(const AttnArgs a) {
 }
 
 template <typename E, int NP, int PP, int D, int NW>
-void launch_rows(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
-    const dim3 grid((unsigned)plan.blocks);
-    if (plan.shared) k_attend_rows<E, NP, PP, D, NW, true><<<grid, 64 * NW, 0, s>>>(a);
-    else k_attend_rows<E, NP, PP, D, NW, false><<<grid, 64 * NW, 0, s>>>(a);
+hipError_t launch_rows(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
+    if (plan.shared) {
+        k_attend_rows<E, NP, PP, D, NW, true><<<dim3((unsigned)plan.blocks), 64 * NW, 0, s>>>(a);
+        return hipGetLastError();
+    }
+    return launch_in_pieces(plan.blocks, [&](uint32_t first, unsigned n) {
+        AttnArgs piece = a;
+        piece.first_block = first;
+        k_attend_rows<E, NP, PP, D, NW, false><<<n, 64 * NW, 0, s>>>(piece);
+    });
 }
 
 template <typename E, int NP, int D>
 hipError_t launch(const AttnArgs& a, const AttnPlan& plan, hipStream_t s) {
     const dim3 grid((unsigned)plan.blocks);
+    hipError_t e = hipSuccess;
     if (plan.few) {
         k_attend_few<E, NP, NP == 1 ? 2 : 3, D, 1><<<grid, 256, 0, s>>>(a);
     } else if (plan.pair) {
         if constexpr (D <= 128) k_attend_few<E, NP, NP == 1 ? 2 : 3, D, 2><<<grid, 256, 0, s>>>(a);
     } else if constexpr (NP == 3) {
-        launch_rows<E, 3, 3, D, 4>(a, plan, s);
+        e = launch_rows<E, 3, 3, D, 4>(a, plan, s);
     } else if (plan.pieces == 2) {
-        launch_rows<E, 1, 2, D, 4>(a, plan, s);
+        e = launch_rows<E, 1, 2, D, 4>(a, plan, s);
     } else {
-        launch_rows<E, 1, 1, D, D <= 128 ? 8 : 4>(a, plan, s);
+        e = launch_rows<E, 1, 1, D, D <= 128 ? 8 : 4>(a, plan, s);
     }
-    hipError_t e = hipGetLastError();
+    if (e == hipSuccess) e = hipGetLastError();
     if (e != hipSuccess || plan.splits == 1) return e;
-    const int64_t rows = a.c.T * a.Hq;
+    const int64_t rows = a.c.T * a.Hq;      // half a million at most, for two parts each (kPartBytes)
     if (rows < kWaveRows) k_attend_join<E, D, 256><<<dim3((unsigned)rows), 256, 0, s>>>(a);
     else k_attend_join<E, D, 64><<<dim3((unsigned)((rows + 3) / 4)), 256, 0, s>>>(a);
     return hipGetLastError();

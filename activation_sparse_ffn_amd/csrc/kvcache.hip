@@ -43,8 +43,8 @@ struct PageJob {
 };
 
 // Fills the job of this workgroup; false if it has no token.
-__device__ bool page_job(const CacheArgs& c, int per_seq, PageJob& j) {
-    uint32_t id = blockIdx.x;
+__device__ bool page_job(const CacheArgs& c, int per_seq, uint32_t first_block, PageJob& j) {
+    uint32_t id = first_block + blockIdx.x;
     j.values = id & 1;
     id >>= 1;
     j.h = (int)(id % (uint32_t)c.Hkv);
@@ -133,11 +133,11 @@ __device__ __forceinline__ uint32_t raw_most(const Raw<float>& r) {
 
 template <typename E>
 __global__ __launch_bounds__(kThreads) void k_cache_append(const CacheArgs c, const Heads k, const Heads v,
-                                                           int per_seq) {
+                                                           int per_seq, uint32_t first_block) {
     __shared__ uint32_t wave_max[kThreads / 64];
     extern __shared__ uint32_t tile[];      // values: new entries, four tokens a word
     PageJob j;
-    if (!page_job(c, per_seq, j) || !j.known) return;
+    if (!page_job(c, per_seq, first_block, j) || !j.known) return;
     const Heads& in = j.values ? v : k;
     const E* x = static_cast<const E*>(in.p) + (j.t0 * in.st + (int64_t)j.h * in.sh);
     float* scale = (j.values ? c.v_scale : c.k_scale) + j.row;
@@ -270,10 +270,10 @@ __global__ __launch_bounds__(kThreads) void k_cache_append(const CacheArgs c, co
 
 template <typename E>
 __global__ __launch_bounds__(kThreads) void k_cache_read(const CacheArgs c, const Heads k, const Heads v,
-                                                         int per_seq) {
+                                                         int per_seq, uint32_t first_block) {
     extern __shared__ uint32_t tile[];      // values: the page's rows [D][P]
     PageJob j;
-    const bool any = page_job(c, per_seq, j);
+    const bool any = page_job(c, per_seq, first_block, j);
     const Heads& out = j.values ? v : k;
     const int chunks = c.D / 8;
     const float none[8] = {__builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""), __builtin_nanf(""),
@@ -342,18 +342,18 @@ __global__ __launch_bounds__(kThreads) void k_cache_read(const CacheArgs c, cons
 
 hipError_t launch_cache_append(const CacheArgs& c, const Heads& k, const Heads& v, hipStream_t s) {
     const int per_seq = (int)pages_touched(c.max_new, c.P);
-    const dim3 grid((unsigned)cache_copy_blocks(c));
-    if (c.dt == Dt::BF16) k_cache_append<uint16_t><<<grid, kThreads, tile_bytes(c), s>>>(c, k, v, per_seq);
-    else k_cache_append<float><<<grid, kThreads, tile_bytes(c), s>>>(c, k, v, per_seq);
-    return hipGetLastError();
+    return launch_in_pieces(cache_copy_blocks(c), [&](uint32_t first, unsigned n) {
+        if (c.dt == Dt::BF16) k_cache_append<uint16_t><<<n, kThreads, tile_bytes(c), s>>>(c, k, v, per_seq, first);
+        else k_cache_append<float><<<n, kThreads, tile_bytes(c), s>>>(c, k, v, per_seq, first);
+    });
 }
 
 hipError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v, hipStream_t s) {
     const int per_seq = (int)pages_touched(c.max_new, c.P);
-    const dim3 grid((unsigned)cache_copy_blocks(c));
-    if (c.dt == Dt::BF16) k_cache_read<uint16_t><<<grid, kThreads, tile_bytes(c), s>>>(c, k, v, per_seq);
-    else k_cache_read<float><<<grid, kThreads, tile_bytes(c), s>>>(c, k, v, per_seq);
-    return hipGetLastError();
+    return launch_in_pieces(cache_copy_blocks(c), [&](uint32_t first, unsigned n) {
+        if (c.dt == Dt::BF16) k_cache_read<uint16_t><<<n, kThreads, tile_bytes(c), s>>>(c, k, v, per_seq, first);
+        else k_cache_read<float><<<n, kThreads, tile_bytes(c), s>>>(c, k, v, per_seq, first);
+    });
 }
 
 }  // namespace sffn

@@ -434,10 +434,27 @@ int64_t backward_blocks(const RopeArgs& a) {
     return blocks < kBackwardBlocks ? blocks : kBackwardBlocks;
 }
 
+// A forward of tokens t .. t + n - 1 alone.
+template <typename E>
+RopeArgs tokens_of(const RopeArgs& a, int64_t t, int64_t n) {
+    RopeArgs b = a;
+    b.T = n;
+    if (b.pos) b.pos += t;
+    for (Heads* v : {&b.q, &b.k, &b.q_out, &b.k_out})
+        if (v->p) v->p = static_cast<E*>(v->p) + t * v->st;
+    return b;
+}
+
 template <typename E>
 hipError_t launch_wide(const RopeArgs& a, hipStream_t s) {
     const int per = groups_per_token(a), LH = lanes_per_head(a.D);
     const int64_t groups = a.T * per, gb = kThreads / LH;
+    if ((groups + gb - 1) / gb > kMostBlocks) {
+        // more than a grid holds: tokens in two halves
+        const int64_t t = a.T / 2;
+        const hipError_t e = launch_wide<E>(tokens_of<E>(a, 0, t), s);
+        return e != hipSuccess ? e : launch_wide<E>(tokens_of<E>(a, t, a.T - t), s);
+    }
     const dim3 grid((unsigned)((groups + gb - 1) / gb));
     if (LH == 8) k_rope<E, 8><<<grid, kThreads, 0, s>>>(a, per);
     else if (LH == 16) k_rope<E, 16><<<grid, kThreads, 0, s>>>(a, per);
@@ -459,7 +476,8 @@ hipError_t launch_wide_backward(const RopeArgs& a, hipStream_t s) {
 
 template <bool BWD>
 hipError_t launch_any(const RopeArgs& a, hipStream_t s) {
-    const int64_t blocks = BWD ? backward_blocks(a) : (a.T * (a.n_q + a.n_k) + 3) / 4;
+    int64_t blocks = BWD ? backward_blocks(a) : (a.T * (a.n_q + a.n_k) + 3) / 4;
+    if (blocks > kMostBlocks) blocks = kMostBlocks;         // waves then take several heads
     if (a.dt == Dt::BF16) k_rope_any<uint16_t, BWD><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
     else k_rope_any<float, BWD><<<dim3((unsigned)blocks), kThreads, 0, s>>>(a);
     return hipGetLastError();
