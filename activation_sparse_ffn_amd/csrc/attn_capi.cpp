@@ -186,8 +186,8 @@ sffn::CacheArgs cache_args(const sffn_kv_cache_t* c, const sffn_kv_batch_t* b, i
     a.cu = b->cu;
     a.B = b->n_seqs;
     a.max_pages = b->max_pages;
-    // no sequence has more new tokens than the call
-    a.max_new = (int)(b->max_new < T ? b->max_new : T);
+    // no sequence has more new tokens than the call, and without offsets each has one
+    a.max_new = !b->cu ? 1 : (int)(b->max_new < T ? b->max_new : T);
     a.max_kv = b->max_kv;
     a.T = T;
     a.dt = dtype == SFFN_BF16 ? sffn::Dt::BF16 : sffn::Dt::F32;
@@ -207,8 +207,7 @@ sffn_status_t cache_copy(const sffn_kv_cache_t* cache, const sffn_kv_batch_t* ba
     SFFN_TRY(check_heads(k, "k", T, cache->kv_heads, cache->head_dim, dt, true, out));
     SFFN_TRY(check_heads(v, "v", T, cache->kv_heads, cache->head_dim, dt, true, out));
     const sffn::CacheArgs a = cache_args(cache, batch, dt, T);
-    const int64_t pages = sffn::pages_touched(a.max_new, a.P) * a.B;
-    if (pages > kMaxGrid || pages * a.Hkv > kMaxGrid / 2)
+    if (sffn::cache_copy_blocks(a) > kMaxGrid)
         return fail(SFFN_ERR_UNSUPPORTED, "T = %lld is too large for one call", (long long)T);
     return hip_status(launch(a, view(k), view(v), static_cast<hipStream_t>(hip_stream)), what);
 }

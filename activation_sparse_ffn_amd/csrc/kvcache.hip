@@ -42,14 +42,41 @@ struct PageJob {
     bool known;         // the page is one of the pool (row is then valid)
 };
 
-// Fills the job of this workgroup; false if it has no token.
+// The last sequence whose places begin at `place` or before: the wave looks at 64
+// sequences at a time, evenly apart and then closer.
+__device__ __forceinline__ int sequence_at(const CacheArgs& c, int64_t place) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, hi = c.B;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 63) / 64, b = lane < (hi - lo + step - 1) / step ? lo + lane * step : -1;
+        const int at = b >= 0 ? c.cu[b] : 0;
+        const uint64_t before = __ballot(b >= 0 && first_place(at > 0 ? at : 0, b, c.shift) <= place);
+        const int k = before != 0 ? __popcll(before) - 1 : 0;
+        lo += k * step;
+        if (hi - lo > step) hi = lo + step;
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// Fills the job of this workgroup; false if it has no token. per_seq: places of each
+// sequence, 0 where they are by the call's tokens.
 __device__ bool page_job(const CacheArgs& c, int per_seq, uint32_t first_block, PageJob& j) {
     uint32_t id = first_block + blockIdx.x;
     j.values = id & 1;
     id >>= 1;
     j.h = (int)(id % (uint32_t)c.Hkv);
     id /= (uint32_t)c.Hkv;
-    const int b = (int)(id / (uint32_t)per_seq), nth = (int)(id % (uint32_t)per_seq);
+    int b, nth;
+    j.beside = false;
+    if (per_seq > 0) {
+        b = (int)(id / (uint32_t)per_seq);
+        nth = (int)(id % (uint32_t)per_seq);
+    } else {
+        b = sequence_at(c, id);
+        const int at = c.cu[b];
+        nth = (int)(id - first_place(at > 0 ? at : 0, b, c.shift));
+        if (nth < 0) return false;          // offsets that do not begin with 0
+    }
     j.b = b;
     j.beside = nth == 0;
     int64_t first = b, last = b + 1;
@@ -341,7 +368,7 @@ __global__ __launch_bounds__(kThreads) void k_cache_read(const CacheArgs c, cons
 }  // namespace
 
 hipError_t launch_cache_append(const CacheArgs& c, const Heads& k, const Heads& v, hipStream_t s) {
-    const int per_seq = (int)pages_touched(c.max_new, c.P);
+    const int per_seq = placed_by_tokens(c) ? 0 : (int)pages_touched(c.max_new, c.P);
     return launch_in_pieces(cache_copy_blocks(c), [&](uint32_t first, unsigned n) {
         if (c.dt == Dt::BF16) k_cache_append<uint16_t><<<n, kThreads, tile_bytes(c), s>>>(c, k, v, per_seq, first);
         else k_cache_append<float><<<n, kThreads, tile_bytes(c), s>>>(c, k, v, per_seq, first);
@@ -349,7 +376,7 @@ hipError_t launch_cache_append(const CacheArgs& c, const Heads& k, const Heads& 
 }
 
 hipError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v, hipStream_t s) {
-    const int per_seq = (int)pages_touched(c.max_new, c.P);
+    const int per_seq = placed_by_tokens(c) ? 0 : (int)pages_touched(c.max_new, c.P);
     return launch_in_pieces(cache_copy_blocks(c), [&](uint32_t first, unsigned n) {
         if (c.dt == Dt::BF16) k_cache_read<uint16_t><<<n, kThreads, tile_bytes(c), s>>>(c, k, v, per_seq, first);
         else k_cache_read<float><<<n, kThreads, tile_bytes(c), s>>>(c, k, v, per_seq, first);

@@ -1,7 +1,8 @@
 // The launchers of the attention-side operators against a faked HIP runtime that
 // records every launch: whatever size the entry points accept, each launch keeps to
 // HIP's limit (fewer than 2^32 threads in a grid) and all of them together cover the
-// work. Built and run by tests/test_attention_launch_limits.py.
+// work; a batch with one long prompt is not launched for prompts of all its
+// sequences. Built and run by tests/test_attention_launch_limits.py.
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -105,12 +106,15 @@ int main() {
     b.cu = static_cast<int32_t*>(dev(16));
     b.n_seqs = 256; b.max_pages = 8192; b.table_stride = 8192; b.max_new = 131072; b.max_kv = 131072;
     const sffn_heads_t kv{dev(17), 1024, 128};
-    // 255 single tokens beside a prompt of 131072
+    // 255 single tokens beside a prompt of 131072: of 33.6 million (sequence, page, head)
+    // places of keys and values 135 thousand have tokens
     const int64_t T = 131072 + 255;
     EXPECT_STATUS(kv_cache_append(&c, &b, &kv, &kv, SFFN_BF16, T, nullptr), SFFN_OK);
-    EXPECT(LAUNCHED() >= 131072 / 16 * 16);
+    uint64_t n = LAUNCHED();
+    EXPECT(n >= 131072 / 16 * 16 && n < 200000);
     EXPECT_STATUS(kv_cache_read(&c, &b, &kv, &kv, SFFN_BF16, T, nullptr), SFFN_OK);
-    EXPECT(LAUNCHED() >= 131072 / 16 * 16);
+    n = LAUNCHED();
+    EXPECT(n >= 131072 / 16 * 16 && n < 200000);
     // a decode step and a chunk alone: a workgroup for each page that can hold a token
     b.max_new = 1;
     EXPECT_STATUS(kv_cache_append(&c, &b, &kv, &kv, SFFN_BF16, 256, nullptr), SFFN_OK);
@@ -118,6 +122,22 @@ int main() {
     b.n_seqs = 1; b.max_new = 4095;
     EXPECT_STATUS(kv_cache_append(&c, &b, &kv, &kv, SFFN_BF16, 4095, nullptr), SFFN_OK);
     EXPECT(LAUNCHED() == 257 * 8 * 2);
+    // where pages have places by the call's tokens, every page that a sequence can touch
+    // has one of its own, and all are launched
+    std::mt19937 rng(1);
+    for (int trial = 0; trial < 3000; ++trial) {
+        const int shift = 4 + (int)(rng() % 4), P = 1 << shift, B = 1 + (int)(rng() % 40);
+        int64_t at = 0, next = 0;
+        for (int s = 0; s < B; ++s) {
+            const int64_t held = rng() % 300, m = rng() % 3 == 0 ? rng() % 500 : rng() % 4;
+            const int64_t pages = m == 0 ? 0 : (held + m - 1) / P - held / P + 1;
+            const int64_t first = sffn::first_place((int)at, s, shift);
+            EXPECT(first >= next && pages <= sffn::pages_touched(m, P));
+            next = first + (pages > 0 ? pages : 1);
+            at += m;
+        }
+        EXPECT(next <= sffn::places_by_tokens(at, B, P));
+    }
     // all sizes of the header's ranges are taken or refused, none fails in a launch
     for (int heads : {1, 8, 64, 1000})
         for (int page : {16, 128})

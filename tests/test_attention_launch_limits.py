@@ -1,6 +1,6 @@
 """The launchers of the attention-side operators on the host alone, against a faked
 HIP runtime that records every launch (tests/host/launch_limits.cpp): no grid of
-2^32 threads or more."""
+2^32 threads or more, no workgroups for tokens that cannot exist."""
 import os
 import re
 import subprocess

@@ -7,7 +7,7 @@ import torch
 
 from oracle import attention_oracle as ao
 from tests.conftest import gpu_available
-from tests.test_gpu_cache_attention import BF, F32, Setup, compare, queries
+from tests.test_gpu_cache_attention import BF, F32, Setup, Twin, compare, queries
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
@@ -251,3 +251,84 @@ def test_append_and_read_take_max_new_tokens_and_no_more(page, most):
     for got, ref in zip((k, v), full):
         for a, n, i in ((0, 30, m[0]), (30, 3, m[1])):
             assert torch.equal(got[a:a + i], ref[a:a + i]) and got[a + i:a + n].isnan().all()
+
+
+# ---------------------------------------------------------------------------
+# append and read: a long prompt beside many sequences of a few tokens, whose pages
+# have places by the call's tokens
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,page,D", [(70, 16, 64), (300, 64, 128), (20, 32, 256)])
+def test_append_of_a_prompt_beside_single_tokens(B, page, D, dtype):
+    """Entries and scales bit for bit, some sequences with no new token."""
+    rng = np.random.default_rng(B)
+    held = rng.integers(0, 3 * page, B)
+    t = Twin(held.tolist(), 2, D, page, seed=41, room=700)
+    for step, (who, n) in enumerate(((B // 2, 650), (0, 600))):
+        new = rng.integers(0, 4, B)
+        new[who], new[B - 1] = n, 1
+        t.append(new.tolist(), dtype, 42 + step, size=1.0 + step)
+    s = t.s
+    cu = np.concatenate([[0], np.cumsum(new)])
+    batch = s.sffn.CacheBatch(i32(s.table), i32(t.kv), max(t.kv), i32(cu), int(new.max()))
+    got = s.sffn.kv_cache_read(t.gpu, batch, int(cu[-1]), dtype)
+    ref = [t.cpu.read(s.table[b], t.kv[b] - n, t.kv[b]) for b, n in enumerate(new)]
+    for x, i in zip(got, (0, 1)):
+        want = torch.from_numpy(np.concatenate([r[i] for r in ref]).astype(np.float32)).to(dtype)
+        assert torch.equal(x.cpu(), want)
+
+
+def test_append_beside_thousands_of_sequences():
+    """5000 sequences (looked up in two steps): what calls of the single tokens and of
+    the prompt alone store."""
+    import activation_sparse_ffn_amd as sffn
+    B, long_one, n, P = 5000, 3210, 900, 16
+    rng = np.random.default_rng(43)
+    kv = rng.integers(1, 40, B)
+    kv[long_one] = n + 21
+    s = Setup(kv.tolist(), 1, 64, P, 44)
+    new = (rng.random(B) < 0.8).astype(int)
+    new[long_one] = n
+    cu = np.concatenate([[0], np.cumsum(new)])
+    T = int(cu[-1])
+    x = torch.randn(T, 1, 64, device="cuda")
+    a, b = s.cache(), s.cache()
+    sffn.kv_cache_append(a, sffn.CacheBatch(i32(s.table), i32(kv), 1000, i32(cu), n), x, x)
+    at = int(cu[long_one])
+    one = new.copy()
+    one[long_one] = 0
+    rest = torch.cat([x[:at], x[at + n:]])
+    sffn.kv_cache_append(b, sffn.CacheBatch(i32(s.table), i32(kv), 1000, i32(np.concatenate([[0], np.cumsum(one)])), 1),
+                         rest, rest)
+    row = s.table[long_one:long_one + 1]
+    sffn.kv_cache_append(b, sffn.CacheBatch(i32(row), i32([n + 21]), 1000, i32([0, n]), n), x[at:at + n], x[at:at + n])
+    for name in ("keys", "values", "k_scale", "v_scale"):
+        assert torch.equal(getattr(a, name).view(torch.uint8), getattr(b, name).view(torch.uint8)), name
+    batch = sffn.CacheBatch(i32(s.table), i32(kv), 1000, i32(cu), n)
+    k, v = sffn.kv_cache_read(a, batch, T, torch.float32)
+    assert (k - x).abs().max() < 0.05 and (v - x).abs().max() < 0.05
+
+
+def test_lost_tokens_among_many_sequences():
+    """Beyond max_new, and behind the call's end, where pages have places by tokens."""
+    import activation_sparse_ffn_amd as sffn
+    B, P = 100, 16
+    kv = [400] + [20] * (B - 1)
+    s = Setup(kv, 1, 64, P, 45)
+    new = [300] + [1] * (B - 1)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    cu[-1] += 4                             # the last sequence leaves the call
+    T = 300 + B - 1
+    cache = s.cache()
+    k = torch.full((T, 1, 64), 7.0, device="cuda")
+    sffn.kv_cache_read(cache, sffn.CacheBatch(i32(s.table), i32(kv), 400, i32(cu), 290), T, torch.float32, k=k)
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    bad[290:300] = bad[-1] = True
+    assert k[bad].isnan().all() and not k[~bad].isnan().any() and not (k[~bad] == 7).all()
+    x = torch.full((T, 1, 64), 3.0, device="cuda")
+    before = cache.keys[torch.from_numpy(s.table[B - 1, :2])].clone()
+    sffn.kv_cache_append(cache, sffn.CacheBatch(i32(s.table), i32(kv), 400, i32(cu), 290), x, x)
+    assert torch.equal(before, cache.keys[torch.from_numpy(s.table[B - 1, :2])])
+    back, _ = sffn.kv_cache_read(cache, sffn.CacheBatch(i32(s.table), i32(kv), 400, i32(cu), 290), T, torch.float32)
+    assert (back[~bad] - 3).abs().max() < 0.02
