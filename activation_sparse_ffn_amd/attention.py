@@ -123,6 +123,12 @@ def _new(shape, dtype, device):
     return t, _Heads(t.data_ptr(), H * D, D)
 
 
+def _int32(n: int) -> int:
+    """A count or bound as the library's int32 (ctypes would take its low bits): past 31
+    bits it bounds nothing, below zero it is refused there."""
+    return n if 0 <= n <= _INT32_MAX else _INT32_MAX if n > 0 else -1
+
+
 def _vector(n, dtype, device):
     return _empty_strided((n,), (1,), dtype=dtype, device=device)
 
@@ -344,7 +350,7 @@ class CacheBatch:
         self._c = _Batch(_address(block_table, "block_table", None, torch.int32, dev), pages,
                          _address(kv_lens, "kv_lens", (B,), torch.int32, dev),
                          None if cu is None else _address(cu, "cu", (B + 1,), torch.int32, dev),
-                         B, pages, max_new, max_kv)
+                         B, pages, _int32(max_new), _int32(max_kv))
         self.block_table, self.kv_lens, self.cu, self.device = block_table, kv_lens, cu, dev
         self.max_kv, self.max_new = max_kv, max_new
 
@@ -420,6 +426,7 @@ def cache_attention(cache: KVCache, batch: CacheBatch, q: torch.Tensor, scale: O
         ho = _heads(out, "out", shape, dtype, dev)
     lse = _empty_strided((T, heads), (heads, 1), dtype=torch.float32, device=dev) if return_lse else None
     dt = _DTYPES[dtype]
+    window = _int32(window)
     if workspace is None:
         need = lib.cache_attention_workspace_size(cache._c, batch._c, heads, dt, window, T)
         workspace = _vector(need, torch.uint8, dev) if need else None

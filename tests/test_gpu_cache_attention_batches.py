@@ -332,3 +332,22 @@ def test_lost_tokens_among_many_sequences():
     assert torch.equal(before, cache.keys[torch.from_numpy(s.table[B - 1, :2])])
     back, _ = sffn.kv_cache_read(cache, sffn.CacheBatch(i32(s.table), i32(kv), 400, i32(cu), 290), T, torch.float32)
     assert (back[~bad] - 3).abs().max() < 0.02
+
+
+@pytest.mark.parametrize("much", [2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 3, 2 ** 40])
+def test_bounds_of_more_than_31_bits(much):
+    """A window, max_new or max_kv past 31 bits means all, not its low bits."""
+    import activation_sparse_ffn_amd as sffn
+    s = Setup([300, 50], 2, 64, 16, 46)
+    q = queries(6, 4, 64, BF, 47)
+    cache, cu = s.cache(), i32([0, 4, 6])
+    ref = sffn.cache_attention(cache, sffn.CacheBatch(i32(s.table), i32(s.kv), 300, cu, 6), q)
+    got = sffn.cache_attention(cache, sffn.CacheBatch(i32(s.table), i32(s.kv), 300, cu, much), q,
+                               out=torch.full_like(q, 7.0), window=much)
+    assert torch.equal(got, ref)
+    got = sffn.cache_attention(cache, sffn.CacheBatch(i32(s.table), i32(s.kv), much, cu, 6), q)
+    assert (got.float() - ref.float()).abs().max() < 2.0 ** -6 * ref.float().abs().max()
+    with pytest.raises(sffn.SparseFFNError):
+        sffn.cache_attention(cache, sffn.CacheBatch(i32(s.table), i32(s.kv), 300, cu, 6), q, window=-much - 1)
+    with pytest.raises(sffn.SparseFFNError):
+        sffn.cache_attention(cache, sffn.CacheBatch(i32(s.table), i32(s.kv), 300, cu, -much - 1), q)
