@@ -811,9 +811,10 @@ __device__ __forceinline__ void attend_rows(const AttnArgs& a, const Work& w, in
             // scale the logarithm (base 2) and the reciprocal of one factor, and the
             // other factor. The first goes into the exponent, so it may not take
             // weights that count to where fp32 ends: scales far from 1 are a mantissa
-            // and a power of two there, all others themselves and 1.
+            // and a power of two there, all others themselves and 1. What is not finite
+            // is the other factor: the sum of the weights does not know the values.
             float first = vs, rest = 1.f;
-            if (vs < 0x1p-64f || vs > 0x1p100f) {
+            if (!(vs >= 0x1p-64f && vs <= 0x1p100f)) {
                 const bool finite = vs > 0.f && vs < __builtin_huge_valf();
                 first = finite ? 2.f * __builtin_amdgcn_frexp_mantf(vs) : 1.f;
                 rest = finite ? __builtin_amdgcn_ldexpf(1.f, __builtin_amdgcn_frexp_expf(vs) - 1) : vs;

@@ -351,3 +351,22 @@ def test_bounds_of_more_than_31_bits(much):
         sffn.cache_attention(cache, sffn.CacheBatch(i32(s.table), i32(s.kv), 300, cu, 6), q, window=-much - 1)
     with pytest.raises(sffn.SparseFFNError):
         sffn.cache_attention(cache, sffn.CacheBatch(i32(s.table), i32(s.kv), 300, cu, -much - 1), q)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("H,n", [(4, 2), (8, 6), (8, 20), (8, 70)])
+def test_lse_does_not_know_the_values(H, n, bad, dtype):
+    """A page of values that are not finite shows in the rows that see it, not in the
+    statistics, whichever kernel takes them (lse within 2^-17 + 2^-19 a of the reference,
+    as everywhere: the scale's way through the exponent rounds differently)."""
+    s = Setup([300], 2, 64, 16, 48)
+    q = queries(n, H, 64, dtype, 49)
+    good, _ = s.sffn.cache_attention(s.cache(), s.batch([n]), q, return_lse=True)
+    k, v = s.tokens(0)
+    _, ref, _, a = ao.attend(q.double().cpu().numpy(), k, v, 300 - n, 0.125)
+    s.v_scale[s.table[0, 3], 0] = bad
+    o, lse = s.sffn.cache_attention(s.cache(), s.batch([n]), q, return_lse=True)
+    G = H // 2
+    assert (np.abs(lse.double().cpu().numpy() - ref) <= 2.0 ** -17 + 2.0 ** -19 * a).all()
+    assert torch.equal(o[:, G:], good[:, G:]) and not o[:, :G].isfinite().any()
