@@ -89,7 +89,7 @@ hipError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v,
 // Workgroups of k_attend_few that a compute unit holds. (Two tiles of rows of heads
 // of 128 spill 32 bytes a lane so; 32 ragged sequences of 6 tokens of 4 heads take
 // 74 us, at one workgroup without spills 112: loads in flight are what counts.)
-constexpr int few_held(int D, bool f32, int tiles) { return D > 128 || f32 ? 1 : 2; }
+constexpr int few_held(int D, bool f32) { return D > 128 || f32 ? 1 : 2; }
 
 // How one call is cut up: row tiles of `rows` (token, head) rows for each sequence
 // and key head (few: one tile of 16 holds every sequence's). Shared: `blocks`
@@ -147,7 +147,7 @@ inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
     if (p.shared) {
         // no share is less than 8 steps of 64 keys (see share_work); the chip holds one
         // workgroup a compute unit of the largest kinds, else two
-        const int64_t held = p.few || p.pair ? few_held(c.D, c.dt == Dt::F32, p.pair ? 2 : 1)
+        const int64_t held = p.few || p.pair ? few_held(c.D, c.dt == Dt::F32)
                                              : c.D > 128 || c.dt == Dt::F32 || p.waves == 8 ? 1 : 2;
         p.chunk = 8 * 64;
         p.splits = steps <= 8 ? 1 : (int)(steps / 8 + 2);

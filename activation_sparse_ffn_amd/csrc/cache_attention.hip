@@ -684,7 +684,7 @@ __device__ __forceinline__ void attend_few(const AttnArgs& a, const Work& w, int
 }
 
 template <typename E, int NP, int PP, int D, int RT>
-__global__ __launch_bounds__(256, few_held(D, NP == 3, RT)) void k_attend_few(const AttnArgs a) {
+__global__ __launch_bounds__(256, few_held(D, NP == 3)) void k_attend_few(const AttnArgs a) {
     __shared__ float sm[4][16 * RT], sl[4][16 * RT];
     __shared__ __align__(16) float so[4][16 * RT][D + 4];
     share_work(
