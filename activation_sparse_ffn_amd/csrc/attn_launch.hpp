@@ -87,8 +87,9 @@ hipError_t launch_cache_read(const CacheArgs& c, const Heads& k, const Heads& v,
 
 // ---- attention over the cache -----------------------------------------------------
 // Workgroups of k_attend_few that a compute unit holds. (Two tiles of rows of heads
-// of 128 spill 32 bytes a lane so; 32 ragged sequences of 6 tokens of 4 heads take
-// 74 us, at one workgroup without spills 112: loads in flight are what counts.)
+// of 128 spill 24 bytes a lane so; 32 ragged sequences of 6 tokens of 4 heads took
+// 74 us, at one workgroup without spills 112: loads in flight are what counts. For an
+// fp32 q the pieces leave registers for one: the same in fp32 113.)
 constexpr int few_held(int D, bool f32) { return D > 128 || f32 ? 1 : 2; }
 
 // How one call is cut up: row tiles of `rows` (token, head) rows for each sequence
@@ -113,9 +114,13 @@ constexpr int kPreciseRows = 128;
 
 // Calls of up to so many rows are shared out evenly, whatever their lengths, and
 // joined (a join of 32768 rows takes 15 us); larger ones have row tiles to fill the
-// chip without. (32 sequences of 1 .. 32768 keys, one token of 32 heads to one of
-// keys: 61 us shared, 240 as a workgroup for each range of keys; 32 tokens of one
-// sequence, where every length is the same, 39 against 36.)
+// chip without, and shares of theirs are uneven (6 prompts of 30 to 1500 tokens, 28
+// heads: 285 us shared, 217 as a workgroup for each row tile). Below, with the join,
+// shared and as a workgroup for each range of keys: 32 ragged sequences of 60 tokens
+// of 4 heads 207 and 506 us; 64 tokens beside 31 single ones 182 and 497, 512 beside
+// them 437 and 928; 6 prompts of up to 150 tokens 55 and 64; 256 tokens over 32768
+// keys 147 and 165; 32 tokens of one sequence, where every length is the same, 47 and
+// 47.
 constexpr int64_t kSharedRows = 32768;
 // The parts of rows take up to so much workspace in any call. Few sequences stay far
 // below it (32 of 32768 keys, 32 heads of 128: 34 MiB); many need few parts each,

@@ -198,7 +198,10 @@ __device__ __forceinline__ int wave_scan(int v, Op op) {
 // steps, or all where nothing joins parts, go whole to the workgroup in whose share
 // they begin. Where there are workgroups enough, every unit begins a share of its own
 // (cost rounded up to shares), so that no workgroup has the end of one and the
-// beginning of the next one after another. `work(w, parts)` is called for each piece
+// beginning of the next one after another. A workgroup looks at all lengths twice, 64
+// at a time: nothing for 64 sequences, but 1024 of 1 to 200 keys take 124 us (64 of
+// them 10.6), 1024 of 1 to 4096 310 + 16 (200 at a copy's rate), and the state of the
+// walk costs every kernel that shares 47 to 82 spilled scalars. `work(w, parts)` is called for each piece
 // of the workgroup's; a row whose part 0 it is has `parts` parts in all. `lost(b)` is
 // called by one workgroup for each sequence with tokens that are not computed.
 constexpr int kLeast = 8;
@@ -472,9 +475,9 @@ __device__ __forceinline__ float row_lse(float M, float l, bool seen) {
 // own running softmax, straight from memory into matrix operands; they meet in
 // LDS at the end. The values of a step and the keys of the next are in flight while
 // it computes: 16 KB a wave of heads of 128, 33 MB over the chip, which its memory
-// needs to stream. One token over 32768 keys of 8 heads of 128 (67 MB): 18.6 us, of
-// which 13 are the bytes at a copy's rate; 32 ragged sequences (237 MB): 55.6 us,
-// 4.3 TB/s.
+// needs to stream. One token over 32768 keys of 8 heads of 128 (67 MB): 19.2 us, of
+// which 13 are the bytes at a copy's rate; 32 ragged sequences (237 MB): 57 us, 4.2
+// TB/s; with an fp32 q 22 and 82 (one workgroup a compute unit).
 //
 // v_mfma_f32_16x16x32_bf16: lane l holds operand row (A) or column (B) l % 16,
 // k = 8 (l / 16) .. + 7, and of the result column l % 16, rows 4 (l / 16) ..
@@ -713,7 +716,8 @@ __global__ __launch_bounds__(256, few_held(D, NP == 3)) void k_attend_few(const 
 // of which the matrix cores are busy for 2050, and what shortens it lowers the
 // clock (1.8 to 2.1 GHz; with a cache of zeros, which costs less power, a version
 // of 1.92 ms took 1.63). A chunk of 4096 tokens over 32768 keys, 32 heads of 128:
-// 1.82 ms, 1.13 PF, 82% of what a library's product of 16384^3 reaches.
+// 1.89 ms (median; least 1.81), 1.09 PF, 79% of what a library's product of 16384^3
+// reaches.
 //
 // What a wave loads lies in one page, so page entries and addresses are scalar.
 //

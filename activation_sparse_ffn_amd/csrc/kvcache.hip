@@ -12,15 +12,18 @@
 // of values, so that the maximum, the rescaling and the store are one kernel
 // and no two workgroups share a scale; what it costs is the chain lengths ->
 // table -> rows -> maximum -> store, so a thread's loads are all in flight at once
-// and stay in registers for the rounding. A thread's piece is four tokens of
+// and stay in registers for the rounding. (In an append the link from the table to
+// the rows is the code's own: page_job reads the entry first, though the new tokens'
+// addresses do not need it. In a read it is the data's.) A thread's piece is four tokens of
 // eight channels: four tokens of a channel are one word of the values' order
 // ([D][P]), which they reach through LDS in whole words. Held entries are touched
 // only where the scale grew.
 //
-// One token in each of 32 sequences (8 heads of 128): 5.6 us, launch and chain. A
-// chunk of 4095 tokens (17 MB in, 8.4 MB out, a copy's 5 us): 12.3 us, one round of
-// 1040 workgroups that all wait for the same links of the chain; with the values'
-// bytes stored one at a time 16.7. Reading that chunk back: 7.5 us, 3.4 TB/s.
+// One token in each of 32 sequences (8 heads of 128): 5.7 us, launch and chain (fp32
+// 5.7). A chunk of 4095 tokens (17 MB in, 8.4 MB out, a copy's 5 us): 12.2 us, one
+// round of 1040 workgroups that all wait for the same links of the chain; with the
+// values' bytes stored one at a time 16.7; from fp32 12.1. Reading that chunk back:
+// 7.8 us, 3.2 TB/s, to fp32 12.4.
 #include "attn_common.hpp"
 #include "attn_launch.hpp"
 

@@ -292,10 +292,17 @@ __global__ __launch_bounds__(16 * kSumRows) void k_rope_sum(const float* __restr
 // elements l, l + 64, .... A pair's other element is read from memory as well,
 // before anything is written, so an output may be its own input.
 //
-// The gradient's difference u - x^ mean(u x^) cancels where u is nearly along
-// x^, as in heads of a few elements, which come here (with one element it
-// leaves eps r^2 of its terms). So this kernel takes r, x^, the mean and the
-// difference in 64 bits; it waits for memory either way.
+// It takes what the 16-byte kernels do not (see wide): heads of a size that eight
+// does not divide, rotated parts that do not fill eights of both halves, rows that
+// are not 16-byte aligned. Each element is read twice, 2 or 4 bytes at a time, and
+// the table's row again for every head: 4096 tokens of 40 heads of 80, 40 of them
+// rotated in halves, take 112 us, their gradient 158 + 4.6 (with 32 rotated, by the
+// 16-byte kernels, 18.7 and 26 + 4.0).
+//
+// The gradient's difference u - x^ mean(u x^) cancels where u is nearly along x^,
+// most of all in heads of a few elements (with one it leaves eps r^2 of its terms);
+// those of fewer than eight come here. So this kernel takes r, x^, the mean and the
+// difference in 64 bits.
 // ---------------------------------------------------------------------------
 constexpr int kPer = 8;     // 512 / 64
 
