@@ -20,7 +20,7 @@
 // only where the scale grew.
 //
 // One token in each of 32 sequences (8 heads of 128): 5.7 us, launch and chain (fp32
-// 5.7). A chunk of 4095 tokens (17 MB in, 8.4 MB out, a copy's 5 us): 12.2 us, one
+// 5.7; 7.6 where every scale grows and up to 63 held tokens are rounded again). A chunk of 4095 tokens (17 MB in, 8.4 MB out, a copy's 5 us): 12.2 us, one
 // round of 1040 workgroups that all wait for the same links of the chain; with the
 // values' bytes stored one at a time 16.7; from fp32 12.1. Reading that chunk back:
 // 7.8 us, 3.2 TB/s, to fp32 12.4.
