@@ -1,5 +1,6 @@
 """Predictor-gated bank-wise sparse SwiGLU FFN forward on AMD MI355X, and the
-attention-side operators of the layer around it (see attention.py).
+operators of the layer around it: its attention side (see attention.py) and the norm
+between its halves (norm.py).
 
 A thin ctypes binding over libsparse_ffn.so (include/sparse_ffn.h). Every
 step of the forward runs in the library's HIP kernels; this module only
@@ -28,7 +29,7 @@ __all__ = ["SparseFFN", "bank_topk", "library_path", "load_library", "SparseFFNE
            "SFFN_OK", "SFFN_ERR_INVALID_ARG", "SFFN_ERR_UNSUPPORTED", "SFFN_ERR_WORKSPACE",
            "SFFN_ERR_HIP", "Config", "EXPORTED_SYMBOLS",
            "rope_table", "qk_norm_rope", "qk_norm_rope_backward", "KVCache", "CacheBatch", "kv_cache_append",
-           "kv_cache_read", "cache_attention"]
+           "kv_cache_read", "cache_attention", "add_rms_norm", "add_rms_norm_backward"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 
@@ -104,6 +105,7 @@ def load_library():
     lib.sparse_ffn_forward_noalloc.argtypes = [P, P, I64, P, P, P, P]
     lib.sparse_ffn_forward_noalloc.restype = st
     attention.declare(lib)
+    norm.declare(lib)
     _LIB = lib
     return lib
 
@@ -345,8 +347,9 @@ class SparseFFN:
             pass
 
 
-from . import attention  # noqa: E402 (it uses the helpers above)
+from . import attention, norm  # noqa: E402 (they use the helpers above)
 from .attention import (CacheBatch, KVCache, cache_attention, kv_cache_append, kv_cache_read,  # noqa: E402
                         qk_norm_rope, qk_norm_rope_backward, rope_table)
+from .norm import add_rms_norm, add_rms_norm_backward  # noqa: E402
 
-EXPORTED_SYMBOLS = EXPORTED_SYMBOLS + attention.EXPORTED_SYMBOLS
+EXPORTED_SYMBOLS = EXPORTED_SYMBOLS + attention.EXPORTED_SYMBOLS + norm.EXPORTED_SYMBOLS
