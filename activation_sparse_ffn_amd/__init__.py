@@ -1,6 +1,6 @@
 """Predictor-gated bank-wise sparse SwiGLU FFN forward on AMD MI355X, and the
-operators of the layer around it: its attention side (see attention.py) and the norm
-between its halves (norm.py).
+operators of the layer around it: its attention side (see attention.py), the norm
+between its halves (norm.py) and the bookkeeping of cache pages (paging.py).
 
 A thin ctypes binding over libsparse_ffn.so (include/sparse_ffn.h). Every
 step of the forward runs in the library's HIP kernels; this module only
@@ -29,7 +29,8 @@ __all__ = ["SparseFFN", "bank_topk", "library_path", "load_library", "SparseFFNE
            "SFFN_OK", "SFFN_ERR_INVALID_ARG", "SFFN_ERR_UNSUPPORTED", "SFFN_ERR_WORKSPACE",
            "SFFN_ERR_HIP", "Config", "EXPORTED_SYMBOLS",
            "rope_table", "qk_norm_rope", "qk_norm_rope_backward", "KVCache", "CacheBatch", "kv_cache_append",
-           "kv_cache_read", "cache_attention", "add_rms_norm", "add_rms_norm_backward"]
+           "kv_cache_read", "cache_attention", "add_rms_norm", "add_rms_norm_backward",
+           "PagePlan", "free_pages", "page_plan", "cache_slots"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 
@@ -106,6 +107,7 @@ def load_library():
     lib.sparse_ffn_forward_noalloc.restype = st
     attention.declare(lib)
     norm.declare(lib)
+    paging.declare(lib)
     _LIB = lib
     return lib
 
@@ -347,9 +349,10 @@ class SparseFFN:
             pass
 
 
-from . import attention, norm  # noqa: E402 (they use the helpers above)
+from . import attention, norm, paging  # noqa: E402 (they use the helpers above)
 from .attention import (CacheBatch, KVCache, cache_attention, kv_cache_append, kv_cache_read,  # noqa: E402
                         qk_norm_rope, qk_norm_rope_backward, rope_table)
 from .norm import add_rms_norm, add_rms_norm_backward  # noqa: E402
+from .paging import PagePlan, cache_slots, free_pages, page_plan  # noqa: E402
 
-EXPORTED_SYMBOLS = EXPORTED_SYMBOLS + attention.EXPORTED_SYMBOLS + norm.EXPORTED_SYMBOLS
+EXPORTED_SYMBOLS = EXPORTED_SYMBOLS + attention.EXPORTED_SYMBOLS + norm.EXPORTED_SYMBOLS + paging.EXPORTED_SYMBOLS

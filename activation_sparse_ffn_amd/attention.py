@@ -336,11 +336,13 @@ class CacheBatch:
     without cu, and with cu as many as the call has (a call of few tokens for each
     of many sequences is faster if told so). A sequence's tokens beyond it are not
     stored, and their rows are NaN. max_kv: about the largest kv_lens (it splits
-    the work and never changes what is computed).
+    the work and never changes what is computed). slots: the new tokens' slots, int64 [T],
+    as page_plan and cache_slots give them (an append to a 4-bit cache then looks up none).
     """
 
     def __init__(self, block_table: torch.Tensor, kv_lens: torch.Tensor, max_kv: int,
-                 cu: Optional[torch.Tensor] = None, max_new: Optional[int] = None):
+                 cu: Optional[torch.Tensor] = None, max_new: Optional[int] = None,
+                 slots: Optional[torch.Tensor] = None):
         if block_table.dim() != 2 or not block_table.is_cuda:
             raise ValueError("block_table must be [B, max_pages] on the GPU")
         B, pages = block_table.shape
@@ -352,7 +354,7 @@ class CacheBatch:
                          None if cu is None else _address(cu, "cu", (B + 1,), torch.int32, dev),
                          B, pages, _int32(max_new), _int32(max_kv))
         self.block_table, self.kv_lens, self.cu, self.device = block_table, kv_lens, cu, dev
-        self.max_kv, self.max_new = max_kv, max_new
+        self.max_kv, self.max_new, self.slots = max_kv, max_new, slots
 
 
 def _same_device(cache: KVCache, batch: CacheBatch):

@@ -34,3 +34,20 @@ def test_norm_gradient_by_differences(weighted):
             d = np.zeros(5)
             d[i] = e
             assert np.isclose(g_w[i], (loss(h, w + d) - loss(h, w - d)) / (2 * e), rtol=1e-6, atol=1e-8)
+
+
+def test_plan_by_hand():
+    """Pages of 16. The first sequence gives its second page back and begins a new one, the
+    second ends, the third takes what came back first, and one page is lacking."""
+    table, free, n, lacking, lens, cu, pos, slots = lo.plan(
+        [[5, 7, -1], [2, 9, -1], [-1, -1, -1]], [30, 17, 0], [16, 0, 0], [1, 0, 65], [1, -1, -1, -1, -1, -1, -1, -1, -1, -1],
+        1, 16, 70)
+    # onto the stack: 7, 2, 9 above 1; off it: 9 for the first sequence, 2, 7, 1 for the third
+    assert table == [[5, 9, -1], [2, 9, -1], [2, 7, 1]] and n == 0 and lacking == 0
+    assert lens == [17, 0, 65] and cu == [0, 1, 1, 66]
+    assert pos[0] == 16 and slots[0] == 9 * 16 and pos[1:66] == list(range(65))
+    assert slots[1] == 32 and slots[17] == 7 * 16 and slots[33] == 16 and slots[48] == 31
+    assert slots[49:66] == [-1] * 17        # behind the table's three pages
+    assert slots[66:] == [-1] * 4 and pos[66:] == [0] * 4
+    short = lo.plan([[-1, -1]], [0], None, [20], [3, 0, 0, 0], 1, 16, 20)
+    assert short[0] == [[3, -1]] and short[3] == 1 and short[7] == [48 + i for i in range(16)] + [-1] * 4
