@@ -28,7 +28,7 @@ import torch
 __all__ = ["SparseFFN", "bank_topk", "library_path", "load_library", "SparseFFNError",
            "SFFN_OK", "SFFN_ERR_INVALID_ARG", "SFFN_ERR_UNSUPPORTED", "SFFN_ERR_WORKSPACE",
            "SFFN_ERR_HIP", "Config", "EXPORTED_SYMBOLS",
-           "rope_table", "qk_norm_rope", "qk_norm_rope_backward", "KVCache", "CacheBatch", "kv_cache_append",
+           "rope_table", "qk_norm_rope", "qk_norm_rope_backward", "KVCache", "KVCache4", "CacheBatch", "kv_cache_append",
            "kv_cache_read", "cache_attention", "add_rms_norm", "add_rms_norm_backward",
            "PagePlan", "free_pages", "page_plan", "cache_slots"]
 
@@ -350,7 +350,7 @@ class SparseFFN:
 
 
 from . import attention, norm, paging  # noqa: E402 (they use the helpers above)
-from .attention import (CacheBatch, KVCache, cache_attention, kv_cache_append, kv_cache_read,  # noqa: E402
+from .attention import (CacheBatch, KVCache, KVCache4, cache_attention, kv_cache_append, kv_cache_read,  # noqa: E402
                         qk_norm_rope, qk_norm_rope_backward, rope_table)
 from .norm import add_rms_norm, add_rms_norm_backward  # noqa: E402
 from .paging import PagePlan, cache_slots, free_pages, page_plan  # noqa: E402

@@ -1,10 +1,10 @@
 """The attention-side operators of a decoder layer that stand next to the sparse
 FFN: norms of q and k for each head with the rotary positions, a paged cache
-that holds keys and values in 8 bits, and attention over it.
+that holds keys and values in 8 bits or in 4, and attention over it.
 
     table = rope_table(32768, 128)
     q, k = qk_norm_rope(q, k, positions, table, q_weight=w_q, k_weight=w_k)
-    cache = KVCache.empty(n_pages, kv_heads, head_dim)
+    cache = KVCache.empty(n_pages, kv_heads, head_dim)      # or KVCache4.empty
     batch = CacheBatch(block_table, kv_lens, max_kv, cu, max_new)
     kv_cache_append(cache, batch, k, v)
     o = cache_attention(cache, batch, q)
@@ -23,8 +23,8 @@ import torch
 
 from . import SFFN_BF16, SFFN_F32, _check, _need_buffer, _ptr, _stream, load_library
 
-__all__ = ["rope_table", "qk_norm_rope", "qk_norm_rope_backward", "KVCache", "CacheBatch", "kv_cache_append",
-           "kv_cache_read", "cache_attention"]
+__all__ = ["rope_table", "qk_norm_rope", "qk_norm_rope_backward", "KVCache", "KVCache4", "CacheBatch",
+           "kv_cache_append", "kv_cache_read", "cache_attention"]
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = (None, "linear", "ntk", "by_parts")
@@ -49,6 +49,12 @@ class _Cache(ctypes.Structure):
                 ("page", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
+class _Cache4(ctypes.Structure):
+    _fields_ = [("keys", ctypes.c_void_p), ("values", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
 class _Batch(ctypes.Structure):
     _fields_ = [("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("kv_lens", ctypes.c_void_p),
                 ("cu", ctypes.c_void_p), ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32),
@@ -56,7 +62,8 @@ class _Batch(ctypes.Structure):
 
 
 EXPORTED_SYMBOLS = ("qk_norm_rope", "qk_norm_rope_backward", "qk_norm_rope_backward_workspace_size",
-                    "kv_cache_append", "kv_cache_read", "cache_attention", "cache_attention_workspace_size")
+                    "kv_cache_append", "kv_cache_read", "cache_attention", "cache_attention_workspace_size",
+                    "kv_cache4_append", "kv_cache4_read", "cache4_attention", "cache4_attention_workspace_size")
 
 
 def declare(lib):
@@ -77,6 +84,15 @@ def declare(lib):
     lib.cache_attention_workspace_size.restype = S
     lib.cache_attention.argtypes = [C, B, H, I32, st, I64, F, I32, H, P, P, S, P]
     lib.cache_attention.restype = st
+    C4 = ctypes.POINTER(_Cache4)
+    lib.kv_cache4_append.argtypes = [C4, B, P, H, H, st, I64, P]
+    lib.kv_cache4_append.restype = st
+    lib.kv_cache4_read.argtypes = [C4, B, H, H, st, I64, P]
+    lib.kv_cache4_read.restype = st
+    lib.cache4_attention_workspace_size.argtypes = [C4, B, I32, st, I32, I64]
+    lib.cache4_attention_workspace_size.restype = S
+    lib.cache4_attention.argtypes = [C4, B, H, I32, st, I64, F, I32, H, P, P, S, P]
+    lib.cache4_attention.restype = st
 
 
 # ---------------------------------------------------------------------------
@@ -292,7 +308,7 @@ def qk_norm_rope_backward(q: Optional[torch.Tensor], k: Optional[torch.Tensor], 
 
 
 # ---------------------------------------------------------------------------
-# the 8-bit cache
+# the caches
 # ---------------------------------------------------------------------------
 
 class KVCache:
@@ -326,6 +342,37 @@ class KVCache:
                    torch.empty((n_pages, kv_heads), **f32), torch.empty((n_pages, kv_heads), **f32))
 
 
+class KVCache4:
+    """A pool of pages of keys and values in 4-bit floating point (0, 0.5, 1, 1.5, 2, 3, 4, 6
+    and their negatives), two entries a byte, the even channel in the low half: keys, values
+    uint8 [pages, kv_heads, page, head_dim / 2]. Keys have a power of two for each 32 channels
+    of a token, k_exp uint8 [pages, kv_heads, page, head_dim / 32] (its exponent plus 127; 255
+    is NaN), values a scale for each token and head, v_scale fp32 [pages, kv_heads, page]. A
+    little more than half of KVCache's memory; an append changes no other token's entries. Sizes
+    and use as KVCache's."""
+
+    def __init__(self, keys: torch.Tensor, values: torch.Tensor, k_exp: torch.Tensor, v_scale: torch.Tensor):
+        if keys.dim() != 4 or not keys.is_cuda:
+            raise ValueError("keys must be [pages, kv_heads, page, head_dim / 2] on the GPU")
+        n, h, p, d = keys.shape
+        d *= 2
+        dev = keys.device
+        self._c = _Cache4(_address(keys, "keys", None, torch.uint8, dev),
+                          _address(values, "values", keys.shape, torch.uint8, dev),
+                          _address(k_exp, "k_exp", (n, h, p, d // 32), torch.uint8, dev),
+                          _address(v_scale, "v_scale", (n, h, p), torch.float32, dev), n, h, p, d)
+        self.keys, self.values, self.k_exp, self.v_scale = keys, values, k_exp, v_scale
+        self.device, self.kv_heads, self.page, self.head_dim = dev, h, p, d
+
+    @classmethod
+    def empty(cls, n_pages: int, kv_heads: int, head_dim: int, page: int = 64, device="cuda") -> "KVCache4":
+        """An unused cache (contents undefined until tokens are appended)."""
+        u8 = dict(dtype=torch.uint8, device=device)
+        rows = (n_pages, kv_heads, page)
+        return cls(torch.empty(rows + (head_dim // 2,), **u8), torch.empty(rows + (head_dim // 2,), **u8),
+                   torch.empty(rows + (head_dim // 32,), **u8), torch.empty(rows, dtype=torch.float32, device=device))
+
+
 class CacheBatch:
     """The sequences of a call and its new tokens. Sequence b holds kv_lens[b]
     tokens (the new ones included) in the pages block_table[b]; tokens cu[b] ..
@@ -357,16 +404,18 @@ class CacheBatch:
         self.max_kv, self.max_new, self.slots = max_kv, max_new, slots
 
 
-def _same_device(cache: KVCache, batch: CacheBatch):
+def _same_device(cache, batch: CacheBatch):
     if cache.device is not batch.device and cache.device != batch.device:
         raise ValueError(f"the cache is on {cache.device}, the batch on {batch.device}")
 
 
-def kv_cache_append(cache: KVCache, batch: CacheBatch, k: torch.Tensor, v: torch.Tensor) -> None:
+def kv_cache_append(cache, batch: CacheBatch, k: torch.Tensor, v: torch.Tensor) -> None:
     """Stores the keys and values k, v [T, kv_heads, head_dim] of the batch's
-    tokens, in place. A page and head whose new tokens exceed its scale gets a
+    tokens, in place. KVCache: a page and head whose new tokens exceed its scale gets a
     larger one and its held entries are rounded again; a NaN or an infinity
-    makes the scale of its page and head NaN."""
+    makes the scale of its page and head NaN. KVCache4: a token goes to its slot of
+    batch.slots, or, without them, of the batch's tables; a NaN or an infinity makes the
+    token's 32 channels (keys) or head (values) NaN."""
     lib = load_library()
     _same_device(cache, batch)
     dtype, dev = k.dtype, cache.device
@@ -376,10 +425,14 @@ def kv_cache_append(cache: KVCache, batch: CacheBatch, k: torch.Tensor, v: torch
     shape = (T, cache.kv_heads, cache.head_dim)
     hk = _heads(k, "k", shape, dtype, dev)
     hv = _heads(v, "v", shape, dtype, dev)
+    if type(cache) is KVCache4:
+        slots = None if batch.slots is None else _address(batch.slots, "slots", (T,), torch.int64, dev)
+        _check(lib, lib.kv_cache4_append(cache._c, batch._c, slots, hk, hv, _DTYPES[dtype], T, _stream(dev)))
+        return
     _check(lib, lib.kv_cache_append(cache._c, batch._c, hk, hv, _DTYPES[dtype], T, _stream(dev)))
 
 
-def kv_cache_read(cache: KVCache, batch: CacheBatch, total: int, dtype: torch.dtype = torch.bfloat16,
+def kv_cache_read(cache, batch: CacheBatch, total: int, dtype: torch.dtype = torch.bfloat16,
                   k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None):
     """The batch's `total` tokens out of the cache: (k, v), each [total,
     kv_heads, head_dim], as the values the entries stand for. Rows of tokens in no
@@ -398,11 +451,12 @@ def kv_cache_read(cache: KVCache, batch: CacheBatch, total: int, dtype: torch.dt
         v, hv = _new(shape, dtype, dev)
     else:
         hv = _heads(v, "v", shape, dtype, dev)
-    _check(lib, lib.kv_cache_read(cache._c, batch._c, hk, hv, _DTYPES[dtype], total, _stream(dev)))
+    read = lib.kv_cache4_read if type(cache) is KVCache4 else lib.kv_cache_read
+    _check(lib, read(cache._c, batch._c, hk, hv, _DTYPES[dtype], total, _stream(dev)))
     return k, v
 
 
-def cache_attention(cache: KVCache, batch: CacheBatch, q: torch.Tensor, scale: Optional[float] = None,
+def cache_attention(cache, batch: CacheBatch, q: torch.Tensor, scale: Optional[float] = None,
                     window: int = 0, out: Optional[torch.Tensor] = None, return_lse: bool = False,
                     workspace: Optional[torch.Tensor] = None):
     """Causal attention of the batch's tokens q [T, heads, head_dim] over the
@@ -413,7 +467,9 @@ def cache_attention(cache: KVCache, batch: CacheBatch, q: torch.Tensor, scale: O
     no key gives zeros and -inf; rows of tokens in no sequence are left as out
     holds them (undefined where it is not given). The softmax weights of a bf16 q are kept to 16
     bits, or to 8 in a sequence whose new tokens times heads / kv_heads are more
-    than 128; those of an fp32 q to fp32."""
+    than 128; those of an fp32 q to fp32. (KVCache4: q and weights as sums of 6-bit pieces, to
+    2^-13 of the largest of 32 channels or keys, weights to 2^-8 where the 8-bit cache's have 8 bits,
+    both to 2^-21 for an fp32 q.)"""
     lib = load_library()
     _same_device(cache, batch)
     dev = cache.device
@@ -429,12 +485,15 @@ def cache_attention(cache: KVCache, batch: CacheBatch, q: torch.Tensor, scale: O
     lse = _empty_strided((T, heads), (heads, 1), dtype=torch.float32, device=dev) if return_lse else None
     dt = _DTYPES[dtype]
     window = _int32(window)
+    four = type(cache) is KVCache4
     if workspace is None:
-        need = lib.cache_attention_workspace_size(cache._c, batch._c, heads, dt, window, T)
+        size = lib.cache4_attention_workspace_size if four else lib.cache_attention_workspace_size
+        need = size(cache._c, batch._c, heads, dt, window, T)
         workspace = _vector(need, torch.uint8, dev) if need else None
     else:
         _need_buffer(workspace, "workspace", None, torch.uint8, dev)
         need = workspace.numel()
-    _check(lib, lib.cache_attention(cache._c, batch._c, hq, heads, dt, T, D ** -0.5 if scale is None else scale,
-                                    window, ho, _ptr(lse), _ptr(workspace), need, _stream(dev)))
+    attend = lib.cache4_attention if four else lib.cache_attention
+    _check(lib, attend(cache._c, batch._c, hq, heads, dt, T, D ** -0.5 if scale is None else scale, window, ho,
+                       _ptr(lse), _ptr(workspace), need, _stream(dev)))
     return (out, lse) if return_lse else out

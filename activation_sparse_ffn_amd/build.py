@@ -18,8 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsparse_ffn.so")
 SOURCES = ["topk.hip", "gather.hip", "gemm.hip", "skinny.hip", "backward.hip", "rope.hip", "kvcache.hip",
-           "cache_attention.hip", "norm.hip", "paging.hip", "capi.cpp", "attn_capi.cpp", "norm_capi.cpp",
-           "paging_capi.cpp"]
+           "cache_attention.hip", "kvcache4.hip", "cache4_attention.hip", "norm.hip", "paging.hip", "capi.cpp",
+           "attn_capi.cpp", "attn4_capi.cpp", "norm_capi.cpp", "paging_capi.cpp"]
 ARCH = os.environ.get("SFFN_OFFLOAD_ARCH", "gfx950")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

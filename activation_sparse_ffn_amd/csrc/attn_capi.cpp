@@ -4,68 +4,11 @@
 
 #include <cmath>
 
-#include "../../include/sparse_ffn_attention.h"
-#include "attn_launch.hpp"
-#include "status.hpp"
+#include "attn_checks.hpp"
 
 namespace {
 
-using sffn::aligned16;
-using sffn::as_int;
-using sffn::fail;
-using sffn::hip_status;
-
-// Bounds that keep every size product below 2^63 and every grid below 2^31.
-constexpr int64_t kMaxTokens = (int64_t)1 << 30;
-// Of the cache: new tokens of a call and tokens of a sequence, so that every
-// position, with a call's tokens added, fits 31 bits.
-constexpr int64_t kMaxNewTokens = (int64_t)1 << 28;
-constexpr int64_t kMaxCapacity = (int64_t)1 << 30;
-constexpr int64_t kMaxStride = (int64_t)1 << 42;
-constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
-constexpr int32_t kMaxHeads = 65536;
-
-size_t elem_size(int dtype) { return dtype == SFFN_BF16 ? 2 : 4; }
-
-sffn_status_t check_dtype(int dtype) {
-    if (dtype != SFFN_F32 && dtype != SFFN_BF16) return fail(SFFN_ERR_INVALID_ARG, "unknown dtype %d", dtype);
-    return SFFN_OK;
-}
-
-// A [T, heads, dim] view. wide: rows must be 16-byte aligned. out: elements
-// must not overlap (tokens outside heads or heads outside tokens).
-sffn_status_t check_heads(const sffn_heads_t* v, const char* name, int64_t T, int64_t heads, int64_t dim, int dtype,
-                          bool wide, bool out) {
-    if (!v || !v->data) return fail(SFFN_ERR_INVALID_ARG, "%s is null", name);
-    if (v->stride_token < 0 || v->stride_head < 0 || v->stride_token > kMaxStride || v->stride_head > kMaxStride)
-        return fail(SFFN_ERR_INVALID_ARG, "%s has strides out of range (%lld, %lld)", name,
-                    (long long)v->stride_token, (long long)v->stride_head);
-    int64_t a, b, last;
-    if (__builtin_mul_overflow(T - 1, v->stride_token, &a) || __builtin_mul_overflow(heads - 1, v->stride_head, &b) ||
-        __builtin_add_overflow(a, b, &last) || last > ((int64_t)1 << 60))
-        return fail(SFFN_ERR_INVALID_ARG, "%s is too large", name);
-    const size_t e = elem_size(dtype);
-    if (reinterpret_cast<uintptr_t>(v->data) % e != 0)
-        return fail(SFFN_ERR_INVALID_ARG, "%s is not aligned to its elements", name);
-    if (wide && (!aligned16(v->data) || (size_t)v->stride_token * e % 16 != 0 || (size_t)v->stride_head * e % 16 != 0))
-        return fail(SFFN_ERR_INVALID_ARG, "%s must have 16-byte aligned rows", name);
-    if (out) {
-        const bool heads_inside = (heads == 1 || v->stride_head >= dim) && (T == 1 || v->stride_token >= b + dim);
-        const bool tokens_inside = (T == 1 || v->stride_token >= dim) && (heads == 1 || v->stride_head >= a + dim);
-        if (!heads_inside && !tokens_inside) return fail(SFFN_ERR_INVALID_ARG, "%s overlaps itself", name);
-    }
-    return SFFN_OK;
-}
-
-sffn::Heads view(const sffn_heads_t* v) {
-    return v ? sffn::Heads{v->data, v->stride_token, v->stride_head} : sffn::Heads{nullptr, 0, 0};
-}
-
-#define SFFN_TRY(call)                            \
-    do {                                          \
-        const sffn_status_t try_st = (call);      \
-        if (try_st != SFFN_OK) return try_st;     \
-    } while (0)
+using namespace sffn;
 
 // ---- head norms and rotary positions -------------------------------------------
 
@@ -127,70 +70,16 @@ sffn::RopeArgs rope_args(const sffn_rope_config_t* c, const int32_t* positions, 
 
 // ---- cache ---------------------------------------------------------------------------
 
-sffn_status_t check_cache(const sffn_kv_cache_t* c, const sffn_kv_batch_t* b, int64_t T) {
-    if (!c || !b) return fail(SFFN_ERR_INVALID_ARG, "cache and batch must not be null");
-    if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128)
-        return fail(SFFN_ERR_UNSUPPORTED, "page must be 16, 32, 64 or 128 (got %d)", c->page);
-    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
-        return fail(SFFN_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256 (got %d)", c->head_dim);
-    if (c->kv_heads < 1 || c->kv_heads > kMaxHeads)
-        return fail(SFFN_ERR_INVALID_ARG, "kv_heads must be positive (got %d)", c->kv_heads);
-    if (c->n_pages < 1 || c->n_pages > INT32_MAX)
-        return fail(SFFN_ERR_INVALID_ARG, "n_pages must lie in [1, 2^31) (got %lld)", (long long)c->n_pages);
-    if (b->n_seqs < 0 || b->max_pages < 0 || b->max_new < 0 || b->max_kv < 0)
-        return fail(SFFN_ERR_INVALID_ARG, "n_seqs, max_pages, max_new and max_kv must not be negative");
-    if (b->table_stride < 0 || b->table_stride > kMaxStride || (b->n_seqs > 1 && b->table_stride < b->max_pages))
-        return fail(SFFN_ERR_INVALID_ARG, "table_stride %lld does not fit rows of %d pages",
-                    (long long)b->table_stride, b->max_pages);
-    if (T < 0) return fail(SFFN_ERR_INVALID_ARG, "T must be >= 0 (got %lld)", (long long)T);
-    if (T > kMaxNewTokens) return fail(SFFN_ERR_UNSUPPORTED, "T = %lld is too large for one call", (long long)T);
-    if ((int64_t)b->max_pages * c->page > kMaxCapacity)
-        return fail(SFFN_ERR_UNSUPPORTED, "max_pages %d of %d tokens are too many", b->max_pages, c->page);
-    if (!b->cu && T != b->n_seqs)
-        return fail(SFFN_ERR_INVALID_ARG, "without cu, T must be n_seqs (got %lld, %d)", (long long)T, b->n_seqs);
-    if (!b->cu && T > 0 && b->max_new < 1)
-        return fail(SFFN_ERR_INVALID_ARG, "max_new must be positive (got %d)", b->max_new);
-    return SFFN_OK;
+CacheBuffers buffers(const sffn_kv_cache_t* c) {
+    return {{c->keys, c->values, c->k_scale, c->v_scale}, {"keys", "values", "k_scale", "v_scale"}};
 }
 
-sffn_status_t check_cache_pointers(const sffn_kv_cache_t* c, const sffn_kv_batch_t* b) {
-    const void* ptrs[] = {c->keys, c->values, c->k_scale, c->v_scale};
-    const char* names[] = {"keys", "values", "k_scale", "v_scale"};
-    for (int i = 0; i < 4; ++i) {
-        if (!ptrs[i]) return fail(SFFN_ERR_INVALID_ARG, "%s is null", names[i]);
-        if (!aligned16(ptrs[i])) return fail(SFFN_ERR_INVALID_ARG, "%s is not 16-byte aligned", names[i]);
-    }
-    if (b->max_pages < 1) return fail(SFFN_ERR_INVALID_ARG, "max_pages must be positive (got %d)", b->max_pages);
-    if (!b->kv_lens || !b->block_table)
-        return fail(SFFN_ERR_INVALID_ARG, "block_table and kv_lens must not be null");
-    for (const void* p : {(const void*)b->block_table, (const void*)b->kv_lens, (const void*)b->cu})
-        if (reinterpret_cast<uintptr_t>(p) % 4 != 0)
-            return fail(SFFN_ERR_INVALID_ARG, "block_table, kv_lens and cu must be 4-byte aligned");
-    return SFFN_OK;
-}
-
-sffn::CacheArgs cache_args(const sffn_kv_cache_t* c, const sffn_kv_batch_t* b, int dtype, int64_t T) {
-    sffn::CacheArgs a{};
+CacheArgs cache_args(const sffn_kv_cache_t* c, const sffn_kv_batch_t* b, int dtype, int64_t T) {
+    CacheArgs a = cache_shape(c, b, dtype, T);
     a.keys = c->keys;
     a.values = c->values;
     a.k_scale = c->k_scale;
     a.v_scale = c->v_scale;
-    a.n_pages = c->n_pages;
-    a.Hkv = c->kv_heads;
-    a.P = c->page;
-    a.D = c->head_dim;
-    a.shift = __builtin_ctz((unsigned)c->page);
-    a.table = b->block_table;
-    a.table_stride = b->table_stride;
-    a.lens = b->kv_lens;
-    a.cu = b->cu;
-    a.B = b->n_seqs;
-    a.max_pages = b->max_pages;
-    // no sequence has more new tokens than the call, and without offsets each has one
-    a.max_new = !b->cu ? 1 : (int)(b->max_new < T ? b->max_new : T);
-    a.max_kv = b->max_kv;
-    a.T = T;
-    a.dt = dtype == SFFN_BF16 ? sffn::Dt::BF16 : sffn::Dt::F32;
     return a;
 }
 
@@ -203,39 +92,13 @@ sffn_status_t cache_copy(const sffn_kv_cache_t* cache, const sffn_kv_batch_t* ba
     SFFN_TRY(check_dtype(dt));
     SFFN_TRY(check_cache(cache, batch, T));
     if (T == 0 || batch->n_seqs == 0 || batch->max_new == 0) return SFFN_OK;
-    SFFN_TRY(check_cache_pointers(cache, batch));
+    SFFN_TRY(check_cache_pointers(buffers(cache), batch));
     SFFN_TRY(check_heads(k, "k", T, cache->kv_heads, cache->head_dim, dt, true, out));
     SFFN_TRY(check_heads(v, "v", T, cache->kv_heads, cache->head_dim, dt, true, out));
     const sffn::CacheArgs a = cache_args(cache, batch, dt, T);
     if (sffn::cache_copy_blocks(a) > kMaxGrid)
         return fail(SFFN_ERR_UNSUPPORTED, "T = %lld is too large for one call", (long long)T);
     return hip_status(launch(a, view(k), view(v), static_cast<hipStream_t>(hip_stream)), what);
-}
-
-// The checks of cache_attention that its workspace size needs too.
-sffn_status_t check_attention(const sffn_kv_cache_t* cache, const sffn_kv_batch_t* batch, int32_t n_q_heads,
-                              int32_t window, int64_t T) {
-    SFFN_TRY(check_cache(cache, batch, T));
-    if (n_q_heads < 1 || n_q_heads > kMaxHeads || n_q_heads % cache->kv_heads != 0)
-        return fail(SFFN_ERR_INVALID_ARG, "n_q_heads must be a multiple of kv_heads (got %d, %d)", n_q_heads,
-                    cache->kv_heads);
-    if (window < 0) return fail(SFFN_ERR_INVALID_ARG, "window must be >= 0 (got %d)", window);
-    if (T * n_q_heads > kMaxGrid)
-        return fail(SFFN_ERR_UNSUPPORTED, "T = %lld is too large for one call", (long long)T);
-    return SFFN_OK;
-}
-
-sffn_status_t make_plan(const sffn::CacheArgs& a, int32_t n_q_heads, int32_t window, sffn::AttnPlan* plan) {
-    const int64_t tiles = ((int64_t)a.max_new * (n_q_heads / a.Hkv) + 15) / 16;
-    if (tiles > kMaxGrid || (int64_t)a.B * a.Hkv > kMaxGrid / (tiles > 0 ? tiles : 1))
-        return fail(SFFN_ERR_UNSUPPORTED, "the batch is too large for one call");
-    // the kernels' counts of steps of 64 keys over all sequences and heads
-    const int64_t steps = (int64_t)a.max_pages * a.P / 64 + 8;
-    if ((int64_t)a.B * a.Hkv > kMaxGrid / steps)
-        return fail(SFFN_ERR_UNSUPPORTED, "%d sequences of %d pages are too many for one call", a.B, a.max_pages);
-    *plan = sffn::attn_plan(a, n_q_heads, window);
-    if (plan->blocks > kMaxGrid) return fail(SFFN_ERR_UNSUPPORTED, "the batch is too large for one call");
-    return SFFN_OK;
 }
 
 }  // namespace
@@ -331,7 +194,7 @@ size_t cache_attention_workspace_size(const sffn_kv_cache_t* cache, const sffn_k
     if (check_dtype(as_int(dtype)) != SFFN_OK || check_attention(cache, batch, n_q_heads, window, T) != SFFN_OK) return 0;
     if (T == 0 || batch->n_seqs == 0 || batch->max_new == 0) return 0;
     sffn::AttnPlan plan;
-    if (make_plan(cache_args(cache, batch, as_int(dtype), T), n_q_heads, window, &plan) != SFFN_OK) return 0;
+    if (make_plan(cache_args(cache, batch, as_int(dtype), T), n_q_heads, window, sffn::attn_plan, &plan) != SFFN_OK) return 0;
     return plan.ws_bytes;
 }
 
@@ -344,20 +207,14 @@ sffn_status_t cache_attention(const sffn_kv_cache_t* cache, const sffn_kv_batch_
     SFFN_TRY(check_attention(cache, batch, n_q_heads, window, T));
     if (!std::isfinite(scale)) return fail(SFFN_ERR_INVALID_ARG, "scale must be finite (got %g)", (double)scale);
     if (T == 0 || batch->n_seqs == 0 || batch->max_new == 0) return SFFN_OK;
-    SFFN_TRY(check_cache_pointers(cache, batch));
+    SFFN_TRY(check_cache_pointers(buffers(cache), batch));
     SFFN_TRY(check_heads(q, "q", T, n_q_heads, cache->head_dim, dt, true, false));
     SFFN_TRY(check_heads(out, "out", T, n_q_heads, cache->head_dim, dt, true, true));
     if (reinterpret_cast<uintptr_t>(lse) % 4 != 0) return fail(SFFN_ERR_INVALID_ARG, "lse must be 4-byte aligned");
     const sffn::CacheArgs a = cache_args(cache, batch, dt, T);
     sffn::AttnPlan plan;
-    SFFN_TRY(make_plan(a, n_q_heads, window, &plan));
-    if (plan.ws_bytes > 0) {
-        if (!workspace) return fail(SFFN_ERR_INVALID_ARG, "workspace is null");
-        if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
-            return fail(SFFN_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
-        if (ws_bytes < plan.ws_bytes)
-            return fail(SFFN_ERR_WORKSPACE, "workspace holds %zu bytes, %zu needed", ws_bytes, plan.ws_bytes);
-    }
+    SFFN_TRY(make_plan(a, n_q_heads, window, sffn::attn_plan, &plan));
+    SFFN_TRY(sffn::check_workspace(workspace, ws_bytes, plan.ws_bytes));
     return hip_status(sffn::launch_cache_attention(a, plan, view(q), n_q_heads, scale, window, view(out), lse,
                                                    workspace, static_cast<hipStream_t>(hip_stream)),
                       "cache_attention");

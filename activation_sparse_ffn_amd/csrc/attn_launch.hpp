@@ -127,15 +127,10 @@ constexpr int64_t kSharedRows = 32768;
 // since the shares are then longer than a sequence.
 constexpr int64_t kPartBytes = (int64_t)256 << 20;
 
-inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
-    AttnPlan p{};
+// The rest of a plan whose kernels are chosen (few, pair, waves, pieces); the chip holds
+// `held` of their workgroups a compute unit.
+inline AttnPlan cut_up(const CacheArgs& c, int Hq, int window, AttnPlan p, int64_t held) {
     const int64_t G = Hq / c.Hkv, most = (int64_t)c.max_new * G;
-    p.few = most <= 16;
-    // two tiles of 16 rows: 5 tokens of 4 heads over 32768 keys 24.6 us, by a row tile
-    // of 128 33 (heads of 256 have no registers for it)
-    p.pair = !p.few && most <= 32 && c.D <= 128;
-    p.waves = c.D > 128 || c.dt == Dt::F32 || most <= 128 ? 4 : 8;
-    p.pieces = most <= kPreciseRows ? 2 : 1;
     p.rows = p.few ? 16 : p.pair ? 32 : 32 * p.waves;
     p.row_tiles = (most + p.rows - 1) / p.rows;
     // keys that one row tile sees: all, or the window of its tokens
@@ -150,10 +145,7 @@ inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
     const int64_t steps = (span + 63) / 64, all_steps = ((int64_t)c.max_pages * c.P + c.max_new) / 64 + 16;
     p.shared = p.few || p.pair || (rows <= kSharedRows && whole <= ((int64_t)1 << 31) / all_steps);
     if (p.shared) {
-        // no share is less than 8 steps of 64 keys (see share_work); the chip holds one
-        // workgroup a compute unit of the largest kinds, else two
-        const int64_t held = p.few || p.pair ? few_held(c.D, c.dt == Dt::F32)
-                                             : c.D > 128 || c.dt == Dt::F32 || p.waves == 8 ? 1 : 2;
+        // no share is less than 8 steps of 64 keys (see share_work)
         p.chunk = 8 * 64;
         p.splits = steps <= 8 ? 1 : (int)(steps / 8 + 2);
         if (p.splits > room) p.splits = room < 2 ? 1 : (int)room;
@@ -174,7 +166,42 @@ inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
     return p;
 }
 
+inline AttnPlan attn_plan(const CacheArgs& c, int Hq, int window) {
+    AttnPlan p{};
+    const int64_t most = (int64_t)c.max_new * (Hq / c.Hkv);
+    p.few = most <= 16;
+    // two tiles of 16 rows: 5 tokens of 4 heads over 32768 keys 24.6 us, by a row tile
+    // of 128 33 (heads of 256 have no registers for it)
+    p.pair = !p.few && most <= 32 && c.D <= 128;
+    p.waves = c.D > 128 || c.dt == Dt::F32 || most <= 128 ? 4 : 8;
+    p.pieces = most <= kPreciseRows ? 2 : 1;
+    // one workgroup a compute unit of the largest kinds, else two
+    return cut_up(c, Hq, window, p, p.few || p.pair ? few_held(c.D, c.dt == Dt::F32)
+                                                    : c.D > 128 || c.dt == Dt::F32 || p.waves == 8 ? 1 : 2);
+}
+
 hipError_t launch_cache_attention(const CacheArgs& c, const AttnPlan& plan, const Heads& q, int Hq, float scale,
                                   int window, const Heads& out, float* lse, void* ws, hipStream_t s);
+
+// ---- 4-bit cache ----------------------------------------------------------------
+// Its buffers; the rest of a call is in CacheArgs, whose own buffers are not used.
+struct Cache4 {
+    uint8_t *keys, *values;         // [n_pages, Hkv, P, D / 2]
+    uint8_t* k_exp;                 // [n_pages, Hkv, P, D / 32]
+    float* v_scale;                 // [n_pages, Hkv, P]
+};
+// slots: [T] or null (then the tokens' places come from the tables)
+hipError_t launch_cache4_append(const CacheArgs& c, const Cache4& b, const int64_t* slots, const Heads& k,
+                                const Heads& v, hipStream_t s);
+hipError_t launch_cache4_read(const CacheArgs& c, const Cache4& b, const Heads& k, const Heads& v, hipStream_t s);
+
+inline AttnPlan attn4_plan(const CacheArgs& c, int Hq, int window) {
+    AttnPlan p{};
+    p.few = (int64_t)c.max_new * (Hq / c.Hkv) <= 16;
+    p.waves = 4;
+    return cut_up(c, Hq, window, p, few_held(c.D, c.dt == Dt::F32));
+}
+hipError_t launch_cache4_attention(const CacheArgs& c, const Cache4& b, const AttnPlan& plan, const Heads& q, int Hq,
+                                   float scale, int window, const Heads& out, float* lse, void* ws, hipStream_t s);
 
 }  // namespace sffn

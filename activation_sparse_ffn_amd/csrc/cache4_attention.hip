@@ -1,0 +1,730 @@
+// Attention of new tokens over the paged 4-bit cache.
+//
+//   s_j = scale q . k_j,  o = sum_j p_j v_j / sum_j p_j,  p_j = exp(s_j - max),
+//   k_j = entries times 2^e of each 32 channels,  v_j = entries times a scale sv_j
+//
+// One pass over the keys with the running maximum m and sum l of the softmax, S^T = K Q^T
+// and O^T = V^T P^T as over the 8-bit cache, so that weights stay in the lanes that
+// computed them. Entries are operands of the matrix cores as they lie:
+// v_mfma_scale_f32_*_f8f6f4 multiplies 4-bit rows by 6-bit columns (1 sign, 2 exponent, 3
+// mantissa bits: 0.125 .. 7.5) with a power of two for each 32 elements of either, which is
+// what the keys' exponents are.
+//
+// q (times scale log2 e) and the weights p sv are sums of such 6-bit pieces: the block's
+// largest magnitude goes to (3.75, 7.5] units, and each piece takes what the pieces before
+// left, at 1 / 16 of their unit. The first leaves a quarter of a unit at most (rounding
+// among steps of 1 / 2), the second 2^-7 (a quarter is 4 of its units, below which steps
+// are 1 / 4), the third 2^-12 (2 of its units, steps of 1 / 8), each more 2^-4 of that:
+// two pieces are exact to 2^-8.9 of the block's largest, three to 2^-13.9, five to
+// 2^-21.9. q's blocks are 32 channels of a row, the weights' the 32 keys of a row that a
+// lane holds. q of bf16 has three
+// pieces, of fp32 five; weights two in sequences of more than kPreciseRows rows, three in
+// those of fewer, five for fp32. The sum l takes the weights before they are cut.
+#include <type_traits>
+#include <utility>
+
+#include "attn_work.hpp"
+
+namespace sffn {
+
+namespace {
+
+struct Attn4Args {
+    AttnArgs a;
+    Cache4 b;
+};
+
+typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x32 __attribute__((ext_vector_type(32)));
+
+template <typename F, int... I>
+__device__ __forceinline__ void each(F f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+// f(0) .. f(N - 1), constants
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) {
+    each(f, std::make_integer_sequence<int, N>{});
+}
+
+// ---- 6-bit pieces ---------------------------------------------------------------
+
+// Exponent (plus 127) of the unit of a block whose largest magnitude has the bits `top`:
+// that lies in (3.75, 7.5] units. 255, which is NaN to the matrix cores, where it is not
+// finite. The last of NP pieces' units is still a normal number.
+template <int NP>
+__device__ __forceinline__ int unit_of(uint32_t top) {
+    const int e = (int)(top >> 23) - 2 + ((top & 0x7fffffu) > 0x700000u);
+    return top >= 0x7f800000u ? 255 : max(e, 4 * NP - 3);
+}
+// The units of pieces 4 i .. 4 i + 3, a byte each.
+__device__ __forceinline__ int units(int e, int i) {
+    return e == 255 ? -1 : (int)((uint32_t)(e - 16 * i) * 0x01010101u - 0x0c080400u);
+}
+
+// 32 numbers as NP pieces of unit 2^(e - 127), 2^(e - 131) ..: element 2 j is lo[j], 2 j + 1
+// hi[j]. The conversions write their result while they still read their operands: the empty
+// asm keeps those, the unit among them, in other registers. (With the result over an operand
+// the pieces were wrong.)
+template <int NP>
+__device__ __forceinline__ void split(f32x16 lo, f32x16 hi, int e, u32x6* out) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        const float unit = __uint_as_float((uint32_t)(e - 4 * p) << 23);
+        u32x6 r = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(lo, hi, unit);
+        asm("" : "+v"(r) : "v"(lo), "v"(hi), "v"(unit));
+        out[p] = r;
+        if (p + 1 < NP) {
+            f32x32 back = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(r, unit);
+            asm("" : "+v"(back) : "v"(r), "v"(unit));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                lo[i] -= back[2 * i];
+                hi[i] -= back[2 * i + 1];
+            }
+        }
+    }
+}
+
+// 32 consecutive channels of a row of q times `by`, as NP pieces, and their unit's exponent.
+template <typename E, int NP>
+__device__ __forceinline__ int split_q(const E* p, bool valid, float by, u32x6* out) {
+    float x[32];
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[i + j] = 0.f;
+        if (valid) Elem<E>::load8(p + i, x + i);
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        x[i] *= by;
+        top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    }
+    const int e = unit_of<NP>(top);
+    f32x16 lo, hi;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        lo[i] = x[2 * i];
+        hi[i] = x[2 * i + 1];
+    }
+    split<NP>(lo, hi, e, out);
+    return e;
+}
+
+// ---- products -------------------------------------------------------------------
+
+__device__ __forceinline__ i32x8 operand(const u32x6& v) {
+    return (i32x8)__builtin_shufflevector(v, v, 0, 1, 2, 3, 4, 5, -1, -1);
+}
+__device__ __forceinline__ i32x8 operand(const uint4& v) {
+    return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+}
+
+// c + entries a (4 bits, unit: byte UA of ua) times pieces b (6 bits, byte UB of ub).
+template <int UA, int UB>
+__device__ __forceinline__ f32x4 product(const uint4& a, int ua, const u32x6& b, int ub, f32x4 c) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(a), operand(b), c, 4, 2, UA, ua, UB, ub);
+}
+template <int UA, int UB>
+__device__ __forceinline__ f32x16 product(const uint4& a, int ua, const u32x6& b, int ub, f32x16 c) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(a), operand(b), c, 4, 2, UA, ua, UB, ub);
+}
+constexpr int kOne = 0x7f7f7f7f;        // unit 1
+
+// 16 channels' entries of 16 tokens, a channel a lane: lane i of each 16 names the token
+// that is to be element i.
+__device__ __forceinline__ i32x2 transposed(const char* p) {
+    return __builtin_amdgcn_ds_read_tr4_b64_v2i32((__attribute__((address_space(3))) i32x2*)p);
+}
+__device__ __forceinline__ uint4 joined(i32x2 a, i32x2 b) { return make_uint4(a[0], a[1], b[0], b[1]); }
+
+// ---- softmax of a lane's 32 scores -------------------------------------------------
+
+// State of a row: the reference m (-inf before its first key), the lane's share of the sum.
+// Scores come relative to the reference (0 while there is none). `top` is the largest of
+// the row's in the step, over all its lanes. Moves the reference where scores pass it by
+// more than kSlack or there is none yet; `scale_output(factor)` follows.
+template <typename F>
+__device__ __forceinline__ void follow(float top, float& m, float& l, float (&x)[32], F scale_output) {
+    const bool unset = m == neg_inf();
+    if (__any(unset ? top > neg_inf() : top > kSlack)) {
+        const float by = unset ? (top > neg_inf() ? top : 0.f) : fmaxf(top, 0.f);
+        const float alpha = unset ? 1.f : __builtin_amdgcn_exp2f(-by);
+        if (unset) m = top > neg_inf() ? top : m;
+        else m += by;
+        l *= alpha;
+        scale_output(alpha);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] -= by;
+    }
+}
+__device__ __forceinline__ float reference(float m) { return m == neg_inf() ? 0.f : m; }
+
+// Weights of scores x and the pieces of weights times value scales sv(i); hidden(i) where
+// `masked`. Returns the pieces' unit.
+template <int PP, typename SV, typename H>
+__device__ __forceinline__ int weights(const float (&x)[32], float& l, SV sv, bool masked, H hidden, u32x6* out) {
+    f32x16 lo, hi;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const float p = __builtin_amdgcn_exp2f(x[i]);
+        sum += p;
+        if (i < 16) lo[i] = p * sv(i);
+        else hi[i - 16] = p * sv(i);
+    }
+    l += sum;
+    if (masked) {
+        // what is stored behind a hidden key may be anything
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (hidden(i)) {
+                if (i < 16) lo[i] = 0.f;
+                else hi[i - 16] = 0.f;
+            }
+    }
+    // not negative: compared as integers, in which infinities and NaN come out on top
+    int top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(max(top, __float_as_int(lo[i])), __float_as_int(hi[i]));
+    const int e = unit_of<PP>((uint32_t)top);
+    split<PP>(lo, hi, e, out);
+    return e;
+}
+
+__device__ __forceinline__ uint64_t page_row(const CacheArgs& c, uint32_t page, int h) {
+    return ((uint64_t)page * c.Hkv + h) << c.shift;
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (up to 16 a sequence and key head): four waves take the work's steps of 128
+// keys in turn, each with its own running softmax; they meet in LDS at the end.
+//
+// v_mfma_scale_f32_16x16x128_f8f6f4: lane l holds operand row (A) or column (B) l % 16,
+// k = 32 (l / 16) .. + 31, and of the result column l % 16, rows 4 (l / 16) .. + 3. With
+// g = l / 16, n = l % 16:
+//   S^T of 16 keys: lane l loads the 32 channels 32 g .. of key n, 16 bytes. Heads of 256
+//     take two products; heads of 64 fill k = 64 .. 127 with the same keys again and the
+//     next piece of q.
+//   O^T of 128 keys: the lane has the weights of keys 16 t + 4 g + i (t < 8, i < 4) of row
+//     n; element 2 (4 t + i) is that of t < 4, 2 (4 t + i) + 1 that of t + 4. A value row is
+//     put into LDS at the place 32 g + element, from which 16 of them are read transposed.
+// ---------------------------------------------------------------------------
+constexpr int kStep = 128;
+
+template <int D>
+struct FewLds {
+    static constexpr int pitch = D / 2 + 16;        // rows read together start in other banks
+    char values[kStep * pitch];
+    float v_scale[kStep];
+    uint8_t k_exp[kStep * (D / 32)];
+};
+
+template <typename E, int NP, int PP, int D>
+__device__ __forceinline__ void attend4_few(const Attn4Args& args, const Work& w, int parts, FewLds<D>& lds,
+                                            float (*sm)[16], float (*sl)[16], float (*so)[16][D + 4]) {
+    const AttnArgs& a = args.a;
+    const CacheArgs& c = a.c;
+    const Cache4& cache = args.b;
+    constexpr int RB = D / 2;                       // bytes of a row
+    constexpr int KC = D > 128 ? 2 : 1;             // products of 128 channels
+    constexpr int NM = D == 64 ? (NP + 1) / 2 : NP; // products for q's pieces
+    constexpr int DT = D / 16;
+    constexpr int VL = D / 16;                      // loads of 16 bytes a lane of a step's values
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int g = lane >> 4, n = lane & 15;
+
+    const int32_t* table = c.table + (int64_t)w.b * c.table_stride;
+    // entries of the pages of keys lane and 64 + lane of the step
+    auto load_entries = [&](int t0, uint32_t (&e)[2]) {
+        e[0] = page_entry(c, table, t0 + lane);
+        e[1] = page_entry(c, table, t0 + 64 + lane);
+    };
+    // first row of tile t (16 keys) in the cache's arrays
+    auto tile_row = [&](const uint32_t (&e)[2], int t0, int t) {
+        const uint32_t page = page_in(c, (uint32_t)lane_value((int)e[t >> 2], 16 * (t & 3)));
+        return page_row(c, page, w.h) + ((t0 + 16 * t) & (c.P - 1));
+    };
+    const int k_off = n * RB + 16 * (D == 64 ? g & 1 : g);
+    uint4 kr[8][KC];
+    uint2 ke[2];
+    float vs[2];
+    auto load_keys = [&](const uint32_t (&e)[2], int t0) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            if (t0 + 16 * t < w.k1) {
+                const uint8_t* p = cache.keys + tile_row(e, t0, t) * RB;
+#pragma unroll
+                for (int cc = 0; cc < KC; ++cc) kr[t][cc] = *reinterpret_cast<const uint4*>(p + k_off + 64 * cc);
+            }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int key = t0 + 64 * i + lane;
+            ke[i] = make_uint2(~0u, ~0u);
+            vs[i] = __builtin_nanf("");
+            if (key < w.k1 && known_page(c, e[i], key)) {
+                const uint64_t row = page_row(c, e[i], w.h) + (key & (c.P - 1));
+                const uint8_t* p = cache.k_exp + row * (D / 32);
+                if constexpr (D == 64) ke[i].x = *reinterpret_cast<const uint16_t*>(p);
+                else if constexpr (D == 128) ke[i].x = *reinterpret_cast<const uint32_t*>(p);
+                else ke[i] = *reinterpret_cast<const uint2*>(p);
+                vs[i] = fabsf(cache.v_scale[row]);
+            }
+        }
+    };
+    // piece i of the lane's share of the values: its tile, its row there and the place of
+    // that in LDS
+    auto value_tile = [&](int i) { return D == 64 ? 2 * i + (lane >> 5) : D == 128 ? i : i >> 1; };
+    const int v_row = D == 64 ? (lane & 31) >> 1 : D == 128 ? lane >> 2 : lane >> 3;
+    const int v_off = v_row * RB + lane % (D / 32) * 16;
+    auto value_place = [&](int i) {
+        const int t = value_tile(i), r = D == 256 ? v_row + 8 * (i & 1) : v_row;
+        return ((r >> 2) * 32 + 2 * (r & 3) + 8 * (t & 3) + (t >> 2)) * FewLds<D>::pitch + lane % (D / 32) * 16;
+    };
+
+    uint32_t now[2], next[2];
+    int t0 = w.k0 + kStep * wave;
+    load_entries(t0, now);
+    if (t0 < w.k1) load_keys(now, t0);
+    load_entries(t0 + 4 * kStep, next);
+
+    // q: the row n of the tile, the lane's 32 channels
+    u32x6 qf[KC][NM];
+    int qu[KC][2];
+    const int row = w.r0 + n;
+    const bool valid = row < w.rows;
+    const int tok = valid ? row / a.G : 0;
+    {
+        const int head = w.h * a.G + (valid ? row - tok * a.G : 0);
+        const E* q = static_cast<const E*>(a.q.p) + ((int64_t)(w.first + tok) * a.q.st + head * a.q.sh);
+        const float by = a.negate ? -a.scale2 : a.scale2;
+#pragma unroll
+        for (int cc = 0; cc < KC; ++cc) {
+            u32x6 p[NP + 1];
+            const int e = split_q<E, NP>(q + 128 * cc + 32 * (D == 64 ? g & 1 : g), valid, by, p);
+            qu[cc][0] = units(e, 0);
+            qu[cc][1] = units(e, 1);
+            if constexpr (D == 64) {
+                p[NP] = u32x6{0, 0, 0, 0, 0, 0};
+                uint32_t u = 0;
+#pragma unroll
+                for (int i = 0; i < NM; ++i) {
+                    qf[cc][i] = g >> 1 ? p[2 * i + 1] : p[2 * i];
+                    // (a row that is not finite has the unit NaN in its first piece at least)
+                    const int at = 2 * i + (g >> 1);
+                    u |= (uint32_t)(e == 255 ? 255 : at < NP ? e - 4 * at : 127) << (8 * i);
+                }
+                qu[cc][0] = (int)u;
+            } else {
+#pragma unroll
+                for (int i = 0; i < NM; ++i) qf[cc][i] = p[i];
+            }
+        }
+    }
+    const int pos = w.p0 + tok;
+    const int p_first = w.p0 + w.r0 / a.G;
+    const int p_last = w.p0 + ((w.rows - w.r0 < 16 ? w.rows : w.r0 + 16) - 1) / a.G;
+    f32x4 o[1][DT];
+#pragma unroll
+    for (int i = 0; i < DT; ++i) o[0][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float m[1] = {neg_inf()}, l[1] = {0.f};
+
+    for (; t0 < w.k1; t0 += 4 * kStep) {
+        // scales to LDS, values of this step into flight
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint8_t* p = lds.k_exp + (64 * i + lane) * (D / 32);
+            if constexpr (D == 64) *reinterpret_cast<uint16_t*>(p) = (uint16_t)ke[i].x;
+            else if constexpr (D == 128) *reinterpret_cast<uint32_t*>(p) = ke[i].x;
+            else *reinterpret_cast<uint2*>(p) = ke[i];
+            lds.v_scale[64 * i + lane] = vs[i];
+        }
+        uint4 vr[VL];
+#pragma unroll
+        for (int i = 0; i < VL; ++i) {
+            vr[i] = make_uint4(0, 0, 0, 0);
+            if constexpr (D == 64) {
+                const uint64_t r0 = tile_row(now, t0, 2 * i), r1 = tile_row(now, t0, 2 * i + 1);
+                if (t0 + 16 * value_tile(i) < w.k1)
+                    vr[i] = *reinterpret_cast<const uint4*>(cache.values + (lane < 32 ? r0 : r1) * RB + v_off);
+            } else if (t0 + 16 * value_tile(i) < w.k1) {
+                const uint8_t* p = cache.values + tile_row(now, t0, value_tile(i)) * RB;
+                vr[i] = *reinterpret_cast<const uint4*>(p + v_off + (D == 256 ? (i & 1) * 8 * RB : 0));
+            }
+        }
+
+        f32x4 s[8];
+        const float ref = -reference(m[0]);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            s[t] = f32x4{ref, ref, ref, ref};
+#pragma unroll
+            for (int cc = 0; cc < KC; ++cc) {
+                const int ku = lds.k_exp[(16 * t + n) * (D / 32) + (D == 64 ? g & 1 : 4 * cc + g)];
+                each<NM>([&](auto i) { s[t] = product<0, i % 4>(kr[t][cc], ku, qf[cc][i], qu[cc][i / 4], s[t]); });
+            }
+        }
+        const int tn = t0 + 4 * kStep;
+        now[0] = next[0];
+        now[1] = next[1];
+        if (tn < w.k1) load_keys(now, tn);
+        load_entries(tn + 4 * kStep, next);
+
+        float x[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = s[i >> 2][i & 3];
+        // a key beyond the row's position or before its window has no weight, whatever is
+        // stored there
+        const bool masked =
+            t0 + kStep - 1 > p_first || t0 + kStep > w.k1 || (a.window > 0 && t0 <= p_last - a.window);
+        const int up = last_seen(pos, t0, w.k1) - 4 * g, dn = before_seen(pos, t0, a.window) - 4 * g;
+        auto hidden = [&](int i) {
+            const int key = 16 * (i >> 2) + (i & 3);
+            return key > up || key <= dn;
+        };
+        if (masked)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (hidden(i)) x[i] = neg_inf();
+        float top = x[0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) top = fmaxf(top, x[i]);
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = max_halves(top);
+        follow(top, m[0], l[0], x, [&](float by) {
+#pragma unroll
+            for (int i = 0; i < DT; ++i) o[0][i] *= by;
+        });
+        u32x6 pf[PP];
+        float4 sv[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) sv[t] = *reinterpret_cast<const float4*>(&lds.v_scale[16 * t + 4 * g]);
+        const int pe = weights<PP>(
+            x, l[0], [&](int i) { return (&sv[i >> 2].x)[i & 3]; }, masked, hidden, pf);
+        const int pu[2] = {units(pe, 0), units(pe, 1)};
+
+#pragma unroll
+        for (int i = 0; i < VL; ++i) *reinterpret_cast<uint4*>(lds.values + value_place(i)) = vr[i];
+        const char* at = lds.values + (32 * g + n) * FewLds<D>::pitch;
+#pragma unroll
+        for (int i = 0; i < DT; ++i) {
+            const uint4 v = joined(transposed(at + 8 * i), transposed(at + 16 * FewLds<D>::pitch + 8 * i));
+            each<PP>([&](auto p) { o[0][i] = product<0, p % 4>(v, kOne, pf[p], pu[p / 4], o[0][i]); });
+        }
+    }
+    join_waves<E, D, 1>(a, w, parts, m, l, o, sm, sl, so);
+}
+
+template <typename E, int NP, int PP, int D>
+__global__ __launch_bounds__(256, few_held(D, sizeof(E) == 4)) void k_attend4_few(const Attn4Args args) {
+    __shared__ float sm[4][16], sl[4][16];
+    __shared__ __align__(16) float so[4][16][D + 4];
+    __shared__ __align__(16) FewLds<D> lds[4];
+    share_work(
+        args.a, 16,
+        [&](const Work& w, int parts) { attend4_few<E, NP, PP, D>(args, w, parts, lds[threadIdx.x >> 6], sm, sl, so); },
+        [&](int b) { lose_rows<E, D>(args.a, b, 0, args.a.Hq); });
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: four waves of 32 rows each share steps of 64 keys, staged in LDS as they lie.
+//
+// v_mfma_scale_f32_32x32x64_f8f6f4: lane l holds operand row or column l % 32, k = 32 (l /
+// 32) .. + 31, and of the result column l % 32, rows 8 (j / 4) + 4 (l / 32) + j % 4, j < 16.
+// With half = l / 32:
+//   S^T of 32 keys: 64 channels a product, the lane's are 32 (2 c + half) ..
+//   O^T of 64 keys: the lane has the weights of keys 8 (j / 4) + 4 half + j % 4 of the first
+//     32 (element 2 j) and of the second (2 j + 1). Value rows lie in LDS at the place 32
+//     half + element.
+// ---------------------------------------------------------------------------
+template <int D>
+struct RowsLds {
+    static constexpr int pitch = D / 2 + 16;
+    char keys[kTile * pitch], values[kTile * pitch];
+    float v_scale[kTile];
+    uint8_t k_exp[kTile * (D / 32)];
+};
+
+template <typename E, int NP, int PP, int D>
+__device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& w, int parts, RowsLds<D>* lds) {
+    const AttnArgs& a = args.a;
+    const CacheArgs& c = a.c;
+    const Cache4& cache = args.b;
+    constexpr int RB = D / 2, KC = D / 64, DT = D / 32, pitch = RowsLds<D>::pitch;
+    constexpr int CH = D == 256 ? 2 : 1;            // 16-byte pieces a thread stages of keys, and of values
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int col = lane & 31, half = lane >> 5;
+    const int r = w.r0 + 32 * wave + col;
+    const bool valid = r < w.rows;
+    const int tok = valid ? r / a.G : 0;
+    const int head = w.h * a.G + (valid ? r - tok * a.G : 0);
+    const int pos = w.p0 + tok;
+    const int32_t* table = c.table + (int64_t)w.b * c.table_stride;
+
+    // Staging. Heads of 64 have 128 pieces of each: the first half of the threads takes
+    // the keys, the second the values. Scales: a thread of the first wave the exponents of
+    // a key, one of the second its value scale.
+    const int piece = D == 64 ? tid & 127 : tid;
+    const bool takes_keys = D != 64 || tid < 128, takes_values = D != 64 || tid >= 128;
+    int key[CH], to_k[CH], to_v[CH];
+    const int chunk = piece % (D / 32) * 16;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        key[i] = (piece + 256 * i) / (D / 32);
+        to_k[i] = key[i] * pitch + chunk;
+        const int m = key[i] & 31;
+        to_v[i] = (32 * (m >> 2 & 1) + 2 * (4 * (m >> 3) + (m & 3)) + (key[i] >> 5)) * pitch + chunk;
+    }
+    uint32_t entry[CH], entry_s;
+    uint4 kr[CH], vr[CH];
+    uint2 ke = make_uint2(0, 0);
+    float vs = 0.f;
+    auto load_entries = [&](int t0) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) entry[i] = page_entry(c, table, t0 + key[i]);
+        entry_s = page_entry(c, table, t0 + lane);
+    };
+    auto load = [&](int t0) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            const uint64_t at = (page_row(c, page_in(c, entry[i]), w.h) + ((t0 + key[i]) & (c.P - 1))) * RB + chunk;
+            if (takes_keys) kr[i] = *reinterpret_cast<const uint4*>(cache.keys + at);
+            if (takes_values) vr[i] = *reinterpret_cast<const uint4*>(cache.values + at);
+        }
+        if (wave < 2) {
+            const bool known = known_page(c, entry_s, t0 + lane);
+            const uint64_t row = page_row(c, page_in(c, entry_s), w.h) + ((t0 + lane) & (c.P - 1));
+            if (wave == 0) {
+                const uint8_t* p = cache.k_exp + row * (D / 32);
+                if constexpr (D == 64) ke.x = *reinterpret_cast<const uint16_t*>(p);
+                else if constexpr (D == 128) ke.x = *reinterpret_cast<const uint32_t*>(p);
+                else ke = *reinterpret_cast<const uint2*>(p);
+                if (!known) ke = make_uint2(~0u, ~0u);
+            } else {
+                vs = known ? fabsf(cache.v_scale[row]) : __builtin_nanf("");
+            }
+        }
+    };
+    auto stage = [&](RowsLds<D>& to) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            if (takes_keys) *reinterpret_cast<uint4*>(to.keys + to_k[i]) = kr[i];
+            if (takes_values) *reinterpret_cast<uint4*>(to.values + to_v[i]) = vr[i];
+        }
+        if (wave == 0) {
+            uint8_t* p = to.k_exp + lane * (D / 32);
+            if constexpr (D == 64) *reinterpret_cast<uint16_t*>(p) = (uint16_t)ke.x;
+            else if constexpr (D == 128) *reinterpret_cast<uint32_t*>(p) = ke.x;
+            else *reinterpret_cast<uint2*>(p) = ke;
+        } else if (wave == 1) {
+            to.v_scale[lane] = vs;
+        }
+    };
+    // LDS written by this wave is visible after it; loads stay in flight
+    auto step_end = [&]() {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    if (w.k0 < w.k1) {
+        load_entries(w.k0);
+        load(w.k0);
+        load_entries(w.k0 + kTile);
+    }
+    u32x6 qf[KC][NP];
+    int qu[KC][2];
+    {
+        const E* q = static_cast<const E*>(a.q.p) + ((int64_t)(w.first + tok) * a.q.st + head * a.q.sh);
+        const float by = a.negate ? -a.scale2 : a.scale2;
+#pragma unroll
+        for (int cc = 0; cc < KC; ++cc) {
+            const int e = split_q<E, NP>(q + 64 * cc + 32 * half, valid, by, qf[cc]);
+            qu[cc][0] = units(e, 0);
+            qu[cc][1] = units(e, 1);
+        }
+    }
+    // positions of this wave's rows
+    const int w0 = w.r0 + 32 * wave, w1 = w.rows - w0 < 32 ? w.rows : w0 + 32;
+    const int p_first = w.p0 + w0 / a.G, p_last = w.p0 + (w1 - 1) / a.G;
+
+    f32x16 o[DT];
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
+    float m = neg_inf(), l = 0.f;
+
+    auto compute = [&](const RowsLds<D>& from, int t0) {
+        f32x16 s[2];
+        const float ref = -reference(m);
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s[tt][j] = ref;
+            const int at = 32 * tt + col;
+            uint32_t ku[2];
+            const uint8_t* p = from.k_exp + at * (D / 32);
+            if constexpr (D == 64) ku[0] = *reinterpret_cast<const uint16_t*>(p);
+            else ku[0] = *reinterpret_cast<const uint32_t*>(p);
+            if constexpr (D == 256) ku[1] = *reinterpret_cast<const uint32_t*>(p + 4);
+            // byte 2 c of the lane's words is the unit of block 2 c + half
+#pragma unroll
+            for (int i = 0; i < (D == 256 ? 2 : 1); ++i) ku[i] >>= 8 * half;
+            each<KC>([&](auto cc) {
+                const uint4 k = *reinterpret_cast<const uint4*>(from.keys + at * pitch + 32 * cc + 16 * half);
+                each<NP>([&](auto i) {
+                    s[tt] = product<2 * (cc % 2), i % 4>(k, (int)ku[cc / 2], qf[cc][i], qu[cc][i / 4], s[tt]);
+                });
+            });
+        }
+        float x[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = s[i >> 4][i & 15];
+        const bool masked =
+            t0 + kTile - 1 > p_first || t0 + kTile > w.k1 || (a.window > 0 && t0 <= p_last - a.window);
+        const int up = last_seen(pos, t0, w.k1) - 4 * half, dn = before_seen(pos, t0, a.window) - 4 * half;
+        auto hidden = [&](int i) {
+            const int k = 32 * (i >> 4) + 8 * (i >> 2 & 3) + (i & 3);
+            return k > up || k <= dn;
+        };
+        if (masked)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (hidden(i)) x[i] = neg_inf();
+        float top = x[0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) top = fmaxf(top, x[i]);
+        top = max_halves(top);
+        follow(top, m, l, x, [&](float by) {
+#pragma unroll
+            for (int i = 0; i < DT; ++i) o[i] *= by;
+        });
+        u32x6 pf[PP];
+        float4 sv[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            sv[i] = *reinterpret_cast<const float4*>(&from.v_scale[32 * (i >> 2) + 8 * (i & 3) + 4 * half]);
+        const int pe = weights<PP>(
+            x, l, [&](int i) { return (&sv[i >> 2].x)[i & 3]; }, masked, hidden, pf);
+        const int pu[2] = {units(pe, 0), units(pe, 1)};
+        const char* at = from.values + (32 * half + (lane & 15)) * pitch + 8 * (lane >> 4 & 1);
+#pragma unroll
+        for (int i = 0; i < DT; ++i) {
+            const uint4 v = joined(transposed(at + 16 * i), transposed(at + 16 * pitch + 16 * i));
+            each<PP>([&](auto p) { o[i] = product<0, p % 4>(v, kOne, pf[p], pu[p / 4], o[i]); });
+        }
+    };
+    if (w.k0 < w.k1) {
+        stage(lds[0]);
+        load(w.k0 + kTile);
+        load_entries(w.k0 + 2 * kTile);
+        step_end();
+    }
+    int buf = 0;
+    for (int t0 = w.k0; t0 < w.k1; t0 += kTile, buf ^= 1) {
+        // nothing to do for rows that see none of the tile's keys
+        if (w0 < w1 && t0 <= p_last && (a.window == 0 || (int64_t)t0 + kTile > (int64_t)p_first - a.window + 1))
+            compute(lds[buf], t0);
+        stage(lds[buf ^ 1]);
+        load(t0 + 2 * kTile);
+        load_entries(t0 + 3 * kTile);
+        step_end();
+    }
+
+    l += __shfl_xor(l, 32, 64);
+    if (!valid) return;
+    const int64_t row = (int64_t)(w.first + tok) * a.Hq + head;
+    const bool seen = row_sees(pos, a.window, w.k0, w.k1);
+    const float inv = parts == 1 ? row_inverse(l, seen) : 1.f;
+    const int64_t part = row * a.splits + w.part;
+    E* out = static_cast<E*>(a.out.p) + ((int64_t)(w.first + tok) * a.out.st + head * a.out.sh);
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int d = 32 * i + 8 * q + 4 * half;
+            const float v[4] = {o[i][4 * q] * inv, o[i][4 * q + 1] * inv, o[i][4 * q + 2] * inv, o[i][4 * q + 3] * inv};
+            if (parts == 1) store4(out + d, v);
+            else store4(a.part_o + part * D + d, v);
+        }
+    if (half != 0) return;
+    if (parts > 1) a.part_ml[part] = make_float2(m, l == 0.f && seen ? -1.f : l);
+    else if (a.lse) a.lse[row] = row_lse(m, l, seen);
+    if (a.splits > 1 && w.part == 0) a.parts[row] = parts;
+}
+
+// SHARED: in equal shares (share_work), else a workgroup for each row tile, head and range
+// of keys (find_work). Sequences of few rows beside ones of many keep their weights to
+// three pieces.
+template <typename E, int NP, int PP, int D, bool SHARED>
+__global__ __launch_bounds__(256, few_held(D, sizeof(E) == 4)) void k_attend4_rows(const Attn4Args args) {
+    __shared__ __align__(16) RowsLds<D> lds[2];
+    auto attend = [&](const Work& w, int parts) {
+        if constexpr (PP == 2)
+            if (w.rows <= kPreciseRows) return attend4_rows<E, NP, 3, D>(args, w, parts, lds);
+        attend4_rows<E, NP, PP, D>(args, w, parts, lds);
+    };
+    if constexpr (SHARED) {
+        share_work(
+            args.a, 128,
+            [&](const Work& w, int parts) {
+                __syncthreads();        // the work before has been read from LDS
+                attend(w, parts);
+            },
+            [&](int b) { lose_rows<E, D>(args.a, b, 0, args.a.Hq); });
+    } else {
+        Work w;
+        auto lost = [&](int b, int h) { lose_rows<E, D>(args.a, b, h * args.a.G, (h + 1) * args.a.G); };
+        if (find_work(args.a, 128, w, lost)) attend(w, args.a.splits);
+    }
+}
+
+template <typename E, int NP, int PP, int D>
+hipError_t launch_rows(const Attn4Args& a, const AttnPlan& plan, hipStream_t s) {
+    if (plan.shared) {
+        k_attend4_rows<E, NP, PP, D, true><<<dim3((unsigned)plan.blocks), 256, 0, s>>>(a);
+        return hipGetLastError();
+    }
+    return launch_in_pieces(plan.blocks, [&](uint32_t first, unsigned n) {
+        Attn4Args piece = a;
+        piece.a.first_block = first;
+        k_attend4_rows<E, NP, PP, D, false><<<n, 256, 0, s>>>(piece);
+    });
+}
+
+template <typename E, int D>
+hipError_t launch(const Attn4Args& a, const AttnPlan& plan, hipStream_t s) {
+    constexpr bool wide = sizeof(E) == 4;
+    hipError_t e = hipSuccess;
+    if (plan.few) {
+        k_attend4_few<E, wide ? 5 : 3, wide ? 5 : 3, D><<<dim3((unsigned)plan.blocks), 256, 0, s>>>(a);
+        e = hipGetLastError();
+    } else {
+        e = launch_rows<E, wide ? 5 : 3, wide ? 5 : 2, D>(a, plan, s);
+    }
+    return e != hipSuccess ? e : launch_join<E, D>(a.a, plan, s);
+}
+
+template <typename E>
+hipError_t launch_dim(const Attn4Args& a, const AttnPlan& plan, hipStream_t s) {
+    switch (a.a.c.D) {
+        case 64: return launch<E, 64>(a, plan, s);
+        case 128: return launch<E, 128>(a, plan, s);
+        default: return launch<E, 256>(a, plan, s);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_cache4_attention(const CacheArgs& c, const Cache4& b, const AttnPlan& plan, const Heads& q, int Hq,
+                                   float scale, int window, const Heads& out, float* lse, void* ws, hipStream_t s) {
+    const Attn4Args a{attn_args(c, plan, q, Hq, scale, window, out, lse, ws), b};
+    return c.dt == Dt::BF16 ? launch_dim<uint16_t>(a, plan, s) : launch_dim<float>(a, plan, s);
+}
+
+}  // namespace sffn

@@ -1,0 +1,187 @@
+// The paged 4-bit cache: new tokens stored, tokens read back.
+//
+//   keys: for 32 channels e = the least power of two with max|k| <= 6 e, entry k / e;
+//   values: s = max|v| / 6 of the token and head, entry v / s;
+//   entries rounded to {0, 0.5, 1, 1.5, 2, 3, 4, 6}, ties to the even code.
+//
+// A lane has eight channels of a token and head, keys and values alike: 16 bytes in (fp32:
+// two times 16), 4 bytes of entries out. Largest values are compared as integers, in which
+// infinities and NaN come out on top. Every token's scales are its own: nothing that is held
+// is touched. Memory-bound.
+#include "attn_common.hpp"
+
+namespace sffn {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// Where token t of the call lies: its slot, kLost where it shows as NaN (beyond max_new,
+// offsets that leave the call, no page), kNone in no sequence.
+constexpr int64_t kLost = -1, kNone = -2;
+__device__ __forceinline__ int64_t slot_of(const CacheArgs& c, int t) {
+    int b = t, first = t, last = t + 1;
+    if (c.cu) {
+        int lo = 0, hi = c.B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (c.cu[mid] <= t) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+        first = c.cu[b];
+        last = c.cu[b + 1];
+        if (t < first || t >= last) return kNone;
+        if (first < 0 || last > c.T || t - first >= c.max_new) return kLost;
+    }
+    const int64_t pos = (int64_t)c.lens[b] - (last - first) + (t - first);
+    if (pos < 0 || (pos >> c.shift) >= c.max_pages) return kLost;
+    const uint32_t page = (uint32_t)c.table[(int64_t)b * c.table_stride + (pos >> c.shift)];
+    if (page >= (uint64_t)c.n_pages) return kLost;
+    return ((int64_t)page << c.shift) + (pos & (c.P - 1));
+}
+
+// Row (token of a page and head) of the cache's arrays.
+__device__ __forceinline__ int64_t row_of_slot(const CacheArgs& c, int64_t slot, int h) {
+    return (((slot >> c.shift) * c.Hkv + h) << c.shift) + (slot & (c.P - 1));
+}
+
+// Eight entries of x, already divided by their scale but for the power of two `by`.
+__device__ __forceinline__ uint32_t entries8(const float* x, float by) {
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0], x[1], by, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2], x[3], by, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4], x[5], by, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6], x[7], by, 3);
+}
+__device__ __forceinline__ void values8(uint32_t w, float* x) {
+#define SFFN_TWO(i)                                                                   \
+    {                                                                                 \
+        const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, i);           \
+        x[2 * i] = p[0];                                                              \
+        x[2 * i + 1] = p[1];                                                          \
+    }
+    SFFN_TWO(0) SFFN_TWO(1) SFFN_TWO(2) SFFN_TWO(3)
+#undef SFFN_TWO
+}
+
+// Largest magnitude of eight, as an integer (NaN above infinity above numbers), over
+// groups of LANES lanes.
+template <int LANES>
+__device__ __forceinline__ uint32_t largest(const float* x) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+    return m;
+}
+
+// Rows (token, head) that a workgroup takes at a time.
+constexpr int rows_each(int D) { return kThreads * 8 / D; }
+
+template <typename E, int D>
+__global__ __launch_bounds__(kThreads) void k_cache4_append(const CacheArgs c, const Cache4 cache, const int64_t* slots,
+                                                            const Heads k, const Heads v, uint32_t first) {
+    const int64_t r = ((int64_t)first + blockIdx.x) * rows_each(D) + threadIdx.x / (D / 8);
+    if (r >= c.T * c.Hkv) return;           // whole groups of D / 8 lanes
+    const int t = (int)(r / c.Hkv), h = (int)(r % c.Hkv), d = threadIdx.x % (D / 8) * 8;
+    float x[8], y[8];
+    Elem<E>::load8(static_cast<const E*>(k.p) + (t * k.st + h * k.sh) + d, x);
+    Elem<E>::load8(static_cast<const E*>(v.p) + (t * v.st + h * v.sh) + d, y);
+    const int64_t slot = slots ? slots[t] : slot_of(c, t);
+    const bool stored = slot >= 0 && slot < c.n_pages << c.shift;
+    const int64_t row = row_of_slot(c, stored ? slot : 0, h);
+
+    const uint32_t top = largest<4>(x);     // of 32 channels
+    int e = max((int)(top >> 23) - 2 + ((top & 0x7fffffu) > 0x400000u), 0);
+    if (top >= 0x7f800000u) e = 255;
+    // powers of two below fp32's normal numbers: both sides 2^64 larger
+    const bool low = e < 64;
+    if (low)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= 0x1p64f;
+    const uint32_t kw = entries8(x, __uint_as_float((uint32_t)(low ? e + 64 : e == 255 ? 127 : e) << 23));
+
+    const uint32_t most = largest<D / 8>(y);        // of the head
+    const float s = most >= 0x7f800000u ? __builtin_nanf("") : __uint_as_float(most) / 6.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = s > 0.f ? y[i] / s : 0.f;
+    const uint32_t vw = entries8(y, 1.f);
+    if (!stored) return;
+    *reinterpret_cast<uint32_t*>(cache.keys + row * (D / 2) + d / 2) = kw;
+    *reinterpret_cast<uint32_t*>(cache.values + row * (D / 2) + d / 2) = vw;
+    if (d % 32 == 0) cache.k_exp[row * (D / 32) + d / 32] = (uint8_t)e;
+    if (d == 0) cache.v_scale[row] = s;
+}
+
+template <typename E, int D>
+__global__ __launch_bounds__(kThreads) void k_cache4_read(const CacheArgs c, const Cache4 cache, const Heads k,
+                                                          const Heads v, uint32_t first) {
+    const int64_t r = ((int64_t)first + blockIdx.x) * rows_each(D) + threadIdx.x / (D / 8);
+    if (r >= c.T * c.Hkv) return;
+    const int t = (int)(r / c.Hkv), h = (int)(r % c.Hkv), d = threadIdx.x % (D / 8) * 8;
+    const int64_t slot = slot_of(c, t);
+    if (slot == kNone) return;
+    float x[8], y[8];
+    if (slot == kLost) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = y[i] = __builtin_nanf("");
+    } else {
+        const int64_t row = row_of_slot(c, slot, h);
+        const uint32_t kw = *reinterpret_cast<const uint32_t*>(cache.keys + row * (D / 2) + d / 2);
+        const uint32_t vw = *reinterpret_cast<const uint32_t*>(cache.values + row * (D / 2) + d / 2);
+        const int e = cache.k_exp[row * (D / 32) + d / 32];
+        const float s = cache.v_scale[row];
+        values8(kw, x);
+        values8(vw, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[i] = e == 255 ? __builtin_nanf("") : ldexpf(x[i], e - 127);
+            y[i] *= s;
+        }
+    }
+    store8(static_cast<E*>(k.p) + (t * k.st + h * k.sh) + d, x);
+    store8(static_cast<E*>(v.p) + (t * v.st + h * v.sh) + d, y);
+}
+
+template <typename E, int D>
+hipError_t append(const CacheArgs& c, const Cache4& b, const int64_t* slots, const Heads& k, const Heads& v,
+                  hipStream_t s) {
+    return launch_in_pieces((c.T * c.Hkv + rows_each(D) - 1) / rows_each(D), [&](uint32_t first, unsigned n) {
+        k_cache4_append<E, D><<<dim3(n), kThreads, 0, s>>>(c, b, slots, k, v, first);
+    });
+}
+
+template <typename E, int D>
+hipError_t read(const CacheArgs& c, const Cache4& b, const Heads& k, const Heads& v, hipStream_t s) {
+    return launch_in_pieces((c.T * c.Hkv + rows_each(D) - 1) / rows_each(D), [&](uint32_t first, unsigned n) {
+        k_cache4_read<E, D><<<dim3(n), kThreads, 0, s>>>(c, b, k, v, first);
+    });
+}
+
+// f(element type, head width)
+template <typename F>
+hipError_t by_kind(const CacheArgs& c, F f) {
+    auto width = [&](auto e) {
+        switch (c.D) {
+            case 64: return f(e, std::integral_constant<int, 64>{});
+            case 128: return f(e, std::integral_constant<int, 128>{});
+            default: return f(e, std::integral_constant<int, 256>{});
+        }
+    };
+    return c.dt == Dt::BF16 ? width((uint16_t)0) : width(0.f);
+}
+
+}  // namespace
+
+hipError_t launch_cache4_append(const CacheArgs& c, const Cache4& b, const int64_t* slots, const Heads& k,
+                                const Heads& v, hipStream_t s) {
+    return by_kind(c, [&](auto e, auto d) { return append<decltype(e), d.value>(c, b, slots, k, v, s); });
+}
+
+hipError_t launch_cache4_read(const CacheArgs& c, const Cache4& b, const Heads& k, const Heads& v, hipStream_t s) {
+    return by_kind(c, [&](auto e, auto d) { return read<decltype(e), d.value>(c, b, k, v, s); });
+}
+
+}  // namespace sffn

@@ -7,6 +7,8 @@
  *   kv_cache_append        new keys and values into a paged 8-bit cache
  *   kv_cache_read          tokens of the cache as the values they stand for
  *   cache_attention        attention of new tokens over that cache
+ *   kv_cache4_append, kv_cache4_read, cache4_attention
+ *                          the same for a paged 4-bit cache
  *
  * The conventions of sparse_ffn.h hold: status codes only, every argument
  * checked before anything is enqueued, asynchronous on `hip_stream`, nothing
@@ -171,6 +173,57 @@ sffn_status_t cache_attention(const sffn_kv_cache_t* cache, const sffn_kv_batch_
                               int32_t n_q_heads, sffn_dtype_t dtype, int64_t T, float scale, int32_t window,
                               const sffn_heads_t* out, float* lse, void* workspace, size_t ws_bytes,
                               void* hip_stream);
+
+/* ---- the 4-bit cache --------------------------------------------------------- */
+
+/* As the 8-bit cache, with entries of 4-bit floating point: a sign, two bits of exponent
+ * and one of mantissa, the codes 0 .. 7 standing for 0, 0.5, 1, 1.5, 2, 3, 4, 6 and 8 .. 15
+ * for their negatives; two in a byte, the even channel in the low half. Every token's
+ * scales are its own, so an append changes no other token's entries.
+ *   keys, values  uint8 [n_pages, kv_heads, page, head_dim / 2]
+ *   k_exp    uint8 [n_pages, kv_heads, page, head_dim / 32]: a key is its entry times
+ *            2^(k_exp - 127) of its 32 channels; 255 stands for NaN
+ *   v_scale  fp32 [n_pages, kv_heads, page]: a value is its entry times its token's scale
+ * page 16, 32, 64 or 128; head_dim 64, 128 or 256; pointers 16-byte aligned. 68 + 68 bytes
+ * a token and head of 128 channels, where the 8-bit cache takes 256. */
+typedef struct {
+    uint8_t* keys;
+    uint8_t* values;
+    uint8_t* k_exp;
+    float* v_scale;
+    int64_t n_pages;
+    int32_t kv_heads;
+    int32_t page;
+    int32_t head_dim;
+} sffn_kv_cache4_t;
+
+/* Store k, v [T, kv_heads, head_dim] (views, 16-byte aligned rows) of T tokens. For each 32
+ * channels of a key the least power of two by which none of them exceeds 6 (at least
+ * 2^-127), and 255 where one is NaN or infinite; for a value v_scale = max|v| / 6 (NaN where
+ * one is NaN or infinite). Entries are x / scale rounded to the nearest, ties to the even
+ * code (IEEE fp32 arithmetic; zero where v_scale is 0, undefined where a scale is NaN).
+ *   slots  [T] int64 (device): page * (page's number) + (place in the page) of every token,
+ *          which is not stored where that lies outside the pool; NULL: the slots follow from
+ *          the batch. With slots the batch is not read and may be NULL. No two tokens may
+ *          have the same slot. */
+sffn_status_t kv_cache4_append(const sffn_kv_cache4_t* cache, const sffn_kv_batch_t* batch, const int64_t* slots,
+                               const sffn_heads_t* k, const sffn_heads_t* v, sffn_dtype_t dtype, int64_t T,
+                               void* hip_stream);
+
+/* As kv_cache_read. */
+sffn_status_t kv_cache4_read(const sffn_kv_cache4_t* cache, const sffn_kv_batch_t* batch, const sffn_heads_t* k,
+                             const sffn_heads_t* v, sffn_dtype_t dtype, int64_t T, void* hip_stream);
+
+/* As cache_attention_workspace_size and cache_attention. The products take 4-bit entries as
+ * they are; q and the weights of the values are sums of 6-bit pieces relative to the largest
+ * of 32 channels (q) or keys (weights): q to 2^-13 of it, weights to 2^-9 in sequences of more
+ * than 128 rows and to 2^-13 in those of fewer; 2^-21 both for an fp32 q. */
+size_t cache4_attention_workspace_size(const sffn_kv_cache4_t* cache, const sffn_kv_batch_t* batch,
+                                       int32_t n_q_heads, sffn_dtype_t dtype, int32_t window, int64_t T);
+sffn_status_t cache4_attention(const sffn_kv_cache4_t* cache, const sffn_kv_batch_t* batch, const sffn_heads_t* q,
+                               int32_t n_q_heads, sffn_dtype_t dtype, int64_t T, float scale, int32_t window,
+                               const sffn_heads_t* out, float* lse, void* workspace, size_t ws_bytes,
+                               void* hip_stream);
 
 #ifdef __cplusplus
 }
