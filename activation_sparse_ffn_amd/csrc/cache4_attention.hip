@@ -15,11 +15,14 @@
 // left, at 1 / 16 of their unit. The first leaves a quarter of a unit at most (rounding
 // among steps of 1 / 2), the second 2^-7 (a quarter is 4 of its units, below which steps
 // are 1 / 4), the third 2^-12 (2 of its units, steps of 1 / 8), each more 2^-4 of that:
-// two pieces are exact to 2^-8.9 of the block's largest, three to 2^-13.9, five to
-// 2^-21.9. q's blocks are 32 channels of a row, the weights' the 32 keys of a row that a
-// lane holds. q of bf16 has three
-// pieces, of fp32 five; weights two in sequences of more than kPreciseRows rows, three in
-// those of fewer, five for fp32. The sum l takes the weights before they are cut.
+// three pieces are exact to 2^-13.9 of the block's largest, four to 2^-17.9, five to
+// 2^-21.9. Where there are but two, the second's unit is 1 / 32 of the first's: what the
+// few largest elements leave may pass its range (they are exact to 2^-6 units, 2^-7.9 of
+// the largest), the many below a quarter of the largest are so to 2^-9 units, half of what
+// 1 / 16 leaves. q's blocks are 32 channels of a row, the weights' the 32 keys of a row that
+// a lane holds. q of bf16 has four pieces, of fp32 five; weights two in sequences of more
+// than kPreciseRows rows, three in those of fewer, five for fp32. The sum l takes the
+// weights before they are cut.
 #include <type_traits>
 #include <utility>
 
@@ -33,6 +36,16 @@ struct Attn4Args {
     AttnArgs a;
     Cache4 b;
 };
+
+// The kernel's arguments once more, read where this is called: what only a work's end needs
+// would be kept in spilled scalars during its loop.
+__device__ __forceinline__ AttnArgs late_args() {
+    auto p = (const __attribute__((address_space(4))) char*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    AttnArgs a;
+    __builtin_memcpy(&a, (const void*)(p + offsetof(Attn4Args, a)), sizeof a);
+    return a;
+}
 
 typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
@@ -51,28 +64,33 @@ __device__ __forceinline__ void each(F f) {
 
 // ---- 6-bit pieces ---------------------------------------------------------------
 
+// A piece's unit is 2^-ratio of the one's before.
+constexpr int ratio_of(int NP) { return NP == 2 ? 5 : 4; }
+
 // Exponent (plus 127) of the unit of a block whose largest magnitude has the bits `top`:
 // that lies in (3.75, 7.5] units. 255, which is NaN to the matrix cores, where it is not
 // finite. The last of NP pieces' units is still a normal number.
 template <int NP>
 __device__ __forceinline__ int unit_of(uint32_t top) {
-    const int e = (int)(top >> 23) - 2 + ((top & 0x7fffffu) > 0x700000u);
-    return top >= 0x7f800000u ? 255 : max(e, 4 * NP - 3);
+    const int e = (int)((top + 0x0fffffu) >> 23) - 2;
+    return top >= 0x7f800000u ? 255 : max(e, ratio_of(NP) * (NP - 1) + 1);
 }
-// The units of pieces 4 i .. 4 i + 3, a byte each.
-__device__ __forceinline__ int units(int e, int i) {
-    return e == 255 ? -1 : (int)((uint32_t)(e - 16 * i) * 0x01010101u - 0x0c080400u);
+// The units of NP pieces, a byte each, in two words.
+template <int NP>
+__device__ __forceinline__ void units(int e, int (&u)[2]) {
+    constexpr uint32_t r = ratio_of(NP), steps = r << 8 | 2 * r << 16 | 3 * r << 24;
+    u[0] = e == 255 ? -1 : (int)((uint32_t)e * 0x01010101u - steps);
+    u[1] = NP <= 4 ? 0 : e == 255 ? -1 : e - 4 * (int)r;
 }
 
-// 32 numbers as NP pieces of unit 2^(e - 127), 2^(e - 131) ..: element 2 j is lo[j], 2 j + 1
-// hi[j]. The conversions write their result while they still read their operands: the empty
+// 32 numbers as NP pieces, the first of unit 2^(e - 127): element 2 j is lo[j], 2 j + 1 hi[j]. The conversions write their result while they still read their operands: the empty
 // asm keeps those, the unit among them, in other registers. (With the result over an operand
 // the pieces were wrong.)
 template <int NP>
 __device__ __forceinline__ void split(f32x16 lo, f32x16 hi, int e, u32x6* out) {
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-        const float unit = __uint_as_float((uint32_t)(e - 4 * p) << 23);
+        const float unit = __uint_as_float((uint32_t)(e - ratio_of(NP) * p) << 23);
         u32x6 r = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(lo, hi, unit);
         asm("" : "+v"(r) : "v"(lo), "v"(hi), "v"(unit));
         out[p] = r;
@@ -306,8 +324,7 @@ __device__ __forceinline__ void attend4_few(const Attn4Args& args, const Work& w
         for (int cc = 0; cc < KC; ++cc) {
             u32x6 p[NP + 1];
             const int e = split_q<E, NP>(q + 128 * cc + 32 * (D == 64 ? g & 1 : g), valid, by, p);
-            qu[cc][0] = units(e, 0);
-            qu[cc][1] = units(e, 1);
+            units<NP>(e, qu[cc]);
             if constexpr (D == 64) {
                 p[NP] = u32x6{0, 0, 0, 0, 0, 0};
                 uint32_t u = 0;
@@ -381,7 +398,7 @@ __device__ __forceinline__ void attend4_few(const Attn4Args& args, const Work& w
         // stored there
         const bool masked =
             t0 + kStep - 1 > p_first || t0 + kStep > w.k1 || (a.window > 0 && t0 <= p_last - a.window);
-        const int up = last_seen(pos, t0, w.k1) - 4 * g, dn = before_seen(pos, t0, a.window) - 4 * g;
+        int up = last_seen(pos, t0, w.k1) - 4 * g, dn = before_seen(pos, t0, a.window) - 4 * g;
         auto hidden = [&](int i) {
             const int key = 16 * (i >> 2) + (i & 3);
             return key > up || key <= dn;
@@ -399,13 +416,15 @@ __device__ __forceinline__ void attend4_few(const Attn4Args& args, const Work& w
 #pragma unroll
             for (int i = 0; i < DT; ++i) o[0][i] *= by;
         });
+        asm("" : "+v"(up), "+v"(dn));       // hidden() again: 32 masks kept until then are as many scalars spilled
         u32x6 pf[PP];
         float4 sv[8];
 #pragma unroll
         for (int t = 0; t < 8; ++t) sv[t] = *reinterpret_cast<const float4*>(&lds.v_scale[16 * t + 4 * g]);
         const int pe = weights<PP>(
             x, l[0], [&](int i) { return (&sv[i >> 2].x)[i & 3]; }, masked, hidden, pf);
-        const int pu[2] = {units(pe, 0), units(pe, 1)};
+        int pu[2];
+        units<PP>(pe, pu);
 
 #pragma unroll
         for (int i = 0; i < VL; ++i) *reinterpret_cast<uint4*>(lds.values + value_place(i)) = vr[i];
@@ -416,7 +435,7 @@ __device__ __forceinline__ void attend4_few(const Attn4Args& args, const Work& w
             each<PP>([&](auto p) { o[0][i] = product<0, p % 4>(v, kOne, pf[p], pu[p / 4], o[0][i]); });
         }
     }
-    join_waves<E, D, 1>(a, w, parts, m, l, o, sm, sl, so);
+    join_waves<E, D, 1>(late_args(), w, parts, m, l, o, sm, sl, so);
 }
 
 template <typename E, int NP, int PP, int D>
@@ -463,49 +482,63 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
     const int tok = valid ? r / a.G : 0;
     const int head = w.h * a.G + (valid ? r - tok * a.G : 0);
     const int pos = w.p0 + tok;
-    const int32_t* table = c.table + (int64_t)w.b * c.table_stride;
+    const ConstTable table = (ConstTable)(uintptr_t)(c.table + (int64_t)w.b * c.table_stride);
 
-    // Staging. Heads of 64 have 128 pieces of each: the first half of the threads takes
-    // the keys, the second the values. Scales: a thread of the first wave the exponents of
-    // a key, one of the second its value scale.
-    const int piece = D == 64 ? tid & 127 : tid;
-    const bool takes_keys = D != 64 || tid < 128, takes_values = D != 64 || tid >= 128;
-    int key[CH], to_k[CH], to_v[CH];
-    const int chunk = piece % (D / 32) * 16;
+    // Staging: a thread has CH pieces of 16 bytes of the keys and as many of the values
+    // (heads of 64: one, in the first two waves of the keys, in the others of the values), a
+    // wave the scales of 16 keys. What a wave loads lies in one page (heads of 64: two): page
+    // entries and addresses are scalar.
+    constexpr int PW = 1024 / RB;                   // keys of a wave's 64 pieces
+    const int first_key = D == 64 ? 32 * (wave & 1) : PW * wave;
+    const bool takes_keys = D != 64 || wave < 2, takes_values = D != 64 || wave >= 2;
+    const uint32_t off = (lane * 16 / RB & 15) * RB + lane * 16 % RB;    // in 16 keys
+    int to_k[CH], to_v[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-        key[i] = (piece + 256 * i) / (D / 32);
-        to_k[i] = key[i] * pitch + chunk;
-        const int m = key[i] & 31;
-        to_v[i] = (32 * (m >> 2 & 1) + 2 * (4 * (m >> 3) + (m & 3)) + (key[i] >> 5)) * pitch + chunk;
+        const int key = first_key + 4 * PW * i + lane * 16 / RB, m = key & 31, chunk = lane * 16 % RB;
+        to_k[i] = key * pitch + chunk;
+        to_v[i] = (32 * (m >> 2 & 1) + 2 * (4 * (m >> 3) + (m & 3)) + (key >> 5)) * pitch + chunk;
     }
-    uint32_t entry[CH], entry_s;
+    uint32_t entry[2], entry_s = 0;
     uint4 kr[CH], vr[CH];
     uint2 ke = make_uint2(0, 0);
     float vs = 0.f;
     auto load_entries = [&](int t0) {
 #pragma unroll
-        for (int i = 0; i < CH; ++i) entry[i] = page_entry(c, table, t0 + key[i]);
-        entry_s = page_entry(c, table, t0 + lane);
+        for (int i = 0; i < 2; ++i)
+            if (i < (D == 128 ? 1 : 2)) entry[i] = page_entry(c, table, t0 + first_key + (D == 64 ? 16 : 4 * PW) * i);
+        entry_s = D == 128 ? entry[0] : page_entry(c, table, t0 + 16 * wave);
     };
     auto load = [&](int t0) {
+        // byte of the first of the 16 keys that key0 is one of
+        auto at = [&](uint32_t e, int key0) {
+            return (page_row(c, page_in(c, e), w.h) + ((t0 + (key0 & ~15)) & (c.P - 1))) * RB;
+        };
+        if constexpr (D == 64) {
+            const uint64_t b0 = at(entry[0], first_key), b1 = at(entry[1], first_key + 16);
+            const uint64_t p = (lane < 32 ? b0 : b1) + off;
+            if (takes_keys) kr[0] = *reinterpret_cast<const uint4*>(cache.keys + p);
+            else vr[0] = *reinterpret_cast<const uint4*>(cache.values + p);
+        } else {
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            const uint64_t at = (page_row(c, page_in(c, entry[i]), w.h) + ((t0 + key[i]) & (c.P - 1))) * RB + chunk;
-            if (takes_keys) kr[i] = *reinterpret_cast<const uint4*>(cache.keys + at);
-            if (takes_values) vr[i] = *reinterpret_cast<const uint4*>(cache.values + at);
+            for (int i = 0; i < CH; ++i) {
+                const int key0 = first_key + 4 * PW * i;
+                const uint64_t b = at(entry[i], key0) + (key0 & 15) * RB;
+                kr[i] = *reinterpret_cast<const uint4*>(cache.keys + b + off);
+                vr[i] = *reinterpret_cast<const uint4*>(cache.values + b + off);
+            }
         }
-        if (wave < 2) {
-            const bool known = known_page(c, entry_s, t0 + lane);
-            const uint64_t row = page_row(c, page_in(c, entry_s), w.h) + ((t0 + lane) & (c.P - 1));
-            if (wave == 0) {
-                const uint8_t* p = cache.k_exp + row * (D / 32);
-                if constexpr (D == 64) ke.x = *reinterpret_cast<const uint16_t*>(p);
-                else if constexpr (D == 128) ke.x = *reinterpret_cast<const uint32_t*>(p);
-                else ke = *reinterpret_cast<const uint2*>(p);
-                if (!known) ke = make_uint2(~0u, ~0u);
-            } else {
-                vs = known ? fabsf(cache.v_scale[row]) : __builtin_nanf("");
+        if (lane < 16) {
+            const int t = t0 + 16 * wave;
+            const uint64_t row = page_row(c, page_in(c, entry_s), w.h) + (t & (c.P - 1));
+            const uint8_t* p = cache.k_exp + row * (D / 32) + lane * (D / 32);
+            if constexpr (D == 64) ke.x = *reinterpret_cast<const uint16_t*>(p);
+            else if constexpr (D == 128) ke.x = *reinterpret_cast<const uint32_t*>(p);
+            else ke = *reinterpret_cast<const uint2*>(p);
+            vs = fabsf((cache.v_scale + row)[lane]);
+            if (!known_page(c, entry_s, t)) {
+                ke = make_uint2(~0u, ~0u);
+                vs = __builtin_nanf("");
             }
         }
     };
@@ -515,13 +548,13 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
             if (takes_keys) *reinterpret_cast<uint4*>(to.keys + to_k[i]) = kr[i];
             if (takes_values) *reinterpret_cast<uint4*>(to.values + to_v[i]) = vr[i];
         }
-        if (wave == 0) {
-            uint8_t* p = to.k_exp + lane * (D / 32);
+        if (lane < 16) {
+            const int key = 16 * wave + lane;
+            uint8_t* p = to.k_exp + key * (D / 32);
             if constexpr (D == 64) *reinterpret_cast<uint16_t*>(p) = (uint16_t)ke.x;
             else if constexpr (D == 128) *reinterpret_cast<uint32_t*>(p) = ke.x;
             else *reinterpret_cast<uint2*>(p) = ke;
-        } else if (wave == 1) {
-            to.v_scale[lane] = vs;
+            to.v_scale[key] = vs;
         }
     };
     // LDS written by this wave is visible after it; loads stay in flight
@@ -544,8 +577,7 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
 #pragma unroll
         for (int cc = 0; cc < KC; ++cc) {
             const int e = split_q<E, NP>(q + 64 * cc + 32 * half, valid, by, qf[cc]);
-            qu[cc][0] = units(e, 0);
-            qu[cc][1] = units(e, 1);
+            units<NP>(e, qu[cc]);
         }
     }
     // positions of this wave's rows
@@ -558,14 +590,15 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
     float m = neg_inf(), l = 0.f;
+    f32x16 start;           // what scores begin from: minus the reference, as the products' third operand
+#pragma unroll
+    for (int j = 0; j < 16; ++j) start[j] = 0.f;
 
     auto compute = [&](const RowsLds<D>& from, int t0) {
         f32x16 s[2];
-        const float ref = -reference(m);
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) s[tt][j] = ref;
+            s[tt] = start;
             const int at = 32 * tt + col;
             uint32_t ku[2];
             const uint8_t* p = from.k_exp + at * (D / 32);
@@ -587,7 +620,7 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
         for (int i = 0; i < 32; ++i) x[i] = s[i >> 4][i & 15];
         const bool masked =
             t0 + kTile - 1 > p_first || t0 + kTile > w.k1 || (a.window > 0 && t0 <= p_last - a.window);
-        const int up = last_seen(pos, t0, w.k1) - 4 * half, dn = before_seen(pos, t0, a.window) - 4 * half;
+        int up = last_seen(pos, t0, w.k1) - 4 * half, dn = before_seen(pos, t0, a.window) - 4 * half;
         auto hidden = [&](int i) {
             const int k = 32 * (i >> 4) + 8 * (i >> 2 & 3) + (i & 3);
             return k > up || k <= dn;
@@ -603,7 +636,11 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
         follow(top, m, l, x, [&](float by) {
 #pragma unroll
             for (int i = 0; i < DT; ++i) o[i] *= by;
+            const float ref = -reference(m);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) start[j] = ref;
         });
+        asm("" : "+v"(up), "+v"(dn));       // hidden() again: 32 masks kept until then are as many scalars spilled
         u32x6 pf[PP];
         float4 sv[8];
 #pragma unroll
@@ -611,7 +648,8 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
             sv[i] = *reinterpret_cast<const float4*>(&from.v_scale[32 * (i >> 2) + 8 * (i & 3) + 4 * half]);
         const int pe = weights<PP>(
             x, l, [&](int i) { return (&sv[i >> 2].x)[i & 3]; }, masked, hidden, pf);
-        const int pu[2] = {units(pe, 0), units(pe, 1)};
+        int pu[2];
+        units<PP>(pe, pu);
         const char* at = from.values + (32 * half + (lane & 15)) * pitch + 8 * (lane >> 4 & 1);
 #pragma unroll
         for (int i = 0; i < DT; ++i) {
@@ -638,11 +676,12 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
 
     l += __shfl_xor(l, 32, 64);
     if (!valid) return;
-    const int64_t row = (int64_t)(w.first + tok) * a.Hq + head;
-    const bool seen = row_sees(pos, a.window, w.k0, w.k1);
+    const AttnArgs z = late_args();
+    const int64_t row = (int64_t)(w.first + tok) * z.Hq + head;
+    const bool seen = row_sees(pos, z.window, w.k0, w.k1);
     const float inv = parts == 1 ? row_inverse(l, seen) : 1.f;
-    const int64_t part = row * a.splits + w.part;
-    E* out = static_cast<E*>(a.out.p) + ((int64_t)(w.first + tok) * a.out.st + head * a.out.sh);
+    const int64_t part = row * z.splits + w.part;
+    E* out = static_cast<E*>(z.out.p) + ((int64_t)(w.first + tok) * z.out.st + head * z.out.sh);
 #pragma unroll
     for (int i = 0; i < DT; ++i)
 #pragma unroll
@@ -650,12 +689,12 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
             const int d = 32 * i + 8 * q + 4 * half;
             const float v[4] = {o[i][4 * q] * inv, o[i][4 * q + 1] * inv, o[i][4 * q + 2] * inv, o[i][4 * q + 3] * inv};
             if (parts == 1) store4(out + d, v);
-            else store4(a.part_o + part * D + d, v);
+            else store4(z.part_o + part * D + d, v);
         }
     if (half != 0) return;
-    if (parts > 1) a.part_ml[part] = make_float2(m, l == 0.f && seen ? -1.f : l);
-    else if (a.lse) a.lse[row] = row_lse(m, l, seen);
-    if (a.splits > 1 && w.part == 0) a.parts[row] = parts;
+    if (parts > 1) z.part_ml[part] = make_float2(m, l == 0.f && seen ? -1.f : l);
+    else if (z.lse) z.lse[row] = row_lse(m, l, seen);
+    if (z.splits > 1 && w.part == 0) z.parts[row] = parts;
 }
 
 // SHARED: in equal shares (share_work), else a workgroup for each row tile, head and range
@@ -702,10 +741,10 @@ hipError_t launch(const Attn4Args& a, const AttnPlan& plan, hipStream_t s) {
     constexpr bool wide = sizeof(E) == 4;
     hipError_t e = hipSuccess;
     if (plan.few) {
-        k_attend4_few<E, wide ? 5 : 3, wide ? 5 : 3, D><<<dim3((unsigned)plan.blocks), 256, 0, s>>>(a);
+        k_attend4_few<E, wide ? 5 : 4, wide ? 5 : 3, D><<<dim3((unsigned)plan.blocks), 256, 0, s>>>(a);
         e = hipGetLastError();
     } else {
-        e = launch_rows<E, wide ? 5 : 3, wide ? 5 : 2, D>(a, plan, s);
+        e = launch_rows<E, wide ? 5 : 4, wide ? 5 : 2, D>(a, plan, s);
     }
     return e != hipSuccess ? e : launch_join<E, D>(a.a, plan, s);
 }
