@@ -81,7 +81,7 @@ size_t cache4_attention_workspace_size(const sffn_kv_cache4_t* cache, const sffn
     if (check_dtype(as_int(dtype)) != SFFN_OK || check_attention(cache, batch, n_q_heads, window, T) != SFFN_OK) return 0;
     if (T == 0 || batch->n_seqs == 0 || batch->max_new == 0) return 0;
     AttnPlan plan;
-    if (make_plan(cache_shape(cache, batch, as_int(dtype), T), n_q_heads, window, attn4_plan, &plan) != SFFN_OK) return 0;
+    if (make_plan(cache_shape(cache, batch, as_int(dtype), T), n_q_heads, window, attn4_plan, &plan, kUnitCost4) != SFFN_OK) return 0;
     return plan.ws_bytes;
 }
 
@@ -100,7 +100,7 @@ sffn_status_t cache4_attention(const sffn_kv_cache4_t* cache, const sffn_kv_batc
     if (reinterpret_cast<uintptr_t>(lse) % 4 != 0) return fail(SFFN_ERR_INVALID_ARG, "lse must be 4-byte aligned");
     const CacheArgs a = cache_shape(cache, batch, dt, T);
     AttnPlan plan;
-    SFFN_TRY(make_plan(a, n_q_heads, window, attn4_plan, &plan));
+    SFFN_TRY(make_plan(a, n_q_heads, window, attn4_plan, &plan, kUnitCost4));
     SFFN_TRY(check_workspace(workspace, ws_bytes, plan.ws_bytes));
     return hip_status(launch_cache4_attention(a, cache4(cache), plan, view(q), n_q_heads, scale, window, view(out), lse,
                                               workspace, static_cast<hipStream_t>(hip_stream)),

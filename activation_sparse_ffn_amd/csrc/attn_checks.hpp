@@ -147,12 +147,13 @@ sffn_status_t check_attention(const Cache* cache, const sffn_kv_batch_t* batch, 
 }
 
 inline sffn_status_t make_plan(const CacheArgs& a, int32_t n_q_heads, int32_t window,
-                               AttnPlan (*plan_of)(const CacheArgs&, int, int), AttnPlan* plan) {
+                               AttnPlan (*plan_of)(const CacheArgs&, int, int), AttnPlan* plan,
+                               int unit_cost = 0) {
     const int64_t tiles = ((int64_t)a.max_new * (n_q_heads / a.Hkv) + 15) / 16;
     if (tiles > kMaxGrid || (int64_t)a.B * a.Hkv > kMaxGrid / (tiles > 0 ? tiles : 1))
         return fail(SFFN_ERR_UNSUPPORTED, "the batch is too large for one call");
     // the kernels' counts of steps of 64 keys over all sequences and heads
-    const int64_t steps = (int64_t)a.max_pages * a.P / 64 + 8;
+    const int64_t steps = (int64_t)a.max_pages * a.P / 64 + 8 + unit_cost;
     if ((int64_t)a.B * a.Hkv > kMaxGrid / steps)
         return fail(SFFN_ERR_UNSUPPORTED, "%d sequences of %d pages are too many for one call", a.B, a.max_pages);
     *plan = plan_of(a, n_q_heads, window);

@@ -195,11 +195,16 @@ hipError_t launch_cache4_append(const CacheArgs& c, const Cache4& b, const int64
                                 const Heads& v, hipStream_t s);
 hipError_t launch_cache4_read(const CacheArgs& c, const Cache4& b, const Heads& k, const Heads& v, hipStream_t s);
 
+// What beginning and ending a unit of work costs the few-row kernel, in steps of 64 keys (see
+// share_work).
+constexpr int kUnitCost4 = 16;
 inline AttnPlan attn4_plan(const CacheArgs& c, int Hq, int window) {
     AttnPlan p{};
-    p.few = (int64_t)c.max_new * (Hq / c.Hkv) <= 16;
+    const int64_t most = (int64_t)c.max_new * (Hq / c.Hkv);
+    p.few = most <= 16;
+    p.pair = !p.few && most <= 32 && c.D <= 128;
     p.waves = 4;
-    return cut_up(c, Hq, window, p, few_held(c.D, c.dt == Dt::F32));
+    return cut_up(c, Hq, window, p, p.few || p.pair ? 1 : few_held(c.D, c.dt == Dt::F32));
 }
 hipError_t launch_cache4_attention(const CacheArgs& c, const Cache4& b, const AttnPlan& plan, const Heads& q, int Hq,
                                    float scale, int window, const Heads& out, float* lse, void* ws, hipStream_t s);

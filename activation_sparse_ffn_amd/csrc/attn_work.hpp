@@ -184,7 +184,12 @@ __device__ __forceinline__ int wave_scan(int v, Op op) {
 // called by one workgroup for each sequence with tokens that are not computed.
 constexpr int kLeast = 8;
 
-template <typename F, typename L>
+// EXTRA, ROUND: of kernels that hold one workgroup a compute unit, whose beginnings and ends
+// therefore hide behind no other's work. A unit then costs EXTRA more than its steps; where
+// every unit can begin a share of its own, shares are multiples of ROUND steps (what a
+// workgroup takes at a time) and long enough for that if there are twice as many workgroups
+// as units.
+template <int EXTRA = 0, int ROUND = 1, typename F, typename L>
 __device__ __forceinline__ void share_work(const AttnArgs& a, int tile_rows, F work, L lost) {
     const int lane = threadIdx.x & 63;
     const int B = a.c.B, Hkv = a.c.Hkv;
@@ -198,7 +203,7 @@ __device__ __forceinline__ void share_work(const AttnArgs& a, int tile_rows, F w
     int round_to = 0;           // 0: costs as they are, else rounded up to multiples of it
     auto padded = [&](int steps) {
         if (round_to > 0) return (steps + round_to - 1) / round_to * round_to;
-        return steps > kLeast ? steps : kLeast;
+        return (steps > kLeast ? steps : kLeast) + EXTRA;
     };
     auto add = [](int p, int q) { return p + q; };
     auto sum_costs = [&](Lane& y) { y.cost = wave_scan(padded(y.steps) * y.units, add); };
@@ -247,13 +252,30 @@ __device__ __forceinline__ void share_work(const AttnArgs& a, int tile_rows, F w
     if (share < kLeast) share = kLeast;
     // no more parts than the workspace has room for
     if (a.splits > 1 && share < longest / (a.splits - 1) + 1) share = longest / (a.splits - 1) + 1;
-    if (B <= 64 && lane_value(wave_scan(x.units, add), 63) <= (int)gridDim.x && total < 1 << 29) {
-        round_to = share;
-        const int unrounded = x.cost;
-        sum_costs(x);
-        const int rounded = lane_value(x.cost, 63);
+    const int units_of_all = B <= 64 ? lane_value(wave_scan(x.units, add), 63) : 0;
+    if (B <= 64 && units_of_all <= (int)gridDim.x && total < 1 << 29) {
+        const int unrounded = x.cost, shared = share;
+        auto round_up = [&](int to) {
+            round_to = share = to;
+            sum_costs(x);
+            return lane_value(x.cost, 63);
+        };
+        int rounded;
+        if constexpr (EXTRA == 0) {
+            rounded = round_up(share);
+        } else {
+            const int alone = total - EXTRA * units_of_all, grid = (int)gridDim.x;
+            auto whole = [&](int n) {
+                int to = ((alone + n - 1) / n + ROUND - 1) / ROUND * ROUND;
+                if (a.splits > 1 && to < longest / (a.splits - 1) + 1) to = longest / (a.splits - 1) + 1;
+                return to;
+            };
+            rounded = round_up(whole(grid));
+            if (rounded / share > grid && 2 * units_of_all <= grid) rounded = round_up(whole(grid - units_of_all));
+        }
         if (rounded / share > (int)gridDim.x) {
             round_to = 0;
+            share = shared;
             x.cost = unrounded;
         } else {
             total = rounded;

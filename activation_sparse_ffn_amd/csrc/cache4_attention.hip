@@ -106,49 +106,59 @@ __device__ __forceinline__ void split(f32x16 lo, f32x16 hi, int e, u32x6* out) {
     }
 }
 
-// 32 consecutive channels of a row of q times `by`, as NP pieces, and their unit's exponent.
-template <typename E, int NP>
-__device__ __forceinline__ int split_q(const E* p, bool valid, float by, u32x6* out) {
-    float x[32];
+// 32 consecutive channels of a row of q, as they lie.
+template <typename E>
+struct QBlock {
+    Raw<E> x[4];
+    bool valid;
+    __device__ __forceinline__ void load(const E* p, bool row) {
+        valid = row;
+        if (row)
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[i + j] = 0.f;
-        if (valid) Elem<E>::load8(p + i, x + i);
+            for (int i = 0; i < 4; ++i) x[i].load(p + 8 * i);
     }
-    uint32_t top = 0;
+    // times `by`, as NP pieces: their units' exponent
+    template <int NP>
+    __device__ __forceinline__ int split_into(float by, u32x6* out) const {
+        float v[32];
+        uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        x[i] *= by;
-        top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-    }
-    const int e = unit_of<NP>(top);
-    f32x16 lo, hi;
+        for (int i = 0; i < 4; ++i) {
+            x[i].decode(v + 8 * i);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        lo[i] = x[2 * i];
-        hi[i] = x[2 * i + 1];
+            for (int j = 8 * i; j < 8 * i + 8; ++j) {
+                v[j] = valid ? v[j] * by : 0.f;
+                top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+            }
+        }
+        const int e = unit_of<NP>(top);
+        f32x16 lo, hi;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            lo[i] = v[2 * i];
+            hi[i] = v[2 * i + 1];
+        }
+        split<NP>(lo, hi, e, out);
+        return e;
     }
-    split<NP>(lo, hi, e, out);
-    return e;
-}
+};
 
 // ---- products -------------------------------------------------------------------
 
 __device__ __forceinline__ i32x8 operand(const u32x6& v) {
     return (i32x8)__builtin_shufflevector(v, v, 0, 1, 2, 3, 4, 5, -1, -1);
 }
-__device__ __forceinline__ i32x8 operand(const uint4& v) {
-    return i32x8{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+__device__ __forceinline__ i32x8 operand(const u32x4& v) {
+    return (i32x8)__builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
 }
 
 // c + entries a (4 bits, unit: byte UA of ua) times pieces b (6 bits, byte UB of ub).
 template <int UA, int UB>
-__device__ __forceinline__ f32x4 product(const uint4& a, int ua, const u32x6& b, int ub, f32x4 c) {
+__device__ __forceinline__ f32x4 product(const u32x4& a, int ua, const u32x6& b, int ub, f32x4 c) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(a), operand(b), c, 4, 2, UA, ua, UB, ub);
 }
 template <int UA, int UB>
-__device__ __forceinline__ f32x16 product(const uint4& a, int ua, const u32x6& b, int ub, f32x16 c) {
+__device__ __forceinline__ f32x16 product(const u32x4& a, int ua, const u32x6& b, int ub, f32x16 c) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(a), operand(b), c, 4, 2, UA, ua, UB, ub);
 }
 constexpr int kOne = 0x7f7f7f7f;        // unit 1
@@ -158,7 +168,9 @@ constexpr int kOne = 0x7f7f7f7f;        // unit 1
 __device__ __forceinline__ i32x2 transposed(const char* p) {
     return __builtin_amdgcn_ds_read_tr4_b64_v2i32((__attribute__((address_space(3))) i32x2*)p);
 }
-__device__ __forceinline__ uint4 joined(i32x2 a, i32x2 b) { return make_uint4(a[0], a[1], b[0], b[1]); }
+__device__ __forceinline__ u32x4 joined(i32x2 a, i32x2 b) {
+    return u32x4{(uint32_t)a[0], (uint32_t)a[1], (uint32_t)b[0], (uint32_t)b[1]};
+}
 
 // ---- softmax of a lane's 32 scores -------------------------------------------------
 
@@ -169,7 +181,7 @@ __device__ __forceinline__ uint4 joined(i32x2 a, i32x2 b) { return make_uint4(a[
 template <typename F>
 __device__ __forceinline__ void follow(float top, float& m, float& l, float (&x)[32], F scale_output) {
     const bool unset = m == neg_inf();
-    if (__any(unset ? top > neg_inf() : top > kSlack)) {
+    if (__builtin_expect(__any(unset ? top > neg_inf() : top > kSlack) != 0, false)) {
         const float by = unset ? (top > neg_inf() ? top : 0.f) : fmaxf(top, 0.f);
         const float alpha = unset ? 1.f : __builtin_amdgcn_exp2f(-by);
         if (unset) m = top > neg_inf() ? top : m;
@@ -196,7 +208,7 @@ __device__ __forceinline__ int weights(const float (&x)[32], float& l, SV sv, bo
         else hi[i - 16] = p * sv(i);
     }
     l += sum;
-    if (masked) {
+    if (__builtin_expect(masked, false)) {
         // what is stored behind a hidden key may be anything
 #pragma unroll
         for (int i = 0; i < 32; ++i)
@@ -219,7 +231,7 @@ __device__ __forceinline__ uint64_t page_row(const CacheArgs& c, uint32_t page, 
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (up to 16 a sequence and key head): four waves take the work's steps of 128
+// Few rows (a tile of 16 a sequence and key head, or two): four waves take the work's steps of 128
 // keys in turn, each with its own running softmax; they meet in LDS at the end.
 //
 // v_mfma_scale_f32_16x16x128_f8f6f4: lane l holds operand row (A) or column (B) l % 16,
@@ -242,9 +254,9 @@ struct FewLds {
     uint8_t k_exp[kStep * (D / 32)];
 };
 
-template <typename E, int NP, int PP, int D>
+template <typename E, int NP, int PP, int D, int RT>
 __device__ __forceinline__ void attend4_few(const Attn4Args& args, const Work& w, int parts, FewLds<D>& lds,
-                                            float (*sm)[16], float (*sl)[16], float (*so)[16][D + 4]) {
+                                            float (*sm)[16 * RT], float (*sl)[16 * RT], float (*so)[16 * RT][D + 4]) {
     const AttnArgs& a = args.a;
     const CacheArgs& c = a.c;
     const Cache4& cache = args.b;
@@ -256,196 +268,226 @@ __device__ __forceinline__ void attend4_few(const Attn4Args& args, const Work& w
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int g = lane >> 4, n = lane & 15;
 
+    // Row n of each tile of q, the lane's 32 channels: asked for first, so that cutting them
+    // into pieces waits for nothing behind it.
+    QBlock<E> qx[RT][KC];
+    int pos[RT];
+    each<RT>([&](auto r) {
+        const int row = w.r0 + 16 * r + n;
+        const bool valid = row < w.rows;
+        const int tok = valid ? row / a.G : 0;
+        const int head = w.h * a.G + (valid ? row - tok * a.G : 0);
+        const E* q = static_cast<const E*>(a.q.p) + ((int64_t)(w.first + tok) * a.q.st + head * a.q.sh);
+        each<KC>([&](auto cc) { qx[r][cc].load(q + 128 * cc + 32 * (D == 64 ? g & 1 : g), valid); });
+        pos[r] = w.p0 + tok;
+    });
+
+    // A lane looks up the pages of keys lane and 64 + lane of a step: their rows in the
+    // cache's arrays (safe to read in any case), of which every 16th is the first of a tile
+    // that lies in one page. Tiles behind the last key are loaded like the others.
     const int32_t* table = c.table + (int64_t)w.b * c.table_stride;
-    // entries of the pages of keys lane and 64 + lane of the step
-    auto load_entries = [&](int t0, uint32_t (&e)[2]) {
-        e[0] = page_entry(c, table, t0 + lane);
-        e[1] = page_entry(c, table, t0 + 64 + lane);
+    uint32_t entry[2];
+    uint64_t rows[2];
+    bool known[2];
+    auto load_entries = [&](int t0) {
+        entry[0] = page_entry(c, table, t0 + lane);
+        entry[1] = page_entry(c, table, t0 + 64 + lane);
     };
-    // first row of tile t (16 keys) in the cache's arrays
-    auto tile_row = [&](const uint32_t (&e)[2], int t0, int t) {
-        const uint32_t page = page_in(c, (uint32_t)lane_value((int)e[t >> 2], 16 * (t & 3)));
-        return page_row(c, page, w.h) + ((t0 + 16 * t) & (c.P - 1));
-    };
-    const int k_off = n * RB + 16 * (D == 64 ? g & 1 : g);
-    uint4 kr[8][KC];
-    uint2 ke[2];
-    float vs[2];
-    auto load_keys = [&](const uint32_t (&e)[2], int t0) {
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-            if (t0 + 16 * t < w.k1) {
-                const uint8_t* p = cache.keys + tile_row(e, t0, t) * RB;
-#pragma unroll
-                for (int cc = 0; cc < KC; ++cc) kr[t][cc] = *reinterpret_cast<const uint4*>(p + k_off + 64 * cc);
-            }
+    auto find_rows = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int key = t0 + 64 * i + lane;
-            ke[i] = make_uint2(~0u, ~0u);
-            vs[i] = __builtin_nanf("");
-            if (key < w.k1 && known_page(c, e[i], key)) {
-                const uint64_t row = page_row(c, e[i], w.h) + (key & (c.P - 1));
-                const uint8_t* p = cache.k_exp + row * (D / 32);
-                if constexpr (D == 64) ke[i].x = *reinterpret_cast<const uint16_t*>(p);
-                else if constexpr (D == 128) ke[i].x = *reinterpret_cast<const uint32_t*>(p);
-                else ke[i] = *reinterpret_cast<const uint2*>(p);
-                vs[i] = fabsf(cache.v_scale[row]);
-            }
+            rows[i] = page_row(c, page_in(c, entry[i]), w.h) + (key & (c.P - 1));
+            known[i] = known_page(c, entry[i], key);
+        }
+    };
+    // byte of the first row of tile t
+    auto tile_at = [&](int t) {
+        const uint32_t lo = (uint32_t)lane_value((int)(uint32_t)rows[t >> 2], 16 * (t & 3));
+        const uint32_t hi = (uint32_t)lane_value((int)(uint32_t)(rows[t >> 2] >> 32), 16 * (t & 3));
+        return ((uint64_t)hi << 32 | lo) * RB;
+    };
+    const uint32_t k_off = n * RB + 16 * (D == 64 ? g & 1 : g);
+    u32x4 kr[8][KC];
+    uint2 ke[2];
+    float vs[2];
+    auto load_keys = [&]() {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            const uint8_t* p = cache.keys + tile_at(t);
+#pragma unroll
+            for (int cc = 0; cc < KC; ++cc) kr[t][cc] = *reinterpret_cast<const u32x4*>(p + k_off + 64 * cc);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint8_t* p = cache.k_exp + rows[i] * (D / 32);
+            if constexpr (D == 64) ke[i].x = *reinterpret_cast<const uint16_t*>(p);
+            else if constexpr (D == 128) ke[i].x = *reinterpret_cast<const uint32_t*>(p);
+            else ke[i] = *reinterpret_cast<const uint2*>(p);
+            vs[i] = cache.v_scale[rows[i]];
         }
     };
     // piece i of the lane's share of the values: its tile, its row there and the place of
     // that in LDS
-    auto value_tile = [&](int i) { return D == 64 ? 2 * i + (lane >> 5) : D == 128 ? i : i >> 1; };
     const int v_row = D == 64 ? (lane & 31) >> 1 : D == 128 ? lane >> 2 : lane >> 3;
-    const int v_off = v_row * RB + lane % (D / 32) * 16;
+    const uint32_t v_off = v_row * RB + lane % (D / 32) * 16;
     auto value_place = [&](int i) {
-        const int t = value_tile(i), r = D == 256 ? v_row + 8 * (i & 1) : v_row;
+        const int t = D == 64 ? 2 * i + (lane >> 5) : D == 128 ? i : i >> 1, r = D == 256 ? v_row + 8 * (i & 1) : v_row;
         return ((r >> 2) * 32 + 2 * (r & 3) + 8 * (t & 3) + (t >> 2)) * FewLds<D>::pitch + lane % (D / 32) * 16;
     };
-
-    uint32_t now[2], next[2];
-    int t0 = w.k0 + kStep * wave;
-    load_entries(t0, now);
-    if (t0 < w.k1) load_keys(now, t0);
-    load_entries(t0 + 4 * kStep, next);
-
-    // q: the row n of the tile, the lane's 32 channels
-    u32x6 qf[KC][NM];
-    int qu[KC][2];
-    const int row = w.r0 + n;
-    const bool valid = row < w.rows;
-    const int tok = valid ? row / a.G : 0;
-    {
-        const int head = w.h * a.G + (valid ? row - tok * a.G : 0);
-        const E* q = static_cast<const E*>(a.q.p) + ((int64_t)(w.first + tok) * a.q.st + head * a.q.sh);
-        const float by = a.negate ? -a.scale2 : a.scale2;
-#pragma unroll
-        for (int cc = 0; cc < KC; ++cc) {
-            u32x6 p[NP + 1];
-            const int e = split_q<E, NP>(q + 128 * cc + 32 * (D == 64 ? g & 1 : g), valid, by, p);
-            units<NP>(e, qu[cc]);
+    u32x4 vr[VL];
+    auto load_values = [&]() {
+        each<VL>([&](auto i) {
+            uint64_t p = tile_at(D == 64 ? 2 * i : D == 128 ? i : i / 2) + (D == 256 ? i % 2 * 8 * RB : 0);
             if constexpr (D == 64) {
-                p[NP] = u32x6{0, 0, 0, 0, 0, 0};
+                const uint64_t second = tile_at(2 * i + 1);
+                p = lane < 32 ? p : second;
+            }
+            vr[i] = *reinterpret_cast<const u32x4*>(cache.values + p + v_off);
+        });
+    };
+
+    int t0 = w.k0 + kStep * wave;
+    load_entries(t0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (t0 < w.k1) {
+        find_rows(t0);
+        load_keys();
+        load_values();
+        load_entries(t0 + 4 * kStep);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+
+    u32x6 qf[RT][KC][NM];
+    int qu[RT][KC][2];
+    const float by = a.negate ? -a.scale2 : a.scale2;
+    each<RT>([&](auto r) {
+        each<KC>([&](auto cc) {
+            if constexpr (D == 64) {
+                u32x6 p[NP];
+                const int e = qx[r][cc].template split_into<NP>(by, p);
                 uint32_t u = 0;
+                each<NM>([&](auto i) {
+                    constexpr int first = 2 * i, second = 2 * i + 1;
 #pragma unroll
-                for (int i = 0; i < NM; ++i) {
-                    qf[cc][i] = g >> 1 ? p[2 * i + 1] : p[2 * i];
-                    // (a row that is not finite has the unit NaN in its first piece at least)
+                    for (int j = 0; j < 6; ++j) {
+                        if constexpr (second < NP) qf[r][cc][i][j] = g >> 1 ? p[second][j] : p[first][j];
+                        else qf[r][cc][i][j] = g >> 1 ? 0 : p[first][j];
+                    }
                     const int at = 2 * i + (g >> 1);
                     u |= (uint32_t)(e == 255 ? 255 : at < NP ? e - 4 * at : 127) << (8 * i);
-                }
-                qu[cc][0] = (int)u;
+                });
+                qu[r][cc][0] = (int)u;
+                qu[r][cc][1] = 0;
             } else {
-#pragma unroll
-                for (int i = 0; i < NM; ++i) qf[cc][i] = p[i];
+                const int e = qx[r][cc].template split_into<NP>(by, qf[r][cc]);
+                units<NP>(e, qu[r][cc]);
             }
-        }
-    }
-    const int pos = w.p0 + tok;
+        });
+    });
     const int p_first = w.p0 + w.r0 / a.G;
-    const int p_last = w.p0 + ((w.rows - w.r0 < 16 ? w.rows : w.r0 + 16) - 1) / a.G;
-    f32x4 o[1][DT];
+    const int p_last = w.p0 + ((w.rows - w.r0 < 16 * RT ? w.rows : w.r0 + 16 * RT) - 1) / a.G;
+    f32x4 o[RT][DT];
+    float m[RT], l[RT];
+    each<RT>([&](auto r) {
 #pragma unroll
-    for (int i = 0; i < DT; ++i) o[0][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float m[1] = {neg_inf()}, l[1] = {0.f};
+        for (int i = 0; i < DT; ++i) o[r][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        m[r] = neg_inf();
+        l[r] = 0.f;
+    });
 
     for (; t0 < w.k1; t0 += 4 * kStep) {
-        // scales to LDS, values of this step into flight
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             uint8_t* p = lds.k_exp + (64 * i + lane) * (D / 32);
-            if constexpr (D == 64) *reinterpret_cast<uint16_t*>(p) = (uint16_t)ke[i].x;
-            else if constexpr (D == 128) *reinterpret_cast<uint32_t*>(p) = ke[i].x;
-            else *reinterpret_cast<uint2*>(p) = ke[i];
-            lds.v_scale[64 * i + lane] = vs[i];
-        }
-        uint4 vr[VL];
-#pragma unroll
-        for (int i = 0; i < VL; ++i) {
-            vr[i] = make_uint4(0, 0, 0, 0);
-            if constexpr (D == 64) {
-                const uint64_t r0 = tile_row(now, t0, 2 * i), r1 = tile_row(now, t0, 2 * i + 1);
-                if (t0 + 16 * value_tile(i) < w.k1)
-                    vr[i] = *reinterpret_cast<const uint4*>(cache.values + (lane < 32 ? r0 : r1) * RB + v_off);
-            } else if (t0 + 16 * value_tile(i) < w.k1) {
-                const uint8_t* p = cache.values + tile_row(now, t0, value_tile(i)) * RB;
-                vr[i] = *reinterpret_cast<const uint4*>(p + v_off + (D == 256 ? (i & 1) * 8 * RB : 0));
-            }
+            if constexpr (D == 64) *reinterpret_cast<uint16_t*>(p) = (uint16_t)(known[i] ? ke[i].x : ~0u);
+            else if constexpr (D == 128) *reinterpret_cast<uint32_t*>(p) = known[i] ? ke[i].x : ~0u;
+            else *reinterpret_cast<uint2*>(p) = known[i] ? ke[i] : make_uint2(~0u, ~0u);
+            lds.v_scale[64 * i + lane] = known[i] ? fabsf(vs[i]) : __builtin_nanf("");
         }
 
-        f32x4 s[8];
-        const float ref = -reference(m[0]);
+        f32x4 s[RT][8];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            s[t] = f32x4{ref, ref, ref, ref};
-#pragma unroll
-            for (int cc = 0; cc < KC; ++cc) {
+        for (int t = 0; t < 8; ++t)
+            each<KC>([&](auto cc) {
                 const int ku = lds.k_exp[(16 * t + n) * (D / 32) + (D == 64 ? g & 1 : 4 * cc + g)];
-                each<NM>([&](auto i) { s[t] = product<0, i % 4>(kr[t][cc], ku, qf[cc][i], qu[cc][i / 4], s[t]); });
-            }
-        }
+                each<RT>([&](auto r) {
+                    if constexpr (cc == 0) {
+                        const float ref = -reference(m[r]);
+                        s[r][t] = f32x4{ref, ref, ref, ref};
+                    }
+                    each<NM>([&](auto i) {
+                        s[r][t] = product<0, i % 4>(kr[t][cc], ku, qf[r][cc][i], qu[r][cc][i / 4], s[r][t]);
+                    });
+                });
+            });
+        each<VL>([&](auto i) { *reinterpret_cast<u32x4*>(lds.values + value_place(i)) = vr[i]; });
         const int tn = t0 + 4 * kStep;
-        now[0] = next[0];
-        now[1] = next[1];
-        if (tn < w.k1) load_keys(now, tn);
-        load_entries(tn + 4 * kStep, next);
+        if (tn < w.k1) {
+            find_rows(tn);
+            load_keys();
+            load_values();
+            load_entries(tn + 4 * kStep);
+        }
 
-        float x[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = s[i >> 2][i & 3];
         // a key beyond the row's position or before its window has no weight, whatever is
         // stored there
         const bool masked =
             t0 + kStep - 1 > p_first || t0 + kStep > w.k1 || (a.window > 0 && t0 <= p_last - a.window);
-        int up = last_seen(pos, t0, w.k1) - 4 * g, dn = before_seen(pos, t0, a.window) - 4 * g;
-        auto hidden = [&](int i) {
-            const int key = 16 * (i >> 2) + (i & 3);
-            return key > up || key <= dn;
-        };
-        if (masked)
+        u32x6 pf[RT][PP];
+        int pu[RT][2];
+        each<RT>([&](auto r) {
+            float x[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (hidden(i)) x[i] = neg_inf();
-        float top = x[0];
+            for (int i = 0; i < 32; ++i) x[i] = s[r][i >> 2][i & 3];
+            int up = last_seen(pos[r], t0, w.k1) - 4 * g, dn = before_seen(pos[r], t0, a.window) - 4 * g;
+            auto hidden = [&](int i) {
+                const int key = 16 * (i >> 2) + (i & 3);
+                return key > up || key <= dn;
+            };
+            if (__builtin_expect(masked, false))
 #pragma unroll
-        for (int i = 1; i < 32; ++i) top = fmaxf(top, x[i]);
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = max_halves(top);
-        follow(top, m[0], l[0], x, [&](float by) {
+                for (int i = 0; i < 32; ++i)
+                    if (hidden(i)) x[i] = neg_inf();
+            float top = x[0];
 #pragma unroll
-            for (int i = 0; i < DT; ++i) o[0][i] *= by;
+            for (int i = 1; i < 32; ++i) top = fmaxf(top, x[i]);
+            top = fmaxf(top, __shfl_xor(top, 16, 64));
+            top = max_halves(top);
+            follow(top, m[r], l[r], x, [&](float by) {
+#pragma unroll
+                for (int i = 0; i < DT; ++i) o[r][i] *= by;
+            });
+            asm("" : "+v"(up), "+v"(dn));       // hidden() again: 32 masks kept until then are as many scalars spilled
+            float4 sv[8];
+#pragma unroll
+            for (int t = 0; t < 8; ++t) sv[t] = *reinterpret_cast<const float4*>(&lds.v_scale[16 * t + 4 * g]);
+            const int pe = weights<PP>(
+                x, l[r], [&](int i) { return (&sv[i >> 2].x)[i & 3]; }, masked, hidden, pf[r]);
+            units<PP>(pe, pu[r]);
         });
-        asm("" : "+v"(up), "+v"(dn));       // hidden() again: 32 masks kept until then are as many scalars spilled
-        u32x6 pf[PP];
-        float4 sv[8];
-#pragma unroll
-        for (int t = 0; t < 8; ++t) sv[t] = *reinterpret_cast<const float4*>(&lds.v_scale[16 * t + 4 * g]);
-        const int pe = weights<PP>(
-            x, l[0], [&](int i) { return (&sv[i >> 2].x)[i & 3]; }, masked, hidden, pf);
-        int pu[2];
-        units<PP>(pe, pu);
 
-#pragma unroll
-        for (int i = 0; i < VL; ++i) *reinterpret_cast<uint4*>(lds.values + value_place(i)) = vr[i];
         const char* at = lds.values + (32 * g + n) * FewLds<D>::pitch;
-#pragma unroll
-        for (int i = 0; i < DT; ++i) {
-            const uint4 v = joined(transposed(at + 8 * i), transposed(at + 16 * FewLds<D>::pitch + 8 * i));
-            each<PP>([&](auto p) { o[0][i] = product<0, p % 4>(v, kOne, pf[p], pu[p / 4], o[0][i]); });
-        }
+        each<DT>([&](auto i) {
+            const u32x4 v = joined(transposed(at + 8 * i), transposed(at + 16 * FewLds<D>::pitch + 8 * i));
+            each<RT>([&](auto r) {
+                each<PP>([&](auto p) { o[r][i] = product<0, p % 4>(v, kOne, pf[r][p], pu[r][p / 4], o[r][i]); });
+            });
+        });
     }
-    join_waves<E, D, 1>(late_args(), w, parts, m, l, o, sm, sl, so);
+    join_waves<E, D, RT>(late_args(), w, parts, m, l, o, sm, sl, so);
 }
 
-template <typename E, int NP, int PP, int D>
-__global__ __launch_bounds__(256, few_held(D, sizeof(E) == 4)) void k_attend4_few(const Attn4Args args) {
-    __shared__ float sm[4][16], sl[4][16];
-    __shared__ __align__(16) float so[4][16][D + 4];
+template <typename E, int NP, int PP, int D, int RT>
+__global__ __launch_bounds__(256, 1) void k_attend4_few(const Attn4Args args) {
+    __shared__ float sm[4][16 * RT], sl[4][16 * RT];
+    __shared__ __align__(16) float so[4][16 * RT][D + 4];
     __shared__ __align__(16) FewLds<D> lds[4];
-    share_work(
-        args.a, 16,
-        [&](const Work& w, int parts) { attend4_few<E, NP, PP, D>(args, w, parts, lds[threadIdx.x >> 6], sm, sl, so); },
+    share_work<kUnitCost4, 4 * kStep / kTile>(
+        args.a, 16 * RT,
+        [&](const Work& w, int parts) {
+            attend4_few<E, NP, PP, D, RT>(args, w, parts, lds[threadIdx.x >> 6], sm, sl, so);
+        },
         [&](int b) { lose_rows<E, D>(args.a, b, 0, args.a.Hq); });
 }
 
@@ -500,7 +542,7 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
         to_v[i] = (32 * (m >> 2 & 1) + 2 * (4 * (m >> 3) + (m & 3)) + (key >> 5)) * pitch + chunk;
     }
     uint32_t entry[2], entry_s = 0;
-    uint4 kr[CH], vr[CH];
+    u32x4 kr[CH], vr[CH];
     uint2 ke = make_uint2(0, 0);
     float vs = 0.f;
     auto load_entries = [&](int t0) {
@@ -517,15 +559,15 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
         if constexpr (D == 64) {
             const uint64_t b0 = at(entry[0], first_key), b1 = at(entry[1], first_key + 16);
             const uint64_t p = (lane < 32 ? b0 : b1) + off;
-            if (takes_keys) kr[0] = *reinterpret_cast<const uint4*>(cache.keys + p);
-            else vr[0] = *reinterpret_cast<const uint4*>(cache.values + p);
+            if (takes_keys) kr[0] = *reinterpret_cast<const u32x4*>(cache.keys + p);
+            else vr[0] = *reinterpret_cast<const u32x4*>(cache.values + p);
         } else {
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
                 const int key0 = first_key + 4 * PW * i;
                 const uint64_t b = at(entry[i], key0) + (key0 & 15) * RB;
-                kr[i] = *reinterpret_cast<const uint4*>(cache.keys + b + off);
-                vr[i] = *reinterpret_cast<const uint4*>(cache.values + b + off);
+                kr[i] = *reinterpret_cast<const u32x4*>(cache.keys + b + off);
+                vr[i] = *reinterpret_cast<const u32x4*>(cache.values + b + off);
             }
         }
         if (lane < 16) {
@@ -545,8 +587,8 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
     auto stage = [&](RowsLds<D>& to) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-            if (takes_keys) *reinterpret_cast<uint4*>(to.keys + to_k[i]) = kr[i];
-            if (takes_values) *reinterpret_cast<uint4*>(to.values + to_v[i]) = vr[i];
+            if (takes_keys) *reinterpret_cast<u32x4*>(to.keys + to_k[i]) = kr[i];
+            if (takes_values) *reinterpret_cast<u32x4*>(to.values + to_v[i]) = vr[i];
         }
         if (lane < 16) {
             const int key = 16 * wave + lane;
@@ -576,7 +618,9 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
         const float by = a.negate ? -a.scale2 : a.scale2;
 #pragma unroll
         for (int cc = 0; cc < KC; ++cc) {
-            const int e = split_q<E, NP>(q + 64 * cc + 32 * half, valid, by, qf[cc]);
+            QBlock<E> x;
+            x.load(q + 64 * cc + 32 * half, valid);
+            const int e = x.template split_into<NP>(by, qf[cc]);
             units<NP>(e, qu[cc]);
         }
     }
@@ -609,7 +653,7 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
 #pragma unroll
             for (int i = 0; i < (D == 256 ? 2 : 1); ++i) ku[i] >>= 8 * half;
             each<KC>([&](auto cc) {
-                const uint4 k = *reinterpret_cast<const uint4*>(from.keys + at * pitch + 32 * cc + 16 * half);
+                const u32x4 k = *reinterpret_cast<const u32x4*>(from.keys + at * pitch + 32 * cc + 16 * half);
                 each<NP>([&](auto i) {
                     s[tt] = product<2 * (cc % 2), i % 4>(k, (int)ku[cc / 2], qf[cc][i], qu[cc][i / 4], s[tt]);
                 });
@@ -625,7 +669,7 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
             const int k = 32 * (i >> 4) + 8 * (i >> 2 & 3) + (i & 3);
             return k > up || k <= dn;
         };
-        if (masked)
+        if (__builtin_expect(masked, false))
 #pragma unroll
             for (int i = 0; i < 32; ++i)
                 if (hidden(i)) x[i] = neg_inf();
@@ -653,7 +697,7 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
         const char* at = from.values + (32 * half + (lane & 15)) * pitch + 8 * (lane >> 4 & 1);
 #pragma unroll
         for (int i = 0; i < DT; ++i) {
-            const uint4 v = joined(transposed(at + 16 * i), transposed(at + 16 * pitch + 16 * i));
+            const u32x4 v = joined(transposed(at + 16 * i), transposed(at + 16 * pitch + 16 * i));
             each<PP>([&](auto p) { o[i] = product<0, p % 4>(v, kOne, pf[p], pu[p / 4], o[i]); });
         }
     };
@@ -741,7 +785,11 @@ hipError_t launch(const Attn4Args& a, const AttnPlan& plan, hipStream_t s) {
     constexpr bool wide = sizeof(E) == 4;
     hipError_t e = hipSuccess;
     if (plan.few) {
-        k_attend4_few<E, wide ? 5 : 4, wide ? 5 : 3, D><<<dim3((unsigned)plan.blocks), 256, 0, s>>>(a);
+        k_attend4_few<E, wide ? 5 : 4, wide ? 5 : 3, D, 1><<<dim3((unsigned)plan.blocks), 256, 0, s>>>(a);
+        e = hipGetLastError();
+    } else if (plan.pair) {
+        if constexpr (D <= 128)
+            k_attend4_few<E, wide ? 5 : 4, wide ? 5 : 3, D, 2><<<dim3((unsigned)plan.blocks), 256, 0, s>>>(a);
         e = hipGetLastError();
     } else {
         e = launch_rows<E, wide ? 5 : 4, wide ? 5 : 2, D>(a, plan, s);
