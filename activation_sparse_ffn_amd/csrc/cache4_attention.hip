@@ -176,33 +176,32 @@ __device__ __forceinline__ u32x4 joined(i32x2 a, i32x2 b) {
 
 // State of a row: the reference m (-inf before its first key), the lane's share of the sum.
 // Scores come relative to the reference (0 while there is none). `top` is the largest of
-// the row's in the step, over all its lanes. Moves the reference where scores pass it by
-// more than kSlack or there is none yet; `scale_output(factor)` follows.
+// the row's in the step, over all its lanes. Where scores pass the reference by more than
+// kSlack, or there is none yet, it moves: `move(by, factor)` takes `by` from the scores at
+// hand and multiplies the output by `factor`.
 template <typename F>
-__device__ __forceinline__ void follow(float top, float& m, float& l, float (&x)[32], F scale_output) {
+__device__ __forceinline__ void follow(float top, float& m, float& l, F move) {
     const bool unset = m == neg_inf();
     if (__builtin_expect(__any(unset ? top > neg_inf() : top > kSlack) != 0, false)) {
         const float by = unset ? (top > neg_inf() ? top : 0.f) : fmaxf(top, 0.f);
-        const float alpha = unset ? 1.f : __builtin_amdgcn_exp2f(-by);
+        const float factor = unset ? 1.f : __builtin_amdgcn_exp2f(-by);
         if (unset) m = top > neg_inf() ? top : m;
         else m += by;
-        l *= alpha;
-        scale_output(alpha);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] -= by;
+        l *= factor;
+        move(by, factor);
     }
 }
 __device__ __forceinline__ float reference(float m) { return m == neg_inf() ? 0.f : m; }
 
-// Weights of scores x and the pieces of weights times value scales sv(i); hidden(i) where
+// Weights of scores x(i) and the pieces of weights times value scales sv(i); hidden(i) where
 // `masked`. Returns the pieces' unit.
-template <int PP, typename SV, typename H>
-__device__ __forceinline__ int weights(const float (&x)[32], float& l, SV sv, bool masked, H hidden, u32x6* out) {
+template <int PP, typename X, typename SV, typename H>
+__device__ __forceinline__ int weights(X x, float& l, SV sv, bool masked, H hidden, u32x6* out) {
     f32x16 lo, hi;
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-        const float p = __builtin_amdgcn_exp2f(x[i]);
+        const float p = __builtin_amdgcn_exp2f(x(i));
         sum += p;
         if (i < 16) lo[i] = p * sv(i);
         else hi[i - 16] = p * sv(i);
@@ -437,9 +436,7 @@ __device__ __forceinline__ void attend4_few(const Attn4Args& args, const Work& w
         u32x6 pf[RT][PP];
         int pu[RT][2];
         each<RT>([&](auto r) {
-            float x[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = s[r][i >> 2][i & 3];
+            auto x = [&](int i) { return s[r][i >> 2][i & 3]; };
             int up = last_seen(pos[r], t0, w.k1) - 4 * g, dn = before_seen(pos[r], t0, a.window) - 4 * g;
             auto hidden = [&](int i) {
                 const int key = 16 * (i >> 2) + (i & 3);
@@ -448,15 +445,17 @@ __device__ __forceinline__ void attend4_few(const Attn4Args& args, const Work& w
             if (__builtin_expect(masked, false))
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    if (hidden(i)) x[i] = neg_inf();
-            float top = x[0];
+                    if (hidden(i)) s[r][i >> 2][i & 3] = neg_inf();
+            float top = x(0);
 #pragma unroll
-            for (int i = 1; i < 32; ++i) top = fmaxf(top, x[i]);
+            for (int i = 1; i < 32; ++i) top = fmaxf(top, x(i));
             top = fmaxf(top, __shfl_xor(top, 16, 64));
             top = max_halves(top);
-            follow(top, m[r], l[r], x, [&](float by) {
+            follow(top, m[r], l[r], [&](float by, float factor) {
 #pragma unroll
-                for (int i = 0; i < DT; ++i) o[r][i] *= by;
+                for (int t = 0; t < 8; ++t) s[r][t] -= by;
+#pragma unroll
+                for (int i = 0; i < DT; ++i) o[r][i] *= factor;
             });
             asm("" : "+v"(up), "+v"(dn));       // hidden() again: 32 masks kept until then are as many scalars spilled
             float4 sv[8];
@@ -504,7 +503,7 @@ __global__ __launch_bounds__(256, 1) void k_attend4_few(const Attn4Args args) {
 // ---------------------------------------------------------------------------
 template <int D>
 struct RowsLds {
-    static constexpr int pitch = D / 2 + 16;
+    static constexpr int pitch = D / 2 + 16;        // rows read together start in other banks
     char keys[kTile * pitch], values[kTile * pitch];
     float v_scale[kTile];
     uint8_t k_exp[kTile * (D / 32)];
@@ -515,7 +514,8 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
     const AttnArgs& a = args.a;
     const CacheArgs& c = a.c;
     const Cache4& cache = args.b;
-    constexpr int RB = D / 2, KC = D / 64, DT = D / 32, pitch = RowsLds<D>::pitch;
+    typedef RowsLds<D> Lds;
+    constexpr int RB = D / 2, KC = D / 64, DT = D / 32, pitch = Lds::pitch;
     constexpr int CH = D == 256 ? 2 : 1;            // 16-byte pieces a thread stages of keys, and of values
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
@@ -541,55 +541,56 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
         to_k[i] = key * pitch + chunk;
         to_v[i] = (32 * (m >> 2 & 1) + 2 * (4 * (m >> 3) + (m & 3)) + (key >> 5)) * pitch + chunk;
     }
-    uint32_t entry[2], entry_s = 0;
     u32x4 kr[CH], vr[CH];
     uint2 ke = make_uint2(0, 0);
     float vs = 0.f;
-    auto load_entries = [&](int t0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (i < (D == 128 ? 1 : 2)) entry[i] = page_entry(c, table, t0 + first_key + (D == 64 ? 16 : 4 * PW) * i);
-        entry_s = D == 128 ? entry[0] : page_entry(c, table, t0 + 16 * wave);
+    // page entries of what a wave loads of the step at t0
+    struct Entries {
+        uint32_t e[2], s;
     };
-    auto load = [&](int t0) {
-        // byte of the first of the 16 keys that key0 is one of
-        auto at = [&](uint32_t e, int key0) {
-            return (page_row(c, page_in(c, e), w.h) + ((t0 + (key0 & ~15)) & (c.P - 1))) * RB;
-        };
+    auto entries_of = [&](int t0) {
+        Entries x;
+        x.e[0] = page_entry(c, table, t0 + first_key);
+        x.e[1] = D == 128 ? 0 : page_entry(c, table, t0 + first_key + (D == 64 ? 16 : 4 * PW));
+        x.s = D == 128 ? x.e[0] : page_entry(c, table, t0 + 16 * wave);
+        return x;
+    };
+    // byte of the first of the 16 keys that key0 of the step at t0 is one of
+    auto byte_at = [&](uint32_t e, int t0, int key0) {
+        return (page_row(c, page_in(c, e), w.h) + ((t0 + (key0 & ~15)) & (c.P - 1))) * RB;
+    };
+    auto load = [&](const uint8_t* from, u32x4 (&to)[CH], const Entries& x, int t0) {
         if constexpr (D == 64) {
-            const uint64_t b0 = at(entry[0], first_key), b1 = at(entry[1], first_key + 16);
-            const uint64_t p = (lane < 32 ? b0 : b1) + off;
-            if (takes_keys) kr[0] = *reinterpret_cast<const u32x4*>(cache.keys + p);
-            else vr[0] = *reinterpret_cast<const u32x4*>(cache.values + p);
+            const uint64_t b0 = byte_at(x.e[0], t0, first_key), b1 = byte_at(x.e[1], t0, first_key + 16);
+            to[0] = *reinterpret_cast<const u32x4*>(from + (lane < 32 ? b0 : b1) + off);
         } else {
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
+            each<CH>([&](auto i) {
                 const int key0 = first_key + 4 * PW * i;
-                const uint64_t b = at(entry[i], key0) + (key0 & 15) * RB;
-                kr[i] = *reinterpret_cast<const u32x4*>(cache.keys + b + off);
-                vr[i] = *reinterpret_cast<const u32x4*>(cache.values + b + off);
-            }
+                to[i] = *reinterpret_cast<const u32x4*>(from + byte_at(x.e[i], t0, key0) + (key0 & 15) * RB + off);
+            });
         }
+    };
+    auto load_keys = [&](const Entries& x, int t0) {
+        if (takes_keys) load(cache.keys, kr, x, t0);
         if (lane < 16) {
             const int t = t0 + 16 * wave;
-            const uint64_t row = page_row(c, page_in(c, entry_s), w.h) + (t & (c.P - 1));
+            const uint64_t row = page_row(c, page_in(c, x.s), w.h) + (t & (c.P - 1));
             const uint8_t* p = cache.k_exp + row * (D / 32) + lane * (D / 32);
             if constexpr (D == 64) ke.x = *reinterpret_cast<const uint16_t*>(p);
             else if constexpr (D == 128) ke.x = *reinterpret_cast<const uint32_t*>(p);
             else ke = *reinterpret_cast<const uint2*>(p);
             vs = fabsf((cache.v_scale + row)[lane]);
-            if (!known_page(c, entry_s, t)) {
+            if (!known_page(c, x.s, t)) {
                 ke = make_uint2(~0u, ~0u);
                 vs = __builtin_nanf("");
             }
         }
     };
-    auto stage = [&](RowsLds<D>& to) {
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            if (takes_keys) *reinterpret_cast<u32x4*>(to.keys + to_k[i]) = kr[i];
-            if (takes_values) *reinterpret_cast<u32x4*>(to.values + to_v[i]) = vr[i];
-        }
+    auto load_values = [&](const Entries& x, int t0) {
+        if (takes_values) load(cache.values, vr, x, t0);
+    };
+    auto stage_keys = [&](Lds& to) {
+        if (takes_keys) each<CH>([&](auto i) { *reinterpret_cast<u32x4*>(to.keys + to_k[i]) = kr[i]; });
         if (lane < 16) {
             const int key = 16 * wave + lane;
             uint8_t* p = to.k_exp + key * (D / 32);
@@ -599,6 +600,10 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
             to.v_scale[key] = vs;
         }
     };
+    auto stage_values = [&](Lds& to) {
+        if (takes_values)
+            each<CH>([&](auto i) { *reinterpret_cast<u32x4*>(to.values + to_v[i]) = vr[i]; });
+    };
     // LDS written by this wave is visible after it; loads stay in flight
     auto step_end = [&]() {
         __builtin_amdgcn_sched_barrier(0);
@@ -606,23 +611,24 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
         __builtin_amdgcn_sched_barrier(0);
     };
 
+    Entries next{};                 // of the step that is loaded next
     if (w.k0 < w.k1) {
-        load_entries(w.k0);
-        load(w.k0);
-        load_entries(w.k0 + kTile);
+        next = entries_of(w.k0);
+        load_keys(next, w.k0);
+        load_values(next, w.k0);
+        next = entries_of(w.k0 + kTile);
     }
     u32x6 qf[KC][NP];
     int qu[KC][2];
     {
         const E* q = static_cast<const E*>(a.q.p) + ((int64_t)(w.first + tok) * a.q.st + head * a.q.sh);
         const float by = a.negate ? -a.scale2 : a.scale2;
-#pragma unroll
-        for (int cc = 0; cc < KC; ++cc) {
+        each<KC>([&](auto cc) {
             QBlock<E> x;
             x.load(q + 64 * cc + 32 * half, valid);
             const int e = x.template split_into<NP>(by, qf[cc]);
             units<NP>(e, qu[cc]);
-        }
+        });
     }
     // positions of this wave's rows
     const int w0 = w.r0 + 32 * wave, w1 = w.rows - w0 < 32 ? w.rows : w0 + 32;
@@ -637,11 +643,19 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
     f32x16 start;           // what scores begin from: minus the reference, as the products' third operand
 #pragma unroll
     for (int j = 0; j < 16; ++j) start[j] = 0.f;
+    u32x6 pf[PP];           // the step's weights: pieces and their units
+    int pu[2];
 
-    auto compute = [&](const RowsLds<D>& from, int t0) {
-        f32x16 s[2];
-#pragma unroll
-        for (int tt = 0; tt < 2; ++tt) {
+    auto add_values = [&](const Lds& from) {
+        const char* at = from.values + (32 * half + (lane & 15)) * pitch + 8 * (lane >> 4 & 1);
+        each<DT>([&](auto i) {
+            const u32x4 v = joined(transposed(at + 16 * i), transposed(at + 16 * pitch + 16 * i));
+            each<PP>([&](auto p) { o[i] = product<0, p % 4>(v, kOne, pf[p], pu[p / 4], o[i]); });
+        });
+    };
+    f32x16 s[2];
+    auto score = [&](const Lds& from) {
+        each<2>([&](auto tt) {
             s[tt] = start;
             const int at = 32 * tt + col;
             uint32_t ku[2];
@@ -658,10 +672,10 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
                     s[tt] = product<2 * (cc % 2), i % 4>(k, (int)ku[cc / 2], qf[cc][i], qu[cc][i / 4], s[tt]);
                 });
             });
-        }
-        float x[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = s[i >> 4][i & 15];
+        });
+    };
+    auto weigh = [&](const Lds& from, int t0) {
+        auto x = [&](int i) { return s[i >> 4][i & 15]; };
         const bool masked =
             t0 + kTile - 1 > p_first || t0 + kTile > w.k1 || (a.window > 0 && t0 <= p_last - a.window);
         int up = last_seen(pos, t0, w.k1) - 4 * half, dn = before_seen(pos, t0, a.window) - 4 * half;
@@ -672,49 +686,50 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
         if (__builtin_expect(masked, false))
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                if (hidden(i)) x[i] = neg_inf();
-        float top = x[0];
+                if (hidden(i)) s[i >> 4][i & 15] = neg_inf();
+        float top = x(0);
 #pragma unroll
-        for (int i = 1; i < 32; ++i) top = fmaxf(top, x[i]);
+        for (int i = 1; i < 32; ++i) top = fmaxf(top, x(i));
         top = max_halves(top);
-        follow(top, m, l, x, [&](float by) {
+        follow(top, m, l, [&](float by, float factor) {
 #pragma unroll
-            for (int i = 0; i < DT; ++i) o[i] *= by;
+            for (int tt = 0; tt < 2; ++tt) s[tt] -= by;
+#pragma unroll
+            for (int i = 0; i < DT; ++i) o[i] *= factor;
             const float ref = -reference(m);
 #pragma unroll
             for (int j = 0; j < 16; ++j) start[j] = ref;
         });
         asm("" : "+v"(up), "+v"(dn));       // hidden() again: 32 masks kept until then are as many scalars spilled
-        u32x6 pf[PP];
         float4 sv[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            sv[i] = *reinterpret_cast<const float4*>(&from.v_scale[32 * (i >> 2) + 8 * (i & 3) + 4 * half]);
+            sv[i] = *reinterpret_cast<const float4*>(from.v_scale + 4 * half + 32 * (i >> 2) + 8 * (i & 3));
         const int pe = weights<PP>(
             x, l, [&](int i) { return (&sv[i >> 2].x)[i & 3]; }, masked, hidden, pf);
-        int pu[2];
         units<PP>(pe, pu);
-        const char* at = from.values + (32 * half + (lane & 15)) * pitch + 8 * (lane >> 4 & 1);
-#pragma unroll
-        for (int i = 0; i < DT; ++i) {
-            const u32x4 v = joined(transposed(at + 16 * i), transposed(at + 16 * pitch + 16 * i));
-            each<PP>([&](auto p) { o[i] = product<0, p % 4>(v, kOne, pf[p], pu[p / 4], o[i]); });
-        }
     };
     if (w.k0 < w.k1) {
-        stage(lds[0]);
-        load(w.k0 + kTile);
-        load_entries(w.k0 + 2 * kTile);
+        stage_keys(lds[0]);
+        stage_values(lds[0]);
+        load_keys(next, w.k0 + kTile);
+        load_values(next, w.k0 + kTile);
+        next = entries_of(w.k0 + 2 * kTile);
         step_end();
     }
     int buf = 0;
     for (int t0 = w.k0; t0 < w.k1; t0 += kTile, buf ^= 1) {
         // nothing to do for rows that see none of the tile's keys
-        if (w0 < w1 && t0 <= p_last && (a.window == 0 || (int64_t)t0 + kTile > (int64_t)p_first - a.window + 1))
-            compute(lds[buf], t0);
-        stage(lds[buf ^ 1]);
-        load(t0 + 2 * kTile);
-        load_entries(t0 + 3 * kTile);
+        if (w0 < w1 && t0 <= p_last && (a.window == 0 || (int64_t)t0 + kTile > (int64_t)p_first - a.window + 1)) {
+            score(lds[buf]);
+            weigh(lds[buf], t0);
+            add_values(lds[buf]);
+        }
+        stage_keys(lds[buf ^ 1]);
+        stage_values(lds[buf ^ 1]);
+        load_keys(next, t0 + 2 * kTile);
+        load_values(next, t0 + 2 * kTile);
+        next = entries_of(t0 + 3 * kTile);
         step_end();
     }
 
