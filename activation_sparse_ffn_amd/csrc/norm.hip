@@ -429,17 +429,24 @@ __global__ __launch_bounds__(1024) void k_norm_backward_long(const NormArgs a) {
     }
 }
 
-// Sums of the columns of `partial` in a fixed order: 16 threads a column, each with
-// every 16th row.
-constexpr int kSumCols = 64, kSumRows = 16;
+// Sums of the columns of `partial` in a fixed order: 32 threads a column, each with
+// every 32nd row.
+constexpr int kSumCols = 32, kSumRows = 32;
 __global__ __launch_bounds__(kSumCols* kSumRows) void k_norm_sum(const float* partial, int rows, int d, float* out) {
     __shared__ float lds[kSumRows][kSumCols];
     const int c = threadIdx.x % kSumCols, k = threadIdx.x / kSumCols;
     const int col = blockIdx.x * kSumCols + c;
     float v = 0.f;
+    constexpr int IN = 8;           // loads in flight
     if (col < d)
-#pragma unroll 4
-        for (int r = k; r < rows; r += kSumRows) v += partial[(int64_t)r * d + col];
+        for (int r = k; r < rows; r += IN * kSumRows) {
+            float x[IN];
+#pragma unroll
+            for (int i = 0; i < IN; ++i)
+                x[i] = r + i * kSumRows < rows ? partial[(int64_t)(r + i * kSumRows) * d + col] : 0.f;
+#pragma unroll
+            for (int i = 0; i < IN; ++i) v += x[i];
+        }
     lds[k][c] = v;
     __syncthreads();
     if (k != 0 || col >= d) return;

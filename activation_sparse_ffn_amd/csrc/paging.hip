@@ -12,8 +12,6 @@ namespace sffn {
 
 namespace {
 
-constexpr int kThreads = 1024;      // of the plan's workgroup: as many sequences at a time
-
 // Sums of lanes 0 .. l, in lane l.
 __device__ __forceinline__ int64_t wave_prefix(int64_t v) {
     const int lane = threadIdx.x & 63;
@@ -27,6 +25,7 @@ __device__ __forceinline__ int64_t wave_prefix(int64_t v) {
 
 // Inclusive sums over the workgroup's threads and their total. `lds` is read by nobody
 // after the next barrier.
+template <int NT>
 __device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t* lds, int64_t& total) {
     const int wave = threadIdx.x >> 6;
     v = wave_prefix(v);
@@ -35,7 +34,7 @@ __device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t* lds, int64_t
     int64_t before = 0;
     total = 0;
 #pragma unroll
-    for (int i = 0; i < kThreads / 64; ++i) {
+    for (int i = 0; i < NT / 64; ++i) {
         const int64_t q = lds[i];
         if (i < wave) before += q;
         total += q;
@@ -76,30 +75,32 @@ __device__ __forceinline__ Request request_of(const PlanArgs& a, int b) {
     return r;
 }
 
-// One workgroup; with_tokens: positions and slots too.
-__global__ __launch_bounds__(kThreads) void k_page_plan(const PlanArgs a, bool with_tokens) {
-    __shared__ int64_t sums[2][kThreads], scan[2][kThreads / 64];
-    __shared__ int2 places[kThreads];       // of each sequence: kept tokens, kept pages
+// One workgroup of NT threads, which takes as many sequences at a time; with_tokens:
+// positions and slots too.
+template <int NT>
+__global__ __launch_bounds__(NT) void k_page_plan(const PlanArgs a, bool with_tokens) {
+    __shared__ int64_t sums[2][NT], scan[2][NT / 64];
+    __shared__ int2 places[NT];       // of each sequence: kept tokens, kept pages
     const int tid = threadIdx.x;
     int64_t n_free = min((int64_t)max(a.n_free[0], 0), a.n_pages), total;
 
     if (a.keep) {
-        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        for (int b0 = 0; b0 < a.B; b0 += NT) {
             const Request r = request_of(a, b0 + tid);
             int64_t back;
-            const int64_t s = block_prefix(max(r.had - r.from, 0), scan[0], back);
+            const int64_t s = block_prefix<NT>(max(r.had - r.from, 0), scan[0], back);
             sums[0][tid] = s;
             places[tid].y = r.from;
             __syncthreads();
-            for (int64_t k0 = 0; k0 < back; k0 += kThreads) {
+            for (int64_t k0 = 0; k0 < back; k0 += NT) {
                 int32_t page = -1;
                 if (k0 + tid < back) {
-                    const int at = first_above(sums[0], kThreads, k0 + tid);
+                    const int at = first_above(sums[0], NT, k0 + tid);
                     const int64_t i = k0 + tid - (at > 0 ? sums[0][at - 1] : 0) + places[at].y;
                     page = a.table[(int64_t)(b0 + at) * a.table_stride + i];
                 }
                 const bool known = page >= 0 && page < a.n_pages;
-                const int64_t nth = n_free + block_prefix(known, scan[1], total) - 1;
+                const int64_t nth = n_free + block_prefix<NT>(known, scan[1], total) - 1;
                 if (known && nth < a.n_pages) a.free_pages[nth] = page;
                 n_free = min(n_free + total, a.n_pages);
                 __syncthreads();
@@ -110,12 +111,12 @@ __global__ __launch_bounds__(kThreads) void k_page_plan(const PlanArgs a, bool w
     }
 
     int64_t tokens = 0, taken = 0;          // before the sequences at hand
-    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    for (int b0 = 0; b0 < a.B; b0 += NT) {
         const int b = b0 + tid;
         const Request r = request_of(a, b);
         int64_t new_tokens, new_pages;
-        const int64_t s = block_prefix(r.fresh, scan[0], new_tokens);
-        const int64_t p = block_prefix(max(r.to - r.from, 0), scan[1], new_pages);
+        const int64_t s = block_prefix<NT>(r.fresh, scan[0], new_tokens);
+        const int64_t p = block_prefix<NT>(max(r.to - r.from, 0), scan[1], new_pages);
         sums[0][tid] = s;
         sums[1][tid] = p;
         places[tid] = make_int2(r.kept, r.from);
@@ -128,15 +129,15 @@ __global__ __launch_bounds__(kThreads) void k_page_plan(const PlanArgs a, bool w
         auto page_of = [&](int64_t k) {     // the k-th page that is taken
             return k < n_free ? a.free_pages[n_free - 1 - k] : -1;
         };
-        for (int64_t k = tid; k < new_pages; k += kThreads) {
-            const int at = first_above(sums[1], kThreads, k);
+        for (int64_t k = tid; k < new_pages; k += NT) {
+            const int at = first_above(sums[1], NT, k);
             const int64_t i = k - (at > 0 ? sums[1][at - 1] : 0) + places[at].y;
             a.table[(int64_t)(b0 + at) * a.table_stride + i] = page_of(taken + k);
         }
         if (with_tokens) {
             const int64_t left = a.T - tokens, n = left < new_tokens ? left : new_tokens;
-            for (int64_t t = tid; t < n; t += kThreads) {
-                const int at = first_above(sums[0], kThreads, t);
+            for (int64_t t = tid; t < n; t += NT) {
+                const int at = first_above(sums[0], NT, t);
                 const int2 place = places[at];
                 const int pos = place.x + (int)(t - (at > 0 ? sums[0][at - 1] : 0)), i = pos >> a.shift;
                 int32_t page = -1;
@@ -152,7 +153,7 @@ __global__ __launch_bounds__(kThreads) void k_page_plan(const PlanArgs a, bool w
         __syncthreads();
     }
     if (with_tokens)
-        for (int64_t t = tokens + tid; t < a.T; t += kThreads) {
+        for (int64_t t = tokens + tid; t < a.T; t += NT) {
             a.positions[t] = 0;
             a.slots[t] = -1;
         }
@@ -225,7 +226,9 @@ hipError_t launch_slots(const SlotArgs& a, hipStream_t s) {
 
 hipError_t launch_page_plan(const PlanArgs& a, hipStream_t s) {
     const bool with_tokens = a.T <= kTokensInPlan;
-    k_page_plan<<<dim3(1), kThreads, 0, s>>>(a, with_tokens);
+    // few sequences and tokens: fewer waves to start and to sum over
+    if (a.B <= 256 && a.T <= 1024) k_page_plan<256><<<dim3(1), 256, 0, s>>>(a, with_tokens);
+    else k_page_plan<1024><<<dim3(1), 1024, 0, s>>>(a, with_tokens);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || with_tokens) return e;
     SlotArgs q{};

@@ -88,10 +88,9 @@ def page_plan(block_table: torch.Tensor, kv_lens: torch.Tensor, new_lens: torch.
     if out is None:
         if total < 0:
             raise ValueError(f"total must not be negative (got {total})")
-        # one allocation: a call is bound by what the host does
+        # one allocation for what is int32: a call is bound by what the host does
         ints = _vector(2 * B + 3 + total, _I32, dev)
-        out = PagePlan(ints[:B], ints[B:2 * B + 1], ints[2 * B + 1:2 * B + 3], ints[2 * B + 3:],
-                       _vector(total, _I64, dev))
+        out = PagePlan(*ints.split_with_sizes((B, B + 1, 2, total)), _vector(total, _I64, dev))
         at = ints.data_ptr()
         to = (at, at + 8 * B + 4, at + 4 * B, at + 8 * B + 12, out.slots.data_ptr())
     else:
