@@ -1,12 +1,13 @@
 #!/usr/bin/env python3
 """One decoder layer on the package's operators: a prompt in chunks, then tokens
-one at a time, for several sequences that share a paged 8-bit cache.
+one at a time, for several sequences that share a paged cache of 8 or 4 bits.
 
-    python examples/decoder_layer.py [--seqs 4] [--prompt 300] [--chunk 128] [--tokens 8]
+    python examples/decoder_layer.py [--seqs 4] [--prompt 300] [--chunk 128] [--tokens 8] [--bits 8]
 
-Attention: norms of q and k for each head and rotary positions in one pass, append
-to the cache, attention over it. FFN: the predictor-gated sparse SwiGLU layer. The
-projections around them are plain matrix products. Weights and inputs are random:
+The norms take the residual sum with them. Attention: norms of q and k for each head and
+rotary positions in one pass, append to the cache, attention over it. FFN: the
+predictor-gated sparse SwiGLU layer. The projections around them are plain matrix
+products. Pages, positions and slots come from the GPU. Weights and inputs are random:
 the layer's shapes are what is shown, not a trained model.
 """
 from __future__ import annotations
@@ -20,11 +21,6 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import activation_sparse_ffn_amd as sffn  # noqa: E402
-
-
-def rms_norm(x, weight, eps=1e-6):
-    n = x.float()
-    return (n * torch.rsqrt(n.square().mean(-1, keepdim=True) + eps)).to(x.dtype) * weight
 
 
 class DecoderLayer:
@@ -49,8 +45,9 @@ class DecoderLayer:
         self.ffn = sffn.SparseFFN(weight(d_i, d), weight(d_i, d), weight(d, d_i), weight(rank, d), weight(d_i, rank))
 
     def attention(self, x, positions, cache, batch, window=0):
+        """x: the layer's input after its norm."""
         T = x.shape[0]
-        qkv = (rms_norm(x, self.norm1) @ self.w_qkv.t()).view(T, self.heads + 2 * self.kv_heads, self.head_dim)
+        qkv = (x @ self.w_qkv.t()).view(T, self.heads + 2 * self.kv_heads, self.head_dim)
         q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], 1)
         q, k = sffn.qk_norm_rope(q, k, positions, self.table, self.q_norm, self.k_norm)
         sffn.kv_cache_append(cache, batch, k, v)
@@ -60,46 +57,40 @@ class DecoderLayer:
     def __call__(self, x, positions, cache, batch, window=0):
         """x [T, d] of the batch's tokens at `positions`; their keys and values go
         into the cache."""
-        x = x + self.attention(x, positions, cache, batch, window)
-        return x + self.ffn(rms_norm(x, self.norm2))
+        y, _ = sffn.add_rms_norm(x, weight=self.norm1)
+        y, x = sffn.add_rms_norm(self.attention(y, positions, cache, batch, window), x, self.norm2)
+        return x + self.ffn(y)
 
 
 class Sequences:
-    """Block tables and lengths of sequences that grow together in one cache. Pages
-    are handed out as they are needed, in no order of the sequences."""
+    """Block tables and lengths of sequences that grow together in one cache. The pages are
+    handed out on the GPU as they are needed, here from a shuffled stack."""
 
-    def __init__(self, n, layer, pages_each, page=64):
-        self.n, self.page = n, page
-        self.cache = sffn.KVCache.empty(n * pages_each, layer.kv_heads, layer.head_dim, page)
-        self.table = torch.zeros(n, pages_each, dtype=torch.int32)
-        self.lens = [0] * n
-        self.used = [0] * n
-        self.free = torch.randperm(n * pages_each, generator=torch.Generator().manual_seed(1)).tolist()
+    def __init__(self, n, layer, pages_each, page=64, bits=8):
+        self.cache = (sffn.KVCache4 if bits == 4 else sffn.KVCache).empty(n * pages_each, layer.kv_heads,
+                                                                          layer.head_dim, page)
+        self.table = torch.full((n, pages_each), -1, dtype=torch.int32, device="cuda")
+        self.lens = torch.zeros(n, dtype=torch.int32, device="cuda")
+        self.free, self.n_free = sffn.free_pages(n * pages_each)
+        self.free = self.free[torch.randperm(n * pages_each, generator=torch.Generator().manual_seed(1)).cuda()]
+        self.longest = [0] * n
 
     def extend(self, new):
         """Room for new[b] tokens more in sequence b: their positions and the batch."""
-        positions = []
-        for b, m in enumerate(new):
-            positions += range(self.lens[b], self.lens[b] + m)
-            self.lens[b] += m
-            while self.used[b] * self.page < self.lens[b]:
-                self.table[b, self.used[b]] = self.free.pop()
-                self.used[b] += 1
-        cu = [0]
-        for m in new:
-            cu.append(cu[-1] + m)
-        i32 = dict(dtype=torch.int32, device="cuda")
-        batch = sffn.CacheBatch(self.table.cuda(), torch.tensor(self.lens, **i32), max(self.lens),
-                                torch.tensor(cu, **i32), max(new))
-        return torch.tensor(positions, **i32), batch
+        self.longest = [have + m for have, m in zip(self.longest, new)]
+        plan = sffn.page_plan(self.table, self.lens, torch.tensor(new, dtype=torch.int32, device="cuda"),
+                              self.free, self.n_free, self.cache.page, sum(new))
+        self.lens, self.n_free = plan.kv_lens, plan.n_free
+        return plan.positions, sffn.CacheBatch(self.table, plan.kv_lens, max(self.longest), plan.cu, max(new),
+                                               slots=plan.slots)
 
 
-def run(layer, prompts, tokens, chunk, window=0):
+def run(layer, prompts, tokens, chunk, window=0, bits=8):
     """Prompts (a [n_b, d] tensor for each sequence) in chunks, then `tokens` steps
     that feed each sequence its last output. Returns every sequence's outputs."""
     n = len(prompts)
     pages = -(-(max(p.shape[0] for p in prompts) + tokens) // 64)
-    seqs = Sequences(n, layer, pages)
+    seqs = Sequences(n, layer, pages, bits=bits)
     outs = [[] for _ in range(n)]
 
     def step(xs):
@@ -123,19 +114,20 @@ def main():
     ap.add_argument("--prompt", type=int, default=300)
     ap.add_argument("--chunk", type=int, default=128)
     ap.add_argument("--tokens", type=int, default=8)
+    ap.add_argument("--bits", type=int, default=8, choices=(4, 8), help="bits of a cached channel")
     a = ap.parse_args()
     layer = DecoderLayer()
     g = torch.Generator(device="cuda")
     g.manual_seed(3)
     prompts = [torch.randn(max(1, a.prompt - 37 * b), layer.d, generator=g, device="cuda").bfloat16()
                for b in range(a.seqs)]
-    run(layer, prompts, 1, a.chunk)
+    run(layer, prompts, 1, a.chunk, bits=a.bits)
     torch.cuda.synchronize()
     t = time.perf_counter()
-    outs = run(layer, prompts, a.tokens, a.chunk)
+    outs = run(layer, prompts, a.tokens, a.chunk, bits=a.bits)
     torch.cuda.synchronize()
     total = sum(o.shape[0] for o in outs)
-    print(f"{a.seqs} sequences, {total} tokens through the layer in {(time.perf_counter() - t) * 1e3:.2f} ms; "
+    print(f"{a.seqs} sequences, {a.bits}-bit cache, {total} tokens through the layer in {(time.perf_counter() - t) * 1e3:.2f} ms; "
           f"last outputs' mean square {[round(o[-1].float().square().mean().item(), 3) for o in outs]}")
 
 

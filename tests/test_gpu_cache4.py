@@ -3,15 +3,18 @@
 
 Exponents, scales and entries are integer or IEEE fp32 arithmetic: equal bit for bit (signs
 of zeros aside, which stand for the same). Attention, with w, W, a, b of the row as the
-reference gives them: q is cut to 2^-13.9 (bf16) or 2^-21.9 (fp32) of the largest of its 32
-channels, so a score is off by 2^-13.9 b (2^-21.9 b) and by fp32's roundings, 2^-19 a; a
-weight and the sum each by that much of itself, twice that in their quotient. Weights are cut
-to 2^-13.9 of the largest of 32 that lie within 127 keys of each other (2^-8.9 in sequences of
-more than 128 rows, 2^-21.9 for fp32). The result is rounded by half a step; fp32 sums add
-2^-16 of w over these lengths.
+reference gives them: q is cut to 2^-17.9 (bf16, four pieces) or 2^-21.9 (fp32,
+five) of the largest of its 32 channels, so a score is off by that times b and by fp32's
+roundings, 2^-19 a; a weight and the sum each by that much of itself, twice that in their
+quotient. Weights are cut to 2^-13.9 (three pieces; 2^-21.9 for fp32, five) of the largest of
+32 that lie within 127 keys of each other, to 2^-7.9 in sequences of more than 128 rows: the
+first of two pieces, whose largest lies in (3.75, 7.5] units and whose steps there are 1 / 2,
+leaves up to 2^-2 units, the second's range ends at 7.5 / 32 = 2^-2 - 2^-6 units, and 2^-6 of
+3.75 is 2^-7.9. The result is rounded by half a step; fp32 sums add 2^-16 of w over these
+lengths.
 
-  |o - ref| <= half |ref| + (2^-12.9 b + 2^-18 a + 2^-16) w + 2^-13.9 W    (bf16, few rows)
-  |lse - ref| <= 2^-13.9 b + 2^-19 a + 2^-17"""
+  |o - ref| <= half |ref| + (2^-16.9 b + 2^-18 a + 2^-16) w + 2^-13.9 W    (bf16, few rows)
+  |lse - ref| <= 2^-17.9 b + 2^-19 a + 2^-17"""
 import numpy as np
 import pytest
 import torch
@@ -96,8 +99,8 @@ def reference(s, q, new, scale, window=0):
 def compare(o, lse, ref, many, dtype):
     out, rl, w, W, a, b = ref
     o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
-    cut = 2.0 ** -13.9 if dtype == BF else 2.0 ** -21.9
-    weights = np.where(many, 2.0 ** -8.9, cut)[:, None, None] if dtype == BF else cut
+    cut = 2.0 ** -17.9 if dtype == BF else 2.0 ** -21.9
+    weights = np.where(many, 2.0 ** -7.9, 2.0 ** -13.9)[:, None, None] if dtype == BF else cut
     half = 2.0 ** -8 if dtype == BF else 2.0 ** -24
     bound = half * np.abs(out) + (2 * cut * b + 2.0 ** -18 * a + 2.0 ** -16)[..., None] * w + weights * W + 1e-30
     assert np.isfinite(o).all()
