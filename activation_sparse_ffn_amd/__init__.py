@@ -129,6 +129,16 @@ def _stream(device: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _run(lib, device: torch.device, call, *args):
+    """call(*args, stream) on the device's current stream, with the device current: what is
+    launched on a default stream goes to the current device, whatever the arguments'."""
+    if device.index == torch._C._cuda_getDevice():
+        _check(lib, call(*args, _stream(device)))
+    else:
+        with torch.cuda.device(device):
+            _check(lib, call(*args, _stream(device)))
+
+
 def _need_gpu(*ts: torch.Tensor):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):

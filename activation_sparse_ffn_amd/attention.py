@@ -21,7 +21,7 @@ from typing import Optional
 
 import torch
 
-from . import SFFN_BF16, SFFN_F32, _check, _need_buffer, _ptr, _stream, load_library
+from . import SFFN_BF16, SFFN_F32, _check, _need_buffer, _ptr, _run, _stream, load_library
 
 __all__ = ["rope_table", "qk_norm_rope", "qk_norm_rope_backward", "KVCache", "KVCache4", "CacheBatch",
            "kv_cache_append", "kv_cache_read", "cache_attention"]
@@ -427,9 +427,9 @@ def kv_cache_append(cache, batch: CacheBatch, k: torch.Tensor, v: torch.Tensor) 
     hv = _heads(v, "v", shape, dtype, dev)
     if type(cache) is KVCache4:
         slots = None if batch.slots is None else _address(batch.slots, "slots", (T,), torch.int64, dev)
-        _check(lib, lib.kv_cache4_append(cache._c, batch._c, slots, hk, hv, _DTYPES[dtype], T, _stream(dev)))
+        _run(lib, dev, lib.kv_cache4_append, cache._c, batch._c, slots, hk, hv, _DTYPES[dtype], T)
         return
-    _check(lib, lib.kv_cache_append(cache._c, batch._c, hk, hv, _DTYPES[dtype], T, _stream(dev)))
+    _run(lib, dev, lib.kv_cache_append, cache._c, batch._c, hk, hv, _DTYPES[dtype], T)
 
 
 def kv_cache_read(cache, batch: CacheBatch, total: int, dtype: torch.dtype = torch.bfloat16,
@@ -452,7 +452,7 @@ def kv_cache_read(cache, batch: CacheBatch, total: int, dtype: torch.dtype = tor
     else:
         hv = _heads(v, "v", shape, dtype, dev)
     read = lib.kv_cache4_read if type(cache) is KVCache4 else lib.kv_cache_read
-    _check(lib, read(cache._c, batch._c, hk, hv, _DTYPES[dtype], total, _stream(dev)))
+    _run(lib, dev, read, cache._c, batch._c, hk, hv, _DTYPES[dtype], total)
     return k, v
 
 
@@ -494,6 +494,6 @@ def cache_attention(cache, batch: CacheBatch, q: torch.Tensor, scale: Optional[f
         _need_buffer(workspace, "workspace", None, torch.uint8, dev)
         need = workspace.numel()
     attend = lib.cache4_attention if four else lib.cache_attention
-    _check(lib, attend(cache._c, batch._c, hq, heads, dt, T, D ** -0.5 if scale is None else scale, window, ho,
-                       _ptr(lse), _ptr(workspace), need, _stream(dev)))
+    _run(lib, dev, attend, cache._c, batch._c, hq, heads, dt, T, D ** -0.5 if scale is None else scale, window, ho,
+         _ptr(lse), _ptr(workspace), need)
     return (out, lse) if return_lse else out

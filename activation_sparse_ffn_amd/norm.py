@@ -16,7 +16,7 @@ from typing import Optional
 
 import torch
 
-from . import SFFN_BF16, SFFN_F32, _check, _need_buffer, _ptr, _stream, load_library
+from . import SFFN_BF16, SFFN_F32, _need_buffer, _ptr, _run, load_library
 
 __all__ = ["add_rms_norm", "add_rms_norm_backward"]
 
@@ -131,7 +131,7 @@ def add_rms_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, weigh
         h_out = x
     if small is not None:
         scale = _empty_strided((T,), (1,), dtype=torch.float32, device=dev)
-    _check(lib, lib.add_rms_norm(cfg, T, hx, hr, w, hy, _ptr(scale), hh, _stream(dev)))
+    _run(lib, dev, lib.add_rms_norm, cfg, T, hx, hr, w, hy, _ptr(scale), hh)
     return (y_out, h_out) if small is None else (y_out, scale, h_out)
 
 
@@ -155,5 +155,5 @@ def add_rms_norm_backward(h: torch.Tensor, g_y: torch.Tensor, weight: Optional[t
         gw = _empty_strided((d,), (1,), dtype=torch.float32, device=dev)
         need = lib.add_rms_norm_backward_workspace_size(cfg, T)
         ws = _empty_strided((need,), (1,), dtype=torch.uint8, device=dev) if need else None
-    _check(lib, lib.add_rms_norm_backward(cfg, T, hh, hg, hgh, w, hgx, _ptr(gw), _ptr(ws), need, _stream(dev)))
+    _run(lib, dev, lib.add_rms_norm_backward, cfg, T, hh, hg, hgh, w, hgx, _ptr(gw), _ptr(ws), need)
     return {"x": gx, "weight": gw}

@@ -16,7 +16,7 @@ from typing import NamedTuple, Optional, Tuple
 
 import torch
 
-from . import _check, _stream, load_library
+from . import _run, load_library
 from .attention import CacheBatch, _address, _Batch, _vector
 
 __all__ = ["PagePlan", "free_pages", "page_plan", "cache_slots"]
@@ -97,7 +97,7 @@ def page_plan(block_table: torch.Tensor, kv_lens: torch.Tensor, new_lens: torch.
         to = (_address(out.kv_lens, "out.kv_lens", (B,), _I32, dev), _address(out.n_free, "out.n_free", (2,), _I32, dev),
               _address(out.cu, "out.cu", (B + 1,), _I32, dev), _address(out.positions, "out.positions", (total,), _I32, dev),
               _address(out.slots, "out.slots", (total,), _I64, dev))
-    _check(lib, lib.page_plan(pool, lens, keep, fresh, left, total, *to, _stream(dev)))
+    _run(lib, dev, lib.page_plan, pool, lens, keep, fresh, left, total, *to)
     return out
 
 
@@ -110,6 +110,5 @@ def cache_slots(cache, batch: CacheBatch, total: int) -> Tuple[torch.Tensor, tor
     if cache.device != dev:
         raise ValueError(f"the cache is on {cache.device}, the batch on {dev}")
     positions, slots = _vector(total, _I32, dev), _vector(total, _I64, dev)
-    _check(lib, lib.cache_slots(batch._c, cache._c.n_pages, cache.page, total, positions.data_ptr(), slots.data_ptr(),
-                                _stream(dev)))
+    _run(lib, dev, lib.cache_slots, batch._c, cache._c.n_pages, cache.page, total, positions.data_ptr(), slots.data_ptr())
     return positions, slots

@@ -183,7 +183,8 @@ sffn_status_t cache_attention(const sffn_kv_cache_t* cache, const sffn_kv_batch_
  *   keys, values  uint8 [n_pages, kv_heads, page, head_dim / 2]
  *   k_exp    uint8 [n_pages, kv_heads, page, head_dim / 32]: a key is its entry times
  *            2^(k_exp - 127) of its 32 channels; 255 stands for NaN
- *   v_scale  fp32 [n_pages, kv_heads, page]: a value is its entry times its token's scale
+ *   v_scale  fp32 [n_pages, kv_heads, page], not negative: a value is its entry times its
+ *            token's scale
  * page 16, 32, 64 or 128; head_dim 64, 128 or 256; pointers 16-byte aligned. 68 + 68 bytes
  * a token and head of 128 channels, where the 8-bit cache takes 256. */
 typedef struct {

@@ -43,7 +43,7 @@ typedef struct {
 
 /* For every row t (fp32 inside):
  *   h = x + residual, rounded to dtype (without a residual h = x)
- *   r = rsqrt(mean(h^2) + eps),   n = h w
+ *   r = rsqrt(mean(h^2) + eps),   n = h w     (r = 0 where the sum of squares passes fp32)
  *   SFFN_NORM_SAME:  y = n r, rounded to dtype
  *   8 bits:          s = max|n| / 127 (or / 448), y = n / s rounded to the nearest
  *                    entry, ties to even, scale = s r; the value is y scale. The row's
