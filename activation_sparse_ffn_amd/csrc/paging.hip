@@ -207,10 +207,6 @@ __global__ __launch_bounds__(256) void k_slots(const SlotArgs a, int64_t first) 
     a.slots[t] = slot;
 }
 
-// Up to so many tokens the plan's own workgroup writes their positions and slots; the
-// launch of a second kernel costs more.
-constexpr int64_t kTokensInPlan = 4096;
-
 }  // namespace
 
 hipError_t launch_slots(const SlotArgs& a, hipStream_t s) {
@@ -224,10 +220,15 @@ hipError_t launch_slots(const SlotArgs& a, hipStream_t s) {
     return hipSuccess;
 }
 
+// One workgroup: of 256 threads for as many sequences and few pages (32 single tokens 4.4 us,
+// by 1024 threads 6.6; 8 prompts of 8192 tokens, 1024 pages, 9.05 and 9.35), else of 1024 (as
+// many single tokens 7.6, by 256 threads 12.4). It writes the positions and slots of up to
+// two tokens a thread itself (by 256: 256 tokens 4.6 us, with a second launch 6.0, 1024
+// tokens 7.6 and 6.9; by 1024: 2048 tokens 8.4 and 9.1, 4096 10.2 and 9.2).
 hipError_t launch_page_plan(const PlanArgs& a, hipStream_t s) {
-    const bool with_tokens = a.T <= kTokensInPlan;
-    // few sequences and tokens: fewer waves to start and to sum over
-    if (a.B <= 256 && a.T <= 1024) k_page_plan<256><<<dim3(1), 256, 0, s>>>(a, with_tokens);
+    const bool few = a.B <= 256 && a.T >> a.shift <= 1024;
+    const bool with_tokens = a.T <= (few ? 512 : 2048);
+    if (few) k_page_plan<256><<<dim3(1), 256, 0, s>>>(a, with_tokens);
     else k_page_plan<1024><<<dim3(1), 1024, 0, s>>>(a, with_tokens);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || with_tokens) return e;

@@ -138,7 +138,7 @@ static void pages() {
                     p.n_pages = INT32_MAX; p.n_seqs = seqs; p.max_pages = max_pages; p.table_stride = max_pages; p.page = page;
                     EXPECT_STATUS(page_plan(&p, at<int32_t>(5), nullptr, at<int32_t>(6), at<int32_t>(7), T, at<int32_t>(5),
                                             at<int32_t>(7), at<int32_t>(8), at<int32_t>(9), at<int64_t>(10), nullptr), SFFN_OK);
-                    EXPECT(LAUNCHED() >= (T > 4096 ? (uint64_t)T : 256));
+                    EXPECT(LAUNCHED() >= (T > 2048 ? (uint64_t)T : 256));
                     b.n_seqs = seqs; b.max_pages = max_pages; b.table_stride = max_pages; b.max_new = INT32_MAX;
                     EXPECT_STATUS(cache_slots(&b, INT32_MAX, page, T, at<int32_t>(9), at<int64_t>(10), nullptr), SFFN_OK);
                     EXPECT(LAUNCHED() >= (uint64_t)T);

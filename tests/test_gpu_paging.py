@@ -153,3 +153,13 @@ def test_no_sequences():
     table = torch.empty(0, 3, dtype=torch.int32, device="cuda")
     p = sffn.page_plan(table, i32([]), i32([]), free, n_free, 16, 2)
     assert p.cu.tolist() == [0] and p.n_free.tolist() == [4, 0] and p.slots.tolist() == [-1, -1]
+
+
+@pytest.mark.parametrize("B,new,page,totals", [(255, 2, 16, (511, 512, 513)), (256, 2, 16, (512, 513)), (257, 7, 16, (2047, 2048, 2049)),
+                                               (3, 6000, 16, (16383, 16384, 16400, 18000)), (900, 2, 32, (2048, 2049))])
+def test_sizes_around_which_the_plan_is_made_otherwise(B, new, page, totals):
+    table, held, keep, fresh, free, n = state(B, 50, new, page, True, 3 * B + B * new // page, 11)
+    fresh = [new] * B
+    table = [row + [-1] * (1 + new // page) for row in table]
+    for total in totals:
+        check(table, held, keep, fresh, free, n, page, total)
