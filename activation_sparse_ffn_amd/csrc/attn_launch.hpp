@@ -196,8 +196,11 @@ hipError_t launch_cache4_append(const CacheArgs& c, const Cache4& b, const int64
 hipError_t launch_cache4_read(const CacheArgs& c, const Cache4& b, const Heads& k, const Heads& v, hipStream_t s);
 
 // What beginning and ending a unit of work costs the few-row kernel, in steps of 64 keys (see
-// share_work).
+// share_work): calls of 32 ragged sequences 40.3 us with 16, 40.4 with 32, 47.5 with 56, of
+// an fp32 q 44, 46 and 53.
 constexpr int kUnitCost4 = 16;
+// The few-row kernel for one tile of 16 rows or two, else the row tiles; what either side
+// takes stands at the kernels.
 inline AttnPlan attn4_plan(const CacheArgs& c, int Hq, int window) {
     AttnPlan p{};
     const int64_t most = (int64_t)c.max_new * (Hq / c.Hkv);

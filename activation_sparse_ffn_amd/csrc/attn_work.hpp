@@ -188,7 +188,8 @@ constexpr int kLeast = 8;
 // therefore hide behind no other's work. A unit then costs EXTRA more than its steps; where
 // every unit can begin a share of its own, shares are multiples of ROUND steps (what a
 // workgroup takes at a time) and long enough for that if there are twice as many workgroups
-// as units.
+// as units. (4-bit cache: 32 sequences of 1 to 32768 keys, single tokens, 35 us with EXTRA
+// 16 and 65 with 0; 6 tokens each 58 and 114; one sequence takes the same.)
 template <int EXTRA = 0, int ROUND = 1, typename F, typename L>
 __device__ __forceinline__ void share_work(const AttnArgs& a, int tile_rows, F work, L lost) {
     const int lane = threadIdx.x & 63;

@@ -83,7 +83,8 @@ __device__ __forceinline__ void units(int e, int (&u)[2]) {
     u[1] = NP <= 4 ? 0 : e == 255 ? -1 : e - 4 * (int)r;
 }
 
-// 32 numbers as NP pieces, the first of unit 2^(e - 127): element 2 j is lo[j], 2 j + 1 hi[j]. The conversions write their result while they still read their operands: the empty
+// 32 numbers as NP pieces, the first of unit 2^(e - 127): element 2 j is lo[j], 2 j + 1
+// hi[j]. The conversions write their result while they still read their operands: the empty
 // asm keeps those, the unit among them, in other registers. (With the result over an operand
 // the pieces were wrong.)
 template <int NP>
@@ -242,6 +243,15 @@ __device__ __forceinline__ uint64_t page_row(const CacheArgs& c, uint32_t page, 
 //   O^T of 128 keys: the lane has the weights of keys 16 t + 4 g + i (t < 8, i < 4) of row
 //     n; element 2 (4 t + i) is that of t < 4, 2 (4 t + i) + 1 that of t + 4. A value row is
 //     put into LDS at the place 32 g + element, from which 16 of them are read transposed.
+//
+// Bound by memory and by the chains before and after the steps (lengths, table entry, q into
+// pieces: 4.7 us; the waves' join; 4.0 to 4.9 for the parts'). One workgroup a compute unit,
+// whose waves keep a whole step's keys and values in flight: one token of 32 heads over 8 of
+// the keys', 32768 keys of 128 channels, 14.0 us; 32 sequences of 3620 keys 29 (126 MB: 4.3
+// TB/s), as much in 1 to 32768 keys each 35, with an fp32 q 39. By two workgroups a compute
+// unit, with half the registers, 19.2, 32, 38 and 63. Two tiles at once share what is loaded:
+// 5 tokens over 32768 keys 23.4, 6 for each of the ragged sequences 58; by row tiles of 128
+// rows 30.3 and 102.
 // ---------------------------------------------------------------------------
 constexpr int kStep = 128;
 
@@ -500,6 +510,15 @@ __global__ __launch_bounds__(256, 1) void k_attend4_few(const Attn4Args args) {
 //   O^T of 64 keys: the lane has the weights of keys 8 (j / 4) + 4 half + j % 4 of the first
 //     32 (element 2 j) and of the second (2 j + 1). Value rows lie in LDS at the place 32
 //     half + element.
+//
+// Bound by the vector unit and the products' share of its issue slots: exponentials, maxima
+// and conversions of 32 scores a lane keep it busy for two thirds of the time, and a scaled
+// product takes two to three times the issue cycles of a bf16 one. 4096 tokens of 32 heads
+// over 32768 keys 1855 us (heads of 128; 2.06 TFLOP: 1.11 PFLOP/s), heads of 64 1548; heads of
+// 256 over 8192 keys 980, an fp32 q of heads of 128 866. Tried beside it: the products of one
+// step's values with the next one's scores in one phase 2185; weights as bf16 and values
+// widened in LDS 2115 (heads of 64 1484); scores a step ahead by one wave a SIMD 4328, its
+// registers moved to and fro; raised priority around the products 1877.
 // ---------------------------------------------------------------------------
 template <int D>
 struct RowsLds {

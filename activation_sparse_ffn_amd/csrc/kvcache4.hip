@@ -7,7 +7,12 @@
 // A lane has eight channels of a token and head, keys and values alike: 16 bytes in (fp32:
 // two times 16), 4 bytes of entries out. Largest values are compared as integers, in which
 // infinities and NaN come out on top. Every token's scales are its own: nothing that is held
-// is touched. Memory-bound.
+// is touched, and a lane needs no more than shuffles with its neighbours.
+//
+// Memory-bound, and for few tokens bound by the chain of loads from offsets to table entry:
+// 4096 tokens of 8 heads of 128 in 7.8 us stored and 7.1 read (21 MB in all: 2.8 TB/s; an
+// empty launch and a copy of as much take 3.5 + 4.1), 32 single tokens 3.1 and 3.5. With the
+// slots given an append looks nothing up.
 #include "attn_common.hpp"
 
 namespace sffn {
@@ -83,9 +88,10 @@ constexpr int rows_each(int D) { return kThreads * 8 / D; }
 template <typename E, int D>
 __global__ __launch_bounds__(kThreads) void k_cache4_append(const CacheArgs c, const Cache4 cache, const int64_t* slots,
                                                             const Heads k, const Heads v, uint32_t first) {
-    const int64_t r = ((int64_t)first + blockIdx.x) * rows_each(D) + threadIdx.x / (D / 8);
-    if (r >= c.T * c.Hkv) return;           // whole groups of D / 8 lanes
-    const int t = (int)(r / c.Hkv), h = (int)(r % c.Hkv), d = threadIdx.x % (D / 8) * 8;
+    const uint32_t r = (first + blockIdx.x) * rows_each(D) + threadIdx.x / (D / 8);     // of fewer than 2^31
+    if (r >= (uint32_t)(c.T * c.Hkv)) return;       // whole groups of D / 8 lanes
+    const int t = (int)(r / (uint32_t)c.Hkv), h = (int)(r - (uint32_t)t * (uint32_t)c.Hkv);
+    const int d = threadIdx.x % (D / 8) * 8;
     float x[8], y[8];
     Elem<E>::load8(static_cast<const E*>(k.p) + (t * k.st + h * k.sh) + d, x);
     Elem<E>::load8(static_cast<const E*>(v.p) + (t * v.st + h * v.sh) + d, y);
@@ -105,8 +111,16 @@ __global__ __launch_bounds__(kThreads) void k_cache4_append(const CacheArgs c, c
 
     const uint32_t most = largest<D / 8>(y);        // of the head
     const float s = most >= 0x7f800000u ? __builtin_nanf("") : __uint_as_float(most) / 6.f;
+    // y / s as IEEE division rounds it: with the rounded 1 / s one correction of y times that
+    // does it (P. Markstein), while nothing on the way is subnormal; what is then below 2^-24
+    // of s is entry 0 in any case. (8 divisions a lane and 64-bit row numbers: 8.7 us
+    // for the 4096 tokens above.)
+    const float up = s < 0x1p-60f ? 0x1p64f : 1.f, su = s * up, inv = 1.f / su;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = s > 0.f ? y[i] / s : 0.f;
+    for (int i = 0; i < 8; ++i) {
+        const float yu = y[i] * up, q = yu * inv;
+        y[i] = s > 0.f ? __builtin_fmaf(__builtin_fmaf(-q, su, yu), inv, q) : 0.f;
+    }
     const uint32_t vw = entries8(y, 1.f);
     if (!stored) return;
     *reinterpret_cast<uint32_t*>(cache.keys + row * (D / 2) + d / 2) = kw;
@@ -118,9 +132,10 @@ __global__ __launch_bounds__(kThreads) void k_cache4_append(const CacheArgs c, c
 template <typename E, int D>
 __global__ __launch_bounds__(kThreads) void k_cache4_read(const CacheArgs c, const Cache4 cache, const Heads k,
                                                           const Heads v, uint32_t first) {
-    const int64_t r = ((int64_t)first + blockIdx.x) * rows_each(D) + threadIdx.x / (D / 8);
-    if (r >= c.T * c.Hkv) return;
-    const int t = (int)(r / c.Hkv), h = (int)(r % c.Hkv), d = threadIdx.x % (D / 8) * 8;
+    const uint32_t r = (first + blockIdx.x) * rows_each(D) + threadIdx.x / (D / 8);
+    if (r >= (uint32_t)(c.T * c.Hkv)) return;
+    const int t = (int)(r / (uint32_t)c.Hkv), h = (int)(r - (uint32_t)t * (uint32_t)c.Hkv);
+    const int d = threadIdx.x % (D / 8) * 8;
     const int64_t slot = slot_of(c, t);
     if (slot == kNone) return;
     float x[8], y[8];
