@@ -515,15 +515,19 @@ hipError_t forward_by_output(const NormArgs& a, hipStream_t s) {
 // one a compute unit: 32768 bf16 rows of 512 take 26.8 us with the sum behind it, in
 // workgroups of 512 threads 31.6, of 256 49.2; 4096 rows of 4096 29.7, in workgroups of 512
 // 38.3, with two pieces a thread 45.6; 2048 rows of 8192 34.0, with two pieces 41.8. (One row
-// of 512 takes 7.3 us so, in a workgroup of 256 5.5.) Rows of 16384 by 512 threads of four
+// of 512 took 7.3 us so with a sum behind it, in a workgroup of 256 5.5.) Rows of 16384 by 512 threads of four
 // pieces 42.1, by 1024 of two 45.7, read twice 103.
 int backward_threads(int p) { return p <= 64 ? 64 : p <= 128 ? 128 : p <= 256 ? 256 : p <= 512 ? 512 : 1024; }
 
 int64_t backward_rows_each(const NormArgs& a) { return 1024 / backward_threads(pieces_of(a)); }
 
+// The rows of one or two turns go to one workgroup, whose sums are the weight's gradient: no
+// second launch (rows of 4096: one turn 5.0 us, by two launches 7.0; two 6.7 and 7.1, three
+// 8.3 and 7.2).
+constexpr int64_t kTurnsAlone = 2;
 int64_t backward_grid(const NormArgs& a) {
     const int64_t each = backward_rows_each(a), blocks = (a.T + each - 1) / each, most = compute_units();
-    return blocks < most ? blocks : most;
+    return blocks <= kTurnsAlone ? 1 : blocks < most ? blocks : most;
 }
 
 template <typename E>
@@ -550,10 +554,13 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_norm_backward(const NormArgs& a, hipStream_t s) {
-    const hipError_t e = a.dt == Dt::BF16 ? backward<uint16_t>(a, s) : backward<float>(a, s);
-    if (e != hipSuccess || !a.g_w) return e;
+    const int64_t rows = backward_grid(a);
+    NormArgs b = a;
+    if (rows == 1 && a.g_w) b.partial = a.g_w;
+    const hipError_t e = a.dt == Dt::BF16 ? backward<uint16_t>(b, s) : backward<float>(b, s);
+    if (e != hipSuccess || !a.g_w || rows == 1) return e;
     k_norm_sum<<<dim3((unsigned)((a.d + kSumCols - 1) / kSumCols)), kSumCols * kSumRows, 0, s>>>(
-        a.partial, (int)backward_grid(a), a.d, a.g_w);
+        a.partial, (int)rows, a.d, a.g_w);
     return hipGetLastError();
 }
 

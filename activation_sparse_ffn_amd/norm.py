@@ -55,6 +55,12 @@ def _config(d, dtype, out, eps):
     return _NormConfig(d, _DTYPES[dtype], out, eps)
 
 
+@functools.lru_cache(maxsize=1024)
+def _backward_workspace(d, dtype, T, device):
+    """Its bytes, a constant of its arguments (the device's compute units are)."""
+    return load_library().add_rms_norm_backward_workspace_size(_config(d, dtype, 0, 1.0), T)
+
+
 def _rows(t, name, shape=None, dtype=None, device=None):
     """A [T, d] view on the GPU as the library takes it. Without a shape, the tensor that
     sets it: bfloat16 or float32."""
@@ -153,7 +159,7 @@ def add_rms_norm_backward(h: torch.Tensor, g_y: torch.Tensor, weight: Optional[t
     need = 0
     if w is not None:
         gw = _empty_strided((d,), (1,), dtype=torch.float32, device=dev)
-        need = lib.add_rms_norm_backward_workspace_size(cfg, T)
+        need = _backward_workspace(d, dtype, T, dev)
         ws = _empty_strided((need,), (1,), dtype=torch.uint8, device=dev) if need else None
     _run(lib, dev, lib.add_rms_norm_backward, cfg, T, hh, hg, hgh, w, hgx, _ptr(gw), _ptr(ws), need)
     return {"x": gx, "weight": gw}
