@@ -518,7 +518,9 @@ __global__ __launch_bounds__(256, 1) void k_attend4_few(const Attn4Args args) {
 // 256 over 8192 keys 980, an fp32 q of heads of 128 866. Tried beside it: the products of one
 // step's values with the next one's scores in one phase 2185; weights as bf16 and values
 // widened in LDS 2115 (heads of 64 1484); scores a step ahead by one wave a SIMD 4328, its
-// registers moved to and fro; raised priority around the products 1877.
+// registers moved to and fro; raised priority around the products 1877; workgroups of eight
+// waves, half of them a phase behind, so that one half multiplies while the other weighs, 2677
+// with 128 bytes a lane spilled (heads of 64, without spills, 1529).
 // ---------------------------------------------------------------------------
 template <int D>
 struct RowsLds {

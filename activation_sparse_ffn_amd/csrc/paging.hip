@@ -75,8 +75,11 @@ __device__ __forceinline__ Request request_of(const PlanArgs& a, int b) {
     return r;
 }
 
-// One workgroup of NT threads, which takes as many sequences at a time; with_tokens:
-// positions and slots too.
+// One workgroup of NT threads, which takes as many sequences at a time, and kIn pages a
+// thread, whose loads are in flight together (200 sequences of up to 8000 tokens, of which
+// some end and some get prompts: one page a thread 10.8 us, four 8.4, eight 10.0);
+// with_tokens: positions and slots too.
+constexpr int kIn = 4;
 template <int NT>
 __global__ __launch_bounds__(NT) void k_page_plan(const PlanArgs a, bool with_tokens) {
     __shared__ int64_t sums[2][NT], scan[2][NT / 64];
@@ -92,16 +95,28 @@ __global__ __launch_bounds__(NT) void k_page_plan(const PlanArgs a, bool with_to
             sums[0][tid] = s;
             places[tid].y = r.from;
             __syncthreads();
-            for (int64_t k0 = 0; k0 < back; k0 += NT) {
-                int32_t page = -1;
-                if (k0 + tid < back) {
-                    const int at = first_above(sums[0], NT, k0 + tid);
-                    const int64_t i = k0 + tid - (at > 0 ? sums[0][at - 1] : 0) + places[at].y;
-                    page = a.table[(int64_t)(b0 + at) * a.table_stride + i];
+            for (int64_t k0 = 0; k0 < back; k0 += kIn * NT) {
+                const int64_t first = k0 + kIn * tid;
+                int at = first < back ? first_above(sums[0], NT, first) : 0, known = 0;
+                int32_t page[kIn];
+#pragma unroll
+                for (int j = 0; j < kIn; ++j) {
+                    page[j] = -1;
+                    if (first + j < back) {
+                        while (sums[0][at] <= first + j) ++at;
+                        const int64_t i = first + j - (at > 0 ? sums[0][at - 1] : 0) + places[at].y;
+                        page[j] = a.table[(int64_t)(b0 + at) * a.table_stride + i];
+                    }
                 }
-                const bool known = page >= 0 && page < a.n_pages;
-                const int64_t nth = n_free + block_prefix<NT>(known, scan[1], total) - 1;
-                if (known && nth < a.n_pages) a.free_pages[nth] = page;
+#pragma unroll
+                for (int j = 0; j < kIn; ++j) known += page[j] >= 0 && page[j] < a.n_pages;
+                int64_t nth = n_free + block_prefix<NT>(known, scan[1], total) - known;
+#pragma unroll
+                for (int j = 0; j < kIn; ++j)
+                    if (page[j] >= 0 && page[j] < a.n_pages) {
+                        if (nth < a.n_pages) a.free_pages[nth] = page[j];
+                        ++nth;
+                    }
                 n_free = min(n_free + total, a.n_pages);
                 __syncthreads();
             }
@@ -129,10 +144,18 @@ __global__ __launch_bounds__(NT) void k_page_plan(const PlanArgs a, bool with_to
         auto page_of = [&](int64_t k) {     // the k-th page that is taken
             return k < n_free ? a.free_pages[n_free - 1 - k] : -1;
         };
-        for (int64_t k = tid; k < new_pages; k += NT) {
-            const int at = first_above(sums[1], NT, k);
-            const int64_t i = k - (at > 0 ? sums[1][at - 1] : 0) + places[at].y;
-            a.table[(int64_t)(b0 + at) * a.table_stride + i] = page_of(taken + k);
+        for (int64_t k0 = tid; k0 < new_pages; k0 += kIn * NT) {
+            int32_t page[kIn];
+#pragma unroll
+            for (int j = 0; j < kIn; ++j) page[j] = k0 + j * NT < new_pages ? page_of(taken + k0 + j * NT) : -1;
+#pragma unroll
+            for (int j = 0; j < kIn; ++j) {
+                const int64_t k = k0 + j * NT;
+                if (k >= new_pages) break;
+                const int at = first_above(sums[1], NT, k);
+                const int64_t i = k - (at > 0 ? sums[1][at - 1] : 0) + places[at].y;
+                a.table[(int64_t)(b0 + at) * a.table_stride + i] = page[j];
+            }
         }
         if (with_tokens) {
             const int64_t left = a.T - tokens, n = left < new_tokens ? left : new_tokens;
@@ -222,7 +245,9 @@ hipError_t launch_slots(const SlotArgs& a, hipStream_t s) {
 
 // One workgroup: of 256 threads for as many sequences and few pages (32 single tokens 4.4 us,
 // by 1024 threads 6.6; 8 prompts of 8192 tokens, 1024 pages, 9.05 and 9.35), else of 1024 (as
-// many single tokens 7.6, by 256 threads 12.4). It writes the positions and slots of up to
+// many single tokens 7.6, by 256 threads 12.4). How many pages go back the device alone
+// knows: where 50 of 200 sequences of 8000 tokens end at once 256 threads take 19.9 us, 1024
+// 14.0; one of them 6.5 and 9.5. It writes the positions and slots of up to
 // two tokens a thread itself (by 256: 256 tokens 4.6 us, with a second launch 6.0, 1024
 // tokens 7.6 and 6.9; by 1024: 2048 tokens 8.4 and 9.1, 4096 10.2 and 9.2).
 hipError_t launch_page_plan(const PlanArgs& a, hipStream_t s) {
