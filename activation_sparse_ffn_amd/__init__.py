@@ -123,6 +123,10 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(device: torch.device) -> int:
     # the raw handle of torch's current stream; building a torch.cuda.Stream
     # object for it costs 2 us a call, as much as the launch itself
@@ -132,11 +136,14 @@ def _stream(device: torch.device) -> int:
 def _run(lib, device: torch.device, call, *args):
     """call(*args, stream) on the device's current stream, with the device current: what is
     launched on a default stream goes to the current device, whatever the arguments'."""
-    if device.index == torch._C._cuda_getDevice():
-        _check(lib, call(*args, _stream(device)))
+    index = device.index
+    if index == _current_device():
+        status = call(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            _check(lib, call(*args, _stream(device)))
+            status = call(*args, _raw_stream(index))
+    if status != SFFN_OK:
+        _check(lib, status)
 
 
 def _need_gpu(*ts: torch.Tensor):

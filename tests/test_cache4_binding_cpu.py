@@ -136,8 +136,8 @@ def test_the_tensors_device_is_current_for_the_launch(monkeypatch, current):
         entered.append(d.index)
         yield
 
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current, raising=False)
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 1000 + i, raising=False)
+    monkeypatch.setattr(sffn, "_current_device", lambda: current)
+    monkeypatch.setattr(sffn, "_raw_stream", lambda i: 1000 + i)
     monkeypatch.setattr(torch.cuda, "device", device)
     sffn._run(None, torch.device("cuda", 1), lambda *a: handed.append(a) or 0, "x")
     assert handed == [("x", 1001)] and entered == ([] if current == 1 else [1])
