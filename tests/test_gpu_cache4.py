@@ -447,3 +447,29 @@ def test_both_caches_in_a_step_of_a_planned_batch():
             at += m
     # 4 bits keep about a tenth of each entry, 8 about a hundredth
     assert (outs[0][0] - outs[1][0]).norm() < 0.3 * outs[1][0].norm()
+
+
+def test_pages_beyond_4_gib():
+    """The last pages of a pool of more than 2^32 bytes of keys and of values: append, read and
+    attention as over the first pages of a small one."""
+    import activation_sparse_ffn_amd as sffn
+    K, D, P, big = 8, 256, 128, 34000
+    g = torch.Generator(device="cuda").manual_seed(4)
+    new, T = [300, 1], 301
+    k, v = (torch.randn(T, K, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(T, 2 * K, D, generator=g, device="cuda").bfloat16()
+    outs = []
+    for pages in (8, big):
+        cache = sffn.KVCache4.empty(pages, K, D, P)
+        assert pages == 8 or cache.keys.numel() > 1 << 32
+        table = i32([[pages - 1, pages - 2, pages - 3], [pages - 4, 0, 0]])
+        batch = sffn.CacheBatch(table, i32([300, 1]), 300, i32([0, 300, 301]), 300)
+        _, slots = sffn.cache_slots(cache, batch, T)
+        assert slots[0] == (pages - 1) * P
+        sffn.kv_cache_append(cache, sffn.CacheBatch(table, i32([300, 1]), 300, i32([0, 300, 301]), 300, slots=slots), k, v)
+        chunk = sffn.cache_attention(cache, batch, q)
+        one = sffn.cache_attention(cache, sffn.CacheBatch(table, i32([300, 1]), 300), q[[299, 300]])
+        outs.append((*sffn.kv_cache_read(cache, batch, T), chunk, one))
+        del cache
+    for a, b in zip(*outs):
+        assert torch.equal(a, b) and torch.isfinite(a.float()).all()
