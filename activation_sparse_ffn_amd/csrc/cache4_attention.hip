@@ -22,7 +22,9 @@
 // 1 / 16 leaves. q's blocks are 32 channels of a row, the weights' the 32 keys of a row that
 // a lane holds. q of bf16 has four pieces, of fp32 five; weights two in sequences of more
 // than kPreciseRows rows, three in those of fewer, five for fp32. The sum l takes the
-// weights before they are cut.
+// weights before they are cut. (4096 tokens over 32768 keys, 1.90 ms: with three pieces of
+// the weights 2.21, error 1.7e-3 instead of 2.1e-3; with three of q 1.76, but the logarithms
+// of the sums, fp32 numbers, are then off by more than 1e-6 of themselves.)
 #include <type_traits>
 #include <utility>
 
