@@ -68,7 +68,7 @@ def _rows(t, name, shape=None, dtype=None, device=None):
                                        if shape is not None else t.dim() != 2 or t.dtype not in _DTYPES or not t.is_cuda):
         _check_rows(t, name, shape, dtype, device)
     s, one = t.stride()
-    T, d = t.shape
+    T, d = t.shape if shape is None else shape
     if one != 1 and d > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     return _Rows(t.data_ptr(), s if T > 1 else d)       # a dimension of one element may carry any stride
@@ -112,7 +112,7 @@ def add_rms_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, weigh
     scale 0, one with a NaN or an infinity scale NaN."""
     lib = load_library()
     hx = _rows(x, "x")
-    T, d = x.shape
+    T, d = shape = x.shape
     dtype, dev = x.dtype, x.device
     try:
         kind, small = NORM_OUTPUTS[quant]
@@ -124,13 +124,13 @@ def add_rms_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, weigh
     if y_out is None:
         y_out, hy = _new(T, d, small or dtype, dev)
     else:
-        hy = _rows(y_out, "y_out", x.shape, small or dtype, dev)
+        hy = _rows(y_out, "y_out", shape, small or dtype, dev)
     if residual is not None:
-        hr = _rows(residual, "residual", x.shape, dtype, dev)
+        hr = _rows(residual, "residual", shape, dtype, dev)
         if h_out is None:
             h_out, hh = _new(T, d, dtype, dev)
         else:
-            hh = _rows(h_out, "h_out", x.shape, dtype, dev)
+            hh = _rows(h_out, "h_out", shape, dtype, dev)
     elif h_out is not None:
         raise ValueError("h_out takes the sum with a residual, which is not given")
     else:
@@ -148,11 +148,11 @@ def add_rms_norm_backward(h: torch.Tensor, g_y: torch.Tensor, weight: Optional[t
     residual alike (h's type), and "weight" (fp32; None where no weight was given)."""
     lib = load_library()
     hh = _rows(h, "h")
-    T, d = h.shape
+    T, d = shape = h.shape
     dtype, dev = h.dtype, h.device
     cfg = _config(d, dtype, 0, eps)
-    hg = _rows(g_y, "g_y", h.shape, dtype, dev)
-    hgh = None if g_h is None else _rows(g_h, "g_h", h.shape, dtype, dev)
+    hg = _rows(g_y, "g_y", shape, dtype, dev)
+    hgh = None if g_h is None else _rows(g_h, "g_h", shape, dtype, dev)
     w = _weight(weight, d, dtype, dev)
     gx, hgx = _new(T, d, dtype, dev)
     gw = ws = None
