@@ -128,8 +128,9 @@ constexpr int64_t kSharedRows = 32768;
 constexpr int64_t kPartBytes = (int64_t)256 << 20;
 
 // The rest of a plan whose kernels are chosen (few, pair, waves, pieces); the chip holds
-// `held` of their workgroups a compute unit.
-inline AttnPlan cut_up(const CacheArgs& c, int Hq, int window, AttnPlan p, int64_t held) {
+// `held` of their workgroups a compute unit. Row tiles of fewer than `sharers` sequences are
+// not shared out.
+inline AttnPlan cut_up(const CacheArgs& c, int Hq, int window, AttnPlan p, int64_t held, int sharers = 0) {
     const int64_t G = Hq / c.Hkv, most = (int64_t)c.max_new * G;
     p.rows = p.few ? 16 : p.pair ? 32 : 32 * p.waves;
     p.row_tiles = (most + p.rows - 1) / p.rows;
@@ -143,7 +144,7 @@ inline AttnPlan cut_up(const CacheArgs& c, int Hq, int window, AttnPlan p, int64
     // parts of every row that kPartBytes hold
     const int64_t room = (kPartBytes / 4 / rows - 1) / (c.D + 2);
     const int64_t steps = (span + 63) / 64, all_steps = ((int64_t)c.max_pages * c.P + c.max_new) / 64 + 16;
-    p.shared = p.few || p.pair || (rows <= kSharedRows && whole <= ((int64_t)1 << 31) / all_steps);
+    p.shared = p.few || p.pair || (c.B >= sharers && rows <= kSharedRows && whole <= ((int64_t)1 << 31) / all_steps);
     if (p.shared) {
         // no share is less than 8 steps of 64 keys (see share_work)
         p.chunk = 8 * 64;
@@ -207,7 +208,10 @@ inline AttnPlan attn4_plan(const CacheArgs& c, int Hq, int window) {
     p.few = most <= 16;
     p.pair = !p.few && most <= 32 && c.D <= 128;
     p.waves = 4;
-    return cut_up(c, Hq, window, p, p.few || p.pair ? 1 : few_held(c.D, c.dt == Dt::F32));
+    // one sequence's tiles are alike: without the walk's state their kernel spills nothing (32,
+    // 256 tokens over 32768 keys 47 and 150 us, shared 53 and 164; 600 over 9000 114 and 139;
+    // but 64 over 2000 with a max_kv of 32768 54 and 32)
+    return cut_up(c, Hq, window, p, p.few || p.pair ? 1 : few_held(c.D, c.dt == Dt::F32), 2);
 }
 hipError_t launch_cache4_attention(const CacheArgs& c, const Cache4& b, const AttnPlan& plan, const Heads& q, int Hq,
                                    float scale, int window, const Heads& out, float* lse, void* ws, hipStream_t s);
