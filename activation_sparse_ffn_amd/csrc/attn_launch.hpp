@@ -200,6 +200,10 @@ hipError_t launch_cache4_read(const CacheArgs& c, const Cache4& b, const Heads& 
 // share_work): calls of 32 ragged sequences 40.3 us with 16, 40.4 with 32, 47.5 with 56, of
 // an fp32 q 44, 46 and 53.
 constexpr int kUnitCost4 = 16;
+// The same of its row tiles, at most the other: 32 ragged sequences of 60 tokens 170 us with 6,
+// 171 with 3, 198 with none; 16 of 20 tokens, heads of 256, 106, 128 and 130; 16 of 40, fp32,
+// 102, 99 and 121; 64 of 12 tokens over up to 2000 keys 63, 62 and 59.
+constexpr int kTileCost4 = 6;
 // The few-row kernel for one tile of 16 rows or two, else the row tiles; what either side
 // takes stands at the kernels.
 inline AttnPlan attn4_plan(const CacheArgs& c, int Hq, int window) {

@@ -184,11 +184,10 @@ __device__ __forceinline__ int wave_scan(int v, Op op) {
 // called by one workgroup for each sequence with tokens that are not computed.
 constexpr int kLeast = 8;
 
-// EXTRA, ROUND: of kernels that hold one workgroup a compute unit, whose beginnings and ends
-// therefore hide behind no other's work. A unit then costs EXTRA more than its steps; where
-// every unit can begin a share of its own, shares are multiples of ROUND steps (what a
-// workgroup takes at a time) and long enough for that if there are twice as many workgroups
-// as units. (4-bit cache: 32 sequences of 1 to 32768 keys, single tokens, 35 us with EXTRA
+// EXTRA, ROUND: of kernels whose beginnings and ends hide behind no other's work. A unit then
+// costs EXTRA more than its steps; with a ROUND, where every unit can begin a share of its
+// own, shares are multiples of ROUND steps (what a workgroup takes at a time) and long enough
+// for that if there are twice as many workgroups as units. (4-bit cache: 32 sequences of 1 to 32768 keys, single tokens, 35 us with EXTRA
 // 16 and 65 with 0; 6 tokens each 58 and 114; one sequence takes the same.)
 template <int EXTRA = 0, int ROUND = 1, typename F, typename L>
 __device__ __forceinline__ void share_work(const AttnArgs& a, int tile_rows, F work, L lost) {
@@ -262,7 +261,7 @@ __device__ __forceinline__ void share_work(const AttnArgs& a, int tile_rows, F w
             return lane_value(x.cost, 63);
         };
         int rounded;
-        if constexpr (EXTRA == 0) {
+        if constexpr (EXTRA == 0 || ROUND == 1) {
             rounded = round_up(share);
         } else {
             const int alone = total - EXTRA * units_of_all, grid = (int)gridDim.x;

@@ -791,7 +791,7 @@ __global__ __launch_bounds__(256, few_held(D, sizeof(E) == 4)) void k_attend4_ro
         attend4_rows<E, NP, PP, D>(args, w, parts, lds);
     };
     if constexpr (SHARED) {
-        share_work(
+        share_work<kTileCost4>(
             args.a, 128,
             [&](const Work& w, int parts) {
                 __syncthreads();        // the work before has been read from LDS
