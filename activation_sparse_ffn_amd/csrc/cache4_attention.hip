@@ -252,8 +252,8 @@ __device__ __forceinline__ uint64_t page_row(const CacheArgs& c, uint32_t page, 
 // the keys', 32768 keys of 128 channels, 14.0 us; 32 sequences of 3620 keys 29 (126 MB: 4.3
 // TB/s), as much in 1 to 32768 keys each 35, with an fp32 q 39. By two workgroups a compute
 // unit, with half the registers, 19.2, 32, 38 and 63. Two tiles at once share what is loaded:
-// 5 tokens over 32768 keys 23.4, 6 for each of the ragged sequences 58; by row tiles of 128
-// rows 30.3 and 102.
+// 6 tokens for each of the ragged sequences 58, by row tiles of 128 rows 88 (5 tokens over
+// 32768 keys 23.4 and 22.9).
 // ---------------------------------------------------------------------------
 constexpr int kStep = 128;
 
