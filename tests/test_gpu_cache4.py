@@ -473,3 +473,11 @@ def test_pages_beyond_4_gib():
         del cache
     for a, b in zip(*outs):
         assert torch.equal(a, b) and torch.isfinite(a.float()).all()
+
+
+@pytest.mark.parametrize("window", [0, 700])
+@pytest.mark.parametrize("max_kv", [1, 500, 3000, 60000])
+def test_one_sequence_cut_by_any_length(max_kv, window):
+    """max_kv cuts one sequence's row tiles into ranges of keys; what is computed is the same."""
+    check([3000], [70], 8, 2, 128, 64, BF, window=window, seed=21, max_kv=max_kv)
+    check([1300], [41], 4, 1, 64, 16, F32, window=window, seed=22, max_kv=max_kv)
