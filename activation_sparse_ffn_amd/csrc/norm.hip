@@ -100,7 +100,20 @@ __device__ __forceinline__ uint32_t entries4(const float* v, float s) {
     }
 }
 
-// Sums (or largest values) over the NT threads of a row, the same in all of them: within
+// The larger of two magnitudes, compared as integers, in which infinities and NaN come out
+// on top (a floating-point maximum drops a NaN).
+__device__ __forceinline__ float larger(float a, float b) {
+    return __int_as_float(max(__float_as_int(a), __float_as_int(b)));
+}
+
+// The unit of a row's 8-bit entries, whose largest magnitude is `top`: NaN, and so the row's
+// scale, where that is not finite.
+template <NormOut OUT>
+__device__ __forceinline__ float unit_of(float top) {
+    return top < __builtin_huge_valf() ? top / (OUT == NormOut::Int8 ? 127.f : 448.f) : __builtin_nanf("");
+}
+
+// Sums (or largest magnitudes) over the NT threads of a row, the same in all of them: within
 // waves, then across them in LDS in a fixed order. `at` is the row's place in LDS.
 template <int NT, bool MAX>
 __device__ __forceinline__ float2 row_reduce(float sum, float other, float2* at) {
@@ -108,7 +121,7 @@ __device__ __forceinline__ float2 row_reduce(float sum, float other, float2* at)
     for (int o = 32; o >= 1; o >>= 1) {
         sum += __shfl_xor(sum, o, 64);
         const float q = __shfl_xor(other, o, 64);
-        other = MAX ? fmaxf(other, q) : other + q;
+        other = MAX ? larger(other, q) : other + q;
     }
     if constexpr (NT > 64) {
         const int wave = threadIdx.x % NT / 64;
@@ -119,7 +132,7 @@ __device__ __forceinline__ float2 row_reduce(float sum, float other, float2* at)
         for (int i = 1; i < NT / 64; ++i) {
             const float2 q = at[i];
             v.x += q.x;
-            v.y = MAX ? fmaxf(v.y, q.y) : v.y + q.y;
+            v.y = MAX ? larger(v.y, q.y) : v.y + q.y;
         }
         return v;
     }
@@ -177,12 +190,12 @@ __global__ __launch_bounds__(block_of(NT)) void k_norm(const NormArgs a) {
                 for (int j = 0; j < V; ++j) h[j] *= q[j];
             }
 #pragma unroll
-            for (int j = 0; j < V; ++j) top = fmaxf(top, fabsf(h[j]));
+            for (int j = 0; j < V; ++j) top = larger(top, fabsf(h[j]));
         }
     }
     const float2 s = row_reduce<NT, true>(sum, top, lds);
     const float rstd = rsqrtf(s.x / a.d + a.eps);
-    const float unit = s.y / (OUT == NormOut::Int8 ? 127.f : 448.f);
+    const float unit = unit_of<OUT>(s.y);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int at = (tid + i * NT) * V, n = a.d - at;
@@ -250,12 +263,12 @@ __global__ __launch_bounds__(1024) void k_norm_long(const NormArgs a) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             sum += h[j] * h[j];
-            top = fmaxf(top, fabsf(nw[j]));
+            top = larger(top, fabsf(nw[j]));
         }
     }
     const float2 s = row_reduce<NT, true>(sum, top, lds);
     const float rstd = rsqrtf(s.x / a.d + a.eps);
-    const float unit = s.y / (OUT == NormOut::Int8 ? 127.f : 448.f);
+    const float unit = unit_of<OUT>(s.y);
     for (int at = threadIdx.x * V; at < a.d; at += NT * V) {
         const int n = a.d - at;
         float h[V], nw[V];

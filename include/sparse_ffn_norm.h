@@ -48,9 +48,10 @@ typedef struct {
  *   8 bits:          s = max|n| / 127 (or / 448), y = n / s rounded to the nearest
  *                    entry, ties to even, scale = s r; the value is y scale. The row's
  *                    factor r divides out of the entries, so that they follow from h
- *                    and w alone. A row of zeros has scale 0; one that holds a NaN or an
- *                    infinity has scale NaN and undefined entries. SFFN_NORM_SAME makes
- *                    such a row's y NaN, an infinity's other entries 0.
+ *                    and w alone. A row of zeros has scale 0; one with a NaN or an infinity
+ *                    in h or in h w has scale NaN and undefined entries. SFFN_NORM_SAME:
+ *                    a NaN of h makes the row's y NaN, an infinity of h its own entry NaN
+ *                    and the others 0; what is not finite in w shows in its own entry.
  *   x, residual (NULL: none), weight [d] (NULL: ones), y [T, d]
  *   scale [T] fp32, 8 bits only
  *   h     the sum, [T, d] or NULL; not without a residual
