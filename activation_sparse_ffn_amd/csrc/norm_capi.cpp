@@ -53,6 +53,14 @@ sffn_status_t check_rows(const sffn_rows_t* v, const char* name, const sffn_norm
     return SFFN_OK;
 }
 
+// An output that lies where an input does must write every row over itself: over another
+// one it would meet a workgroup that has yet to read it.
+sffn_status_t check_in_place(const sffn_rows_t* out, const char* name, const sffn_rows_t* in, const char* input, int64_t T,
+                             bool same_size = true) {
+    if (!in || out->data != in->data || (same_size && (T == 1 || out->stride == in->stride))) return SFFN_OK;
+    return fail(SFFN_ERR_INVALID_ARG, "%s lies where %s does, with rows of another size", name, input);
+}
+
 sffn_status_t check_vector(const void* p, const char* name, size_t e) {
     if (reinterpret_cast<uintptr_t>(p) % e != 0)
         return fail(SFFN_ERR_INVALID_ARG, "%s is not aligned to its elements", name);
@@ -89,11 +97,15 @@ sffn_status_t add_rms_norm(const sffn_norm_config_t* cfg, int64_t T, const sffn_
     if (residual) SFFN_TRY(check_rows(residual, "residual", cfg, T, e, false));
     SFFN_TRY(check_vector(weight, "weight", e));
     SFFN_TRY(check_rows(y, "y", cfg, T, wide ? 1 : e, true));
+    SFFN_TRY(check_in_place(y, "y", x, "x", T, !wide));
+    SFFN_TRY(check_in_place(y, "y", residual, "residual", T, !wide));
     if (wide && !scale) return fail(SFFN_ERR_INVALID_ARG, "scale is null");
     SFFN_TRY(check_vector(scale, "scale", 4));
     if (h) {
         if (!residual) return fail(SFFN_ERR_INVALID_ARG, "h is the sum with the residual, which is not given");
         SFFN_TRY(check_rows(h, "h", cfg, T, e, true));
+        SFFN_TRY(check_in_place(h, "h", x, "x", T));
+        SFFN_TRY(check_in_place(h, "h", residual, "residual", T));
         if (h->data == y->data) return fail(SFFN_ERR_INVALID_ARG, "h and y are the same");
     }
     sffn::NormArgs a = norm_args(cfg, T, weight);
@@ -125,6 +137,9 @@ sffn_status_t add_rms_norm_backward(const sffn_norm_config_t* cfg, int64_t T, co
     if (g_h) SFFN_TRY(check_rows(g_h, "g_h", cfg, T, e, false));
     SFFN_TRY(check_vector(weight, "weight", e));
     SFFN_TRY(check_rows(g_x, "g_x", cfg, T, e, true));
+    SFFN_TRY(check_in_place(g_x, "g_x", h, "h", T));
+    SFFN_TRY(check_in_place(g_x, "g_x", g_y, "g_y", T));
+    SFFN_TRY(check_in_place(g_x, "g_x", g_h, "g_h", T));
     sffn::NormArgs a = norm_args(cfg, T, weight);
     a.x = view(h);
     a.g_y = view(g_y);

@@ -55,8 +55,8 @@ typedef struct {
  *   x, residual (NULL: none), weight [d] (NULL: ones), y [T, d]
  *   scale [T] fp32, 8 bits only
  *   h     the sum, [T, d] or NULL; not without a residual
- * y and h may each be x or residual themselves (same data and stride), but not each
- * other. T == 0 enqueues nothing. */
+ * h, and with SFFN_NORM_SAME y, may be x or residual themselves (same data and stride), but
+ * not each other. No other two may overlap. T == 0 enqueues nothing. */
 sffn_status_t add_rms_norm(const sffn_norm_config_t* cfg, int64_t T, const sffn_rows_t* x,
                            const sffn_rows_t* residual, const void* weight, const sffn_rows_t* y, float* scale,
                            const sffn_rows_t* h, void* hip_stream);
@@ -68,9 +68,9 @@ size_t add_rms_norm_backward_workspace_size(const sffn_norm_config_t* cfg, int64
 /* Gradients of L for the gradients g_y of y and g_h of h (NULL: zero):
  *   u = g_y w,  xh = h r,  g_x = r (u - xh mean(u xh)) + g_h,  g_weight = sum_t g_y xh
  * with h the forward's sum. g_x [T, d] (dtype) is the gradient of x and of the residual
- * alike and may be h, g_y or g_h themselves. weight NULL: ones. g_weight [d] fp32 is
- * summed over rows in a fixed order (NULL: not wanted; zeros for T == 0); it needs the
- * workspace (256-byte aligned). */
+ * alike and may be h, g_y or g_h themselves (same data and stride). weight NULL: ones.
+ * g_weight [d] fp32 is summed over rows in a fixed order (NULL: not wanted; zeros for
+ * T == 0); it needs the workspace (256-byte aligned). */
 sffn_status_t add_rms_norm_backward(const sffn_norm_config_t* cfg, int64_t T, const sffn_rows_t* h,
                                     const sffn_rows_t* g_y, const sffn_rows_t* g_h, const void* weight,
                                     const sffn_rows_t* g_x, float* g_weight, void* workspace, size_t ws_bytes,
