@@ -264,7 +264,9 @@ __device__ __forceinline__ void share_work(const AttnArgs& a, int tile_rows, F w
         if constexpr (EXTRA == 0 || ROUND == 1) {
             rounded = round_up(share);
         } else {
-            const int alone = total - EXTRA * units_of_all, grid = (int)gridDim.x;
+            // (at least one step: a call whose sequences have no new tokens has no share of 0)
+            const int steps_alone = total - EXTRA * units_of_all, grid = (int)gridDim.x;
+            const int alone = steps_alone > 0 ? steps_alone : 1;
             auto whole = [&](int n) {
                 int to = ((alone + n - 1) / n + ROUND - 1) / ROUND * ROUND;
                 if (a.splits > 1 && to < longest / (a.splits - 1) + 1) to = longest / (a.splits - 1) + 1;
