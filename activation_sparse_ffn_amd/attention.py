@@ -384,7 +384,7 @@ class CacheBatch:
     of many sequences is faster if told so). A sequence's tokens beyond it are not
     stored, and their rows are NaN. max_kv: about the largest kv_lens (it splits
     the work and never changes what is computed). slots: the new tokens' slots, int64 [T],
-    as page_plan and cache_slots give them (an append to a 4-bit cache then looks up none).
+    as page_plan and cache_slots give them (an append to a 4-bit cache then looks up no pages).
     """
 
     def __init__(self, block_table: torch.Tensor, kv_lens: torch.Tensor, max_kv: int,

@@ -16,10 +16,16 @@ CacheBuffers buffers(const sffn_kv_cache4_t* c) {
 
 Cache4 cache4(const sffn_kv_cache4_t* c) { return {c->keys, c->values, c->k_exp, c->v_scale}; }
 
-// Of an append by slots: the batch says nothing but the count of tokens.
-sffn_status_t check_slots(const int64_t* slots) {
+// Of an append by slots: of the batch, where there is one, offsets and max_new are read.
+sffn_status_t check_slots(const int64_t* slots, const sffn_kv_batch_t* batch) {
+    if (!slots) return SFFN_OK;
     if (reinterpret_cast<uintptr_t>(slots) % 8 != 0)
         return fail(SFFN_ERR_INVALID_ARG, "slots must be 8-byte aligned");
+    if (!batch) return SFFN_OK;
+    if (batch->n_seqs < 0 || batch->max_new < 0)
+        return fail(SFFN_ERR_INVALID_ARG, "n_seqs and max_new must not be negative");
+    if (reinterpret_cast<uintptr_t>(batch->cu) % 4 != 0)
+        return fail(SFFN_ERR_INVALID_ARG, "cu must be 4-byte aligned");
     return SFFN_OK;
 }
 
@@ -42,10 +48,12 @@ sffn_status_t kv_cache4_append(const sffn_kv_cache4_t* cache, const sffn_kv_batc
                                void* hip_stream) {
     const int dt = as_int(dtype);
     SFFN_TRY(check_dtype(dt));
-    SFFN_TRY(check_slots(slots));
+    SFFN_TRY(check_slots(slots, batch));
     // the sequences that a call by slots stands for: as many as it has tokens, a page each
     sffn_kv_batch_t by_slots{};
     int32_t unused = 0;
+    // which matters where one can have more than max_new of them
+    const sffn_kv_batch_t* given = slots && batch && batch->cu && batch->max_new < T ? batch : nullptr;
     if (slots) {
         if (T < 0 || T > INT32_MAX) return fail(SFFN_ERR_INVALID_ARG, "T must lie in [0, 2^31) (got %lld)", (long long)T);
         by_slots.n_seqs = (int32_t)T;
@@ -57,9 +65,15 @@ sffn_status_t kv_cache4_append(const sffn_kv_cache4_t* cache, const sffn_kv_batc
     }
     SFFN_TRY(check_cache(cache, batch, T));
     if (T == 0 || batch->n_seqs == 0 || batch->max_new == 0) return SFFN_OK;
+    if (given && given->max_new == 0) return SFFN_OK;
     SFFN_TRY(check_copy(cache, batch, k, v, dt, T, false));
     CacheArgs a = cache_shape(cache, batch, dt, T);
     if (slots) a.table = a.lens = nullptr;      // not read
+    if (given && given->n_seqs > 0) {
+        a.cu = given->cu;
+        a.B = given->n_seqs;
+        a.max_new = given->max_new;
+    }
     return hip_status(launch_cache4_append(a, cache4(cache), slots, view(k), view(v), static_cast<hipStream_t>(hip_stream)),
                       "kv_cache4_append");
 }

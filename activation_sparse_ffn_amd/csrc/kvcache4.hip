@@ -12,7 +12,8 @@
 // Memory-bound, and for few tokens bound by the chain of loads from offsets to table entry:
 // 4096 tokens of 8 heads of 128 in 7.8 us stored and 7.1 read (21 MB in all: 2.8 TB/s; an
 // empty launch and a copy of as much take 3.5 + 4.1), 32 single tokens 3.1 and 3.5. With the
-// slots given an append looks nothing up.
+// slots given an append looks up no pages; the offsets alone where a sequence of the call can
+// have more than max_new tokens (32 single tokens 0.4 us of it, 32 times 128 of them 0.9).
 #include "attn_common.hpp"
 
 namespace sffn {
@@ -21,20 +22,40 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// The sequence in which token t of the call lies, if it is in one, and its first token: the
+// last of n ascending offsets that is not above t (sequence 0 if none is). Found by the L
+// lanes of a row together, L offsets at a time: of 32 in two loads one after another, where
+// halving takes five and one for the offset.
+template <int L>
+__device__ __forceinline__ int sequence_at(const int32_t* offsets, int n, int t, int& first) {
+    if (n == 1) {           // nothing to search, and nothing waits for the others' offsets
+        first = offsets[0];
+        return 0;
+    }
+    const uint32_t lane = threadIdx.x % L, group = (threadIdx.x & 63) / L * L;
+    uint32_t lo = 0, hi = (uint32_t)n, step;
+    first = 0x7fffffff;
+    do {
+        step = (hi - lo + L - 1) / L;
+        const uint32_t i = lo + lane * step;
+        const int at = i < hi ? offsets[i] : 0x7fffffff;
+        const int k = __popcll(__ballot(at <= t) >> group & (((uint64_t)1 << L) - 1));
+        if (k == 0) break;
+        first = __shfl(at, (int)group + k - 1, 64);
+        lo += (k - 1) * step;
+        hi = min(lo + step, hi);
+    } while (step > 1);
+    return (int)lo;
+}
+
 // Where token t of the call lies: its slot, kLost where it shows as NaN (beyond max_new,
 // offsets that leave the call, no page), kNone in no sequence.
 constexpr int64_t kLost = -1, kNone = -2;
+template <int L>
 __device__ __forceinline__ int64_t slot_of(const CacheArgs& c, int t) {
     int b = t, first = t, last = t + 1;
     if (c.cu) {
-        int lo = 0, hi = c.B;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (c.cu[mid] <= t) lo = mid;
-            else hi = mid;
-        }
-        b = lo;
-        first = c.cu[b];
+        b = sequence_at<L>(c.cu, c.B, t, first);
         last = c.cu[b + 1];
         if (t < first || t >= last) return kNone;
         if (first < 0 || last > c.T || t - first >= c.max_new) return kLost;
@@ -44,6 +65,17 @@ __device__ __forceinline__ int64_t slot_of(const CacheArgs& c, int t) {
     const uint32_t page = (uint32_t)c.table[(int64_t)b * c.table_stride + (pos >> c.shift)];
     if (page >= (uint64_t)c.n_pages) return kLost;
     return ((int64_t)page << c.shift) + (pos & (c.P - 1));
+}
+
+// The slot that the caller gives it, unless the batch's offsets (where they count, see
+// kv_cache4_append) have it beyond max_new.
+template <int L>
+__device__ __forceinline__ int64_t slot_given(const CacheArgs& c, const int64_t* slots, int t) {
+    const int64_t slot = slots[t];
+    if (!c.cu) return slot;
+    int first;
+    sequence_at<L>(c.cu, c.B, t, first);
+    return (int64_t)t - first >= c.max_new ? kLost : slot;
 }
 
 // Row (token of a page and head) of the cache's arrays.
@@ -95,7 +127,7 @@ __global__ __launch_bounds__(kThreads) void k_cache4_append(const CacheArgs c, c
     float x[8], y[8];
     Elem<E>::load8(static_cast<const E*>(k.p) + (t * k.st + h * k.sh) + d, x);
     Elem<E>::load8(static_cast<const E*>(v.p) + (t * v.st + h * v.sh) + d, y);
-    const int64_t slot = slots ? slots[t] : slot_of(c, t);
+    const int64_t slot = slots ? slot_given<D / 8>(c, slots, t) : slot_of<D / 8>(c, t);
     const bool stored = slot >= 0 && slot < c.n_pages << c.shift;
     const int64_t row = row_of_slot(c, stored ? slot : 0, h);
 
@@ -136,7 +168,7 @@ __global__ __launch_bounds__(kThreads) void k_cache4_read(const CacheArgs c, con
     if (r >= (uint32_t)(c.T * c.Hkv)) return;
     const int t = (int)(r / (uint32_t)c.Hkv), h = (int)(r - (uint32_t)t * (uint32_t)c.Hkv);
     const int d = threadIdx.x % (D / 8) * 8;
-    const int64_t slot = slot_of(c, t);
+    const int64_t slot = slot_of<D / 8>(c, t);
     if (slot == kNone) return;
     float x[8], y[8];
     if (slot == kLost) {

@@ -205,8 +205,9 @@ typedef struct {
  * code (IEEE fp32 arithmetic; zero where v_scale is 0, undefined where a scale is NaN).
  *   slots  [T] int64 (device): page * (page's number) + (place in the page) of every token,
  *          which is not stored where that lies outside the pool; NULL: the slots follow from
- *          the batch. With slots the batch is not read and may be NULL. No two tokens may
- *          have the same slot. */
+ *          the batch. With slots the batch may be NULL, and nothing of it is read but its
+ *          offsets and max_new: where it has cu, tokens beyond max_new of their sequence are
+ *          not stored, as without slots. No two tokens may have the same slot. */
 sffn_status_t kv_cache4_append(const sffn_kv_cache4_t* cache, const sffn_kv_batch_t* batch, const int64_t* slots,
                                const sffn_heads_t* k, const sffn_heads_t* v, sffn_dtype_t dtype, int64_t T,
                                void* hip_stream);
