@@ -425,7 +425,7 @@ def kv_cache_append(cache, batch: CacheBatch, k: torch.Tensor, v: torch.Tensor) 
     shape = (T, cache.kv_heads, cache.head_dim)
     hk = _heads(k, "k", shape, dtype, dev)
     hv = _heads(v, "v", shape, dtype, dev)
-    if type(cache) is KVCache4:
+    if isinstance(cache, KVCache4):
         slots = None if batch.slots is None else _address(batch.slots, "slots", (T,), torch.int64, dev)
         _run(lib, dev, lib.kv_cache4_append, cache._c, batch._c, slots, hk, hv, _DTYPES[dtype], T)
         return
@@ -451,7 +451,7 @@ def kv_cache_read(cache, batch: CacheBatch, total: int, dtype: torch.dtype = tor
         v, hv = _new(shape, dtype, dev)
     else:
         hv = _heads(v, "v", shape, dtype, dev)
-    read = lib.kv_cache4_read if type(cache) is KVCache4 else lib.kv_cache_read
+    read = lib.kv_cache4_read if isinstance(cache, KVCache4) else lib.kv_cache_read
     _run(lib, dev, read, cache._c, batch._c, hk, hv, _DTYPES[dtype], total)
     return k, v
 
@@ -485,7 +485,7 @@ def cache_attention(cache, batch: CacheBatch, q: torch.Tensor, scale: Optional[f
     lse = _empty_strided((T, heads), (heads, 1), dtype=torch.float32, device=dev) if return_lse else None
     dt = _DTYPES[dtype]
     window = _int32(window)
-    four = type(cache) is KVCache4
+    four = isinstance(cache, KVCache4)
     if workspace is None:
         size = lib.cache4_attention_workspace_size if four else lib.cache_attention_workspace_size
         need = size(cache._c, batch._c, heads, dt, window, T)
