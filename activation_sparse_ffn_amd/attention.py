@@ -467,9 +467,9 @@ def cache_attention(cache, batch: CacheBatch, q: torch.Tensor, scale: Optional[f
     no key gives zeros and -inf; rows of tokens in no sequence are left as out
     holds them (undefined where it is not given). The softmax weights of a bf16 q are kept to 16
     bits, or to 8 in a sequence whose new tokens times heads / kv_heads are more
-    than 128; those of an fp32 q to fp32. (KVCache4: q and weights as sums of 6-bit pieces, q to
-    2^-17.9 and weights to 2^-13.9 of the largest of 32 channels or keys, weights to 2^-7.9 where the
-    8-bit cache's have 8 bits, both to 2^-21.9 for an fp32 q.)"""
+    than 128; those of an fp32 q to fp32. (KVCache4: q and weights as sums
+    of 6-bit pieces, to 2^-17.9 and 2^-13.9 of the largest of 32 channels or keys, weights to
+    2^-7.9 where the 8-bit cache's have 8 bits, both to 2^-21.9 for an fp32 q.)"""
     lib = load_library()
     _same_device(cache, batch)
     dev = cache.device

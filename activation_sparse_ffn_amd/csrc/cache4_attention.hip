@@ -10,7 +10,8 @@
 // mantissa bits: 0.125 .. 7.5) with a power of two for each 32 elements of either, which is
 // what the keys' exponents are.
 //
-// q (times scale log2 e) and the weights p sv are sums of such 6-bit pieces: the block's
+// q (times scale log2 e, or its power of two alone: see whole_q) and the weights p sv are
+// sums of such 6-bit pieces: the block's
 // largest magnitude goes to (3.75, 7.5] units, and each piece takes what the pieces before
 // left, at 1 / 16 of their unit. The first leaves a quarter of a unit at most (rounding
 // among steps of 1 / 2), the second 2^-7 (a quarter is 4 of its units, below which steps
@@ -146,6 +147,29 @@ struct QBlock {
     }
 };
 
+// What of scale log2 e is multiplied into q before it is cut, and what is left for the scores.
+// WHOLE: the power of two alone goes into q. The four pieces then hold a bf16 q's own entries,
+// exactly those down to 2^-10 of the largest of 32, where its products with the scale are off by
+// up to 2^-17.9 of it (the logarithm of a sum over one key by 4e-6 of itself, instead of 1e-7).
+struct Scaling {
+    float q, s;
+};
+// The rest costs a multiplication a score, which the few-row kernels have time for. The row
+// tiles of heads of 128 need the registers that the reference as the products' third operand
+// takes: 4096 tokens over 32768 keys 1830 us whole, 1836 cut after the product; shared tiles
+// (32 ragged sequences of up to 60 tokens), whose kernel then spills nothing, 142 and 163. Heads
+// of 64 (1592 and 1542) and 256 (over 8192 keys 1054 and 976) keep q whole in sequences of up to
+// kPreciseRows rows alone. An fp32 q has more bits than its pieces either way.
+template <typename E, int D, int PP>
+constexpr bool whole_q() { return sizeof(E) == 2 && (D == 128 || PP > 2); }
+template <bool WHOLE>
+__device__ __forceinline__ Scaling scaling(const AttnArgs& a) {
+    const uint32_t bits = __float_as_uint(a.scale2);
+    const bool split = WHOLE && bits >= 0x00800000u;    // has an exponent
+    const float q = split ? __uint_as_float(bits & 0x7f800000u) : a.scale2;
+    return {a.negate ? -q : q, split ? __uint_as_float((bits & 0x007fffffu) | 0x3f800000u) : 1.f};
+}
+
 // ---- products -------------------------------------------------------------------
 
 __device__ __forceinline__ i32x8 operand(const u32x6& v) {
@@ -276,6 +300,7 @@ __device__ __forceinline__ void attend4_few(const Attn4Args& args, const Work& w
     constexpr int NM = D == 64 ? (NP + 1) / 2 : NP; // products for q's pieces
     constexpr int DT = D / 16;
     constexpr int VL = D / 16;                      // loads of 16 bytes a lane of a step's values
+    constexpr bool WHOLE = whole_q<E, D, PP>();
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int g = lane >> 4, n = lane & 15;
 
@@ -371,12 +396,12 @@ __device__ __forceinline__ void attend4_few(const Attn4Args& args, const Work& w
 
     u32x6 qf[RT][KC][NM];
     int qu[RT][KC][2];
-    const float by = a.negate ? -a.scale2 : a.scale2;
+    const Scaling by = scaling<WHOLE>(a);
     each<RT>([&](auto r) {
         each<KC>([&](auto cc) {
             if constexpr (D == 64) {
                 u32x6 p[NP];
-                const int e = qx[r][cc].template split_into<NP>(by, p);
+                const int e = qx[r][cc].template split_into<NP>(by.q, p);
                 uint32_t u = 0;
                 each<NM>([&](auto i) {
                     constexpr int first = 2 * i, second = 2 * i + 1;
@@ -391,7 +416,7 @@ __device__ __forceinline__ void attend4_few(const Attn4Args& args, const Work& w
                 qu[r][cc][0] = (int)u;
                 qu[r][cc][1] = 0;
             } else {
-                const int e = qx[r][cc].template split_into<NP>(by, qf[r][cc]);
+                const int e = qx[r][cc].template split_into<NP>(by.q, qf[r][cc]);
                 units<NP>(e, qu[r][cc]);
             }
         });
@@ -424,7 +449,7 @@ __device__ __forceinline__ void attend4_few(const Attn4Args& args, const Work& w
                 const int ku = lds.k_exp[(16 * t + n) * (D / 32) + (D == 64 ? g & 1 : 4 * cc + g)];
                 each<RT>([&](auto r) {
                     if constexpr (cc == 0) {
-                        const float ref = -reference(m[r]);
+                        const float ref = WHOLE ? 0.f : -reference(m[r]);
                         s[r][t] = f32x4{ref, ref, ref, ref};
                     }
                     each<NM>([&](auto i) {
@@ -449,6 +474,11 @@ __device__ __forceinline__ void attend4_few(const Attn4Args& args, const Work& w
         int pu[RT][2];
         each<RT>([&](auto r) {
             auto x = [&](int i) { return s[r][i >> 2][i & 3]; };
+            if constexpr (WHOLE) {
+                const float ref = -reference(m[r]);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) s[r][i >> 2][i & 3] = __builtin_fmaf(x(i), by.s, ref);
+            }
             int up = last_seen(pos[r], t0, w.k1) - 4 * g, dn = before_seen(pos[r], t0, a.window) - 4 * g;
             auto hidden = [&](int i) {
                 const int key = 16 * (i >> 2) + (i & 3);
@@ -540,6 +570,7 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
     typedef RowsLds<D> Lds;
     constexpr int RB = D / 2, KC = D / 64, DT = D / 32, pitch = Lds::pitch;
     constexpr int CH = D == 256 ? 2 : 1;            // 16-byte pieces a thread stages of keys, and of values
+    constexpr bool WHOLE = whole_q<E, D, PP>();
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = lane & 31, half = lane >> 5;
     const int r = w.r0 + 32 * wave + col;
@@ -643,13 +674,13 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
     }
     u32x6 qf[KC][NP];
     int qu[KC][2];
+    const Scaling by = scaling<WHOLE>(a);
     {
         const E* q = static_cast<const E*>(a.q.p) + ((int64_t)(w.first + tok) * a.q.st + head * a.q.sh);
-        const float by = a.negate ? -a.scale2 : a.scale2;
         each<KC>([&](auto cc) {
             QBlock<E> x;
             x.load(q + 64 * cc + 32 * half, valid);
-            const int e = x.template split_into<NP>(by, qf[cc]);
+            const int e = x.template split_into<NP>(by.q, qf[cc]);
             units<NP>(e, qu[cc]);
         });
     }
@@ -663,7 +694,9 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
     float m = neg_inf(), l = 0.f;
-    f32x16 start;           // what scores begin from: minus the reference, as the products' third operand
+    // what scores begin from: minus the reference, as the products' third operand (WHOLE: zero,
+    // the reference comes with the rest of the scale)
+    f32x16 start;
 #pragma unroll
     for (int j = 0; j < 16; ++j) start[j] = 0.f;
     u32x6 pf[PP];           // the step's weights: pieces and their units
@@ -699,6 +732,11 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
     };
     auto weigh = [&](const Lds& from, int t0) {
         auto x = [&](int i) { return s[i >> 4][i & 15]; };
+        if constexpr (WHOLE) {
+            const float ref = -reference(m);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i >> 4][i & 15] = __builtin_fmaf(x(i), by.s, ref);
+        }
         const bool masked =
             t0 + kTile - 1 > p_first || t0 + kTile > w.k1 || (a.window > 0 && t0 <= p_last - a.window);
         int up = last_seen(pos, t0, w.k1) - 4 * half, dn = before_seen(pos, t0, a.window) - 4 * half;
@@ -719,9 +757,11 @@ __device__ __forceinline__ void attend4_rows(const Attn4Args& args, const Work& 
             for (int tt = 0; tt < 2; ++tt) s[tt] -= by;
 #pragma unroll
             for (int i = 0; i < DT; ++i) o[i] *= factor;
-            const float ref = -reference(m);
+            if constexpr (!WHOLE) {
+                const float ref = -reference(m);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) start[j] = ref;
+                for (int j = 0; j < 16; ++j) start[j] = ref;
+            }
         });
         asm("" : "+v"(up), "+v"(dn));       // hidden() again: 32 masks kept until then are as many scalars spilled
         float4 sv[8];

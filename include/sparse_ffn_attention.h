@@ -218,9 +218,10 @@ sffn_status_t kv_cache4_read(const sffn_kv_cache4_t* cache, const sffn_kv_batch_
 
 /* As cache_attention_workspace_size and cache_attention. The products take 4-bit entries as
  * they are; q and the weights of the values are sums of 6-bit pieces relative to the largest
- * of 32 channels (q) or keys (weights): q to 2^-17.9 of it, weights to 2^-7.9 in sequences of
- * more than 128 rows (to 2^-9 below a quarter of it) and to 2^-13.9 in those of fewer; both to
- * 2^-21.9 for an fp32 q. */
+ * of 32 channels (q) or keys (weights). A bf16 q: its entries, those below 2^-10 of the largest
+ * to 2^-17.9 of it; in sequences of more than 128 rows a key head, heads of 64 and 256: its
+ * products with the scale to 2^-17.9. Weights: to 2^-13.9, in sequences of more than 128 rows to
+ * 2^-7.9 (to 2^-9 below a quarter of the largest). An fp32 q and its weights: to 2^-21.9. */
 size_t cache4_attention_workspace_size(const sffn_kv_cache4_t* cache, const sffn_kv_batch_t* batch,
                                        int32_t n_q_heads, sffn_dtype_t dtype, int32_t window, int64_t T);
 sffn_status_t cache4_attention(const sffn_kv_cache4_t* cache, const sffn_kv_batch_t* batch, const sffn_heads_t* q,
