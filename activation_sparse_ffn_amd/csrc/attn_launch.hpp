@@ -200,9 +200,9 @@ hipError_t launch_cache4_read(const CacheArgs& c, const Cache4& b, const Heads& 
 // share_work): calls of 32 ragged sequences 40.3 us with 16, 40.4 with 32, 47.5 with 56, of
 // an fp32 q 44, 46 and 53.
 constexpr int kUnitCost4 = 16;
-// The same of its row tiles, at most the other: 32 ragged sequences of 60 tokens 170 us with 6,
-// 171 with 3, 198 with none; 16 of 20 tokens, heads of 256, 106, 128 and 130; 16 of 40, fp32,
-// 102, 99 and 121; 64 of 12 tokens over up to 2000 keys 63, 62 and 59.
+// The same of its row tiles, at most the other: 32 ragged sequences of 60 tokens 145 us with 6,
+// 143 with 3, 172 with none; 16 of 40, fp32, 101, 98 and 121; 64 of 12 tokens over up to 2000
+// keys 56, 55 and 51; 16 of 20 tokens, heads of 256, 106, 127 and 127, which decides for 6.
 constexpr int kTileCost4 = 6;
 // The few-row kernel for one tile of 16 rows or two, else the row tiles; what either side
 // takes stands at the kernels.
@@ -212,9 +212,9 @@ inline AttnPlan attn4_plan(const CacheArgs& c, int Hq, int window) {
     p.few = most <= 16;
     p.pair = !p.few && most <= 32 && c.D <= 128;
     p.waves = 4;
-    // one sequence's tiles are alike: without the walk's state their kernel spills nothing (32,
-    // 256 tokens over 32768 keys 47 and 150 us, shared 53 and 164; 600 over 9000 114 and 139;
-    // but 64 over 2000 with a max_kv of 32768 54 and 32)
+    // one sequence's tiles are alike, and their kernel does without the walk (32, 256 tokens
+    // over 32768 keys 46 and 149 us, shared 49 and 151; 600 over 9000 110 and 116, 200 of an
+    // fp32 q 94 and 99; but 64 over 2000 with a max_kv of 32768 54 and 29)
     return cut_up(c, Hq, window, p, p.few || p.pair ? 1 : few_held(c.D, c.dt == Dt::F32), 2);
 }
 hipError_t launch_cache4_attention(const CacheArgs& c, const Cache4& b, const AttnPlan& plan, const Heads& q, int Hq,

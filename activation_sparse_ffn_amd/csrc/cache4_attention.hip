@@ -23,9 +23,9 @@
 // 1 / 16 leaves. q's blocks are 32 channels of a row, the weights' the 32 keys of a row that
 // a lane holds. q of bf16 has four pieces, of fp32 five; weights two in sequences of more
 // than kPreciseRows rows, three in those of fewer, five for fp32. The sum l takes the
-// weights before they are cut. (4096 tokens over 32768 keys, 1.90 ms: with three pieces of
-// the weights 2.21, error 1.7e-3 instead of 2.1e-3; with three of q 1.76, but the logarithms
-// of the sums, fp32 numbers, are then off by more than 1e-6 of themselves.)
+// weights before they are cut. (4096 tokens over 32768 keys, 1.90 ms on one card: with three
+// pieces of the weights 2.21, error 1.7e-3 instead of 2.1e-3; with three of q 1.78, but they
+// hold a bf16 entry whole only down to 2^-6 of the largest of 32.)
 #include <type_traits>
 #include <utility>
 
@@ -276,8 +276,8 @@ __device__ __forceinline__ uint64_t page_row(const CacheArgs& c, uint32_t page, 
 // the keys', 32768 keys of 128 channels, 14.0 us; 32 sequences of 3620 keys 29 (126 MB: 4.3
 // TB/s), as much in 1 to 32768 keys each 35, with an fp32 q 39. By two workgroups a compute
 // unit, with half the registers, 19.2, 32, 38 and 63. Two tiles at once share what is loaded:
-// 6 tokens for each of the ragged sequences 58, by row tiles of 128 rows 88 (5 tokens over
-// 32768 keys 23.4 and 22.9).
+// 6 tokens for each of the ragged sequences 58, by row tiles of 128 rows 70 (calls of 64.5 and
+// 76 us; 5 tokens over 32768 keys 28.0 and 28.5).
 // ---------------------------------------------------------------------------
 constexpr int kStep = 128;
 
@@ -546,13 +546,14 @@ __global__ __launch_bounds__(256, 1) void k_attend4_few(const Attn4Args args) {
 // Bound by the vector unit and the products' share of its issue slots: exponentials, maxima
 // and conversions of 32 scores a lane keep it busy for two thirds of the time, and a scaled
 // product takes two to three times the issue cycles of a bf16 one. 4096 tokens of 32 heads
-// over 32768 keys 1855 us (heads of 128; 2.06 TFLOP: 1.11 PFLOP/s), heads of 64 1548; heads of
-// 256 over 8192 keys 980, an fp32 q of heads of 128 866. Tried beside it: the products of one
-// step's values with the next one's scores in one phase 2185; weights as bf16 and values
-// widened in LDS 2115 (heads of 64 1484); scores a step ahead by one wave a SIMD 4328, its
-// registers moved to and fro; raised priority around the products 1877; workgroups of eight
-// waves, half of them a phase behind, so that one half multiplies while the other weighs, 2677
-// with 128 bytes a lane spilled (heads of 64, without spills, 1529).
+// over 32768 keys 1845 us (heads of 128; 2.06 TFLOP: 1.12 PFLOP/s; 1838 to 1897 from card to
+// card), heads of 64 1538; heads of 256 over 8192 keys 973, an fp32 q of heads of 128 859. Tried
+// beside it, where it took 1855 (heads of 64 1548): the products of one step's values with the
+// next one's scores in one phase 2185; weights as bf16 and values widened in LDS 2115 (heads of
+// 64 1484); scores a step ahead by one wave a SIMD 4328, its registers moved to and fro; raised
+// priority around the products 1877; workgroups of eight waves, half of them a phase behind, so
+// that one half multiplies while the other weighs, 2677 with 128 bytes a lane spilled (heads of
+// 64, without spills, 1529).
 // ---------------------------------------------------------------------------
 template <int D>
 struct RowsLds {

@@ -11,7 +11,7 @@
 //
 // Memory-bound, and for few tokens bound by the chain of loads from offsets to table entry:
 // 4096 tokens of 8 heads of 128 in 7.8 us stored and 7.1 read (21 MB in all: 2.8 TB/s; an
-// empty launch and a copy of as much take 3.5 + 4.1), 32 single tokens 3.1 and 3.5. With the
+// empty launch and a copy of as much take 3.5 + 4.1), 32 single tokens 3.6 and 3.5. With the
 // slots given an append looks up no pages; the offsets alone where a sequence of the call can
 // have more than max_new tokens (32 single tokens 0.4 us of it, 32 times 128 of them 0.9).
 #include "attn_common.hpp"

@@ -37,7 +37,7 @@ typedef struct {
 /* The next step of every sequence b, which holds kv_lens[b] tokens: it keeps the first
  * min(kv_lens[b], keep_lens[b]) of them (keep_lens NULL: all; 0 ends a sequence, a few less
  * than kv_lens takes refused drafts back) and gets new_lens[b] more (numbers below zero count as
- * zero):
+ * zero; together fewer than 2^31):
  *   kv_lens_out[b]  tokens held then;  cu[0 .. n_seqs] offsets of the new ones
  *   free_pages, block_table  pages behind those kept go onto the stack, in the order of
  *       sequences and of their pages (entries that name no page are passed over); then the
