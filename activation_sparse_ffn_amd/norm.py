@@ -109,8 +109,8 @@ def add_rms_norm(x: torch.Tensor, residual: Optional[torch.Tensor] = None, weigh
     torch.int8 or torch.float8_e4m3fn and scale fp32 [T]; y scale[:, None] are the values,
     a row's largest one at 127 or 448. Without a residual h is x itself. weight [d] (None:
     ones). y_out and h_out take the results; h_out, and y_out without quant, may be x or
-    residual (a y_out that is x leaves no h without a residual). A row of zeros has scale 0, one with a NaN or an infinity in h or in h weight
-    scale NaN."""
+    residual (without a residual a y_out that is x leaves no h). A row of zeros has scale 0,
+    one with a NaN or an infinity in h or in h weight scale NaN."""
     lib = load_library()
     hx = _rows(x, "x")
     T, d = shape = x.shape

@@ -221,7 +221,9 @@ sffn_status_t kv_cache4_read(const sffn_kv_cache4_t* cache, const sffn_kv_batch_
  * of 32 channels (q) or keys (weights). A bf16 q: its entries, those below 2^-10 of the largest
  * to 2^-17.9 of it; in sequences of more than 128 rows a key head, heads of 64 and 256: its
  * products with the scale to 2^-17.9. Weights: to 2^-13.9, in sequences of more than 128 rows to
- * 2^-7.9 (to 2^-9 below a quarter of the largest). An fp32 q and its weights: to 2^-21.9. */
+ * 2^-7.9 (to 2^-9 below a quarter of the largest). An fp32 q and its weights: to 2^-21.9.
+ * Sums are fp32, of weights up to 2^8: finite where a sequence's keys times its largest value
+ * stay below 2^120. */
 size_t cache4_attention_workspace_size(const sffn_kv_cache4_t* cache, const sffn_kv_batch_t* batch,
                                        int32_t n_q_heads, sffn_dtype_t dtype, int32_t window, int64_t T);
 sffn_status_t cache4_attention(const sffn_kv_cache4_t* cache, const sffn_kv_batch_t* batch, const sffn_heads_t* q,

@@ -56,7 +56,7 @@ typedef struct {
  *   scale [T] fp32, 8 bits only
  *   h     the sum, [T, d] or NULL; not without a residual
  * h, and with SFFN_NORM_SAME y, may be x or residual themselves (same data and stride), but
- * not each other. No other two may overlap. T == 0 enqueues nothing. */
+ * not each other. No output may overlap anything else. T == 0 enqueues nothing. */
 sffn_status_t add_rms_norm(const sffn_norm_config_t* cfg, int64_t T, const sffn_rows_t* x,
                            const sffn_rows_t* residual, const void* weight, const sffn_rows_t* y, float* scale,
                            const sffn_rows_t* h, void* hip_stream);
