@@ -546,7 +546,7 @@ __global__ __launch_bounds__(256, 1) void k_attend4_few(const Attn4Args args) {
 // Bound by the vector unit and the products' share of its issue slots: exponentials, maxima
 // and conversions of 32 scores a lane keep it busy for two thirds of the time, and a scaled
 // product takes two to three times the issue cycles of a bf16 one. 4096 tokens of 32 heads
-// over 32768 keys 1845 us (heads of 128; 2.06 TFLOP: 1.12 PFLOP/s; 1838 to 1897 from card to
+// over 32768 keys 1845 us (heads of 128; 2.06 TFLOP: 1.12 PFLOP/s; 1838 to 1920 from card to
 // card), heads of 64 1538; heads of 256 over 8192 keys 973, an fp32 q of heads of 128 859. Tried
 // beside it, where it took 1855 (heads of 64 1548): the products of one step's values with the
 // next one's scores in one phase 2185; weights as bf16 and values widened in LDS 2115 (heads of
